@@ -31,7 +31,12 @@ EXPORTS = ("bsr_abi_version", "bsr_pattern_create_from_mask", "bsr_pattern_creat
            "bsr_linear_fwd_24_image", "bsr_values_quantize_fp8_24", "bsr_linear_fwd_fp8_24",
            # include/bsr_rebuild.h
            "bsr_meta_rebuild_workspace", "bsr_meta_rebuild", "bsr_linear_fwd_small_m_csr",
-           "bsr_pattern_create_device", "bsr_pattern_rebuild", "bsr_pattern_device_arrays")
+           "bsr_pattern_create_device", "bsr_pattern_rebuild", "bsr_pattern_device_arrays",
+           # include/bsr_experts.h
+           "bsr_router_fwd", "bsr_router_bwd", "bsr_expert_plan_workspace", "bsr_expert_plan", "bsr_expert_fwd",
+           "bsr_expert_bwd_input", "bsr_expert_bwd_weight", "bsr_expert_combine_fwd", "bsr_expert_combine_bwd",
+           # include/bsr_mx4.h
+           "bsr_mx4_quantize", "bsr_mx4_dequantize", "bsr_expert_fwd_mx4", "bsr_expert_fwd_mx4_mx4")
 
 
 class BsrError(RuntimeError):
@@ -87,6 +92,23 @@ def load() -> ctypes.CDLL:
     L.bsr_pattern_create_device.argtypes = [i32, i32, i32, i32, PP]
     L.bsr_pattern_rebuild.argtypes = [P, P, P]
     L.bsr_pattern_device_arrays.argtypes = [P, PP, PP, PP, PP, PP, PP]
+    L.bsr_router_fwd.argtypes = [P, i32, i64, i32, i32, i32, P, P, P]
+    L.bsr_router_bwd.argtypes = [P, i32, i64, i32, i32, i32, P, P, P, P, P]
+    L.bsr_expert_plan_workspace.argtypes, L.bsr_expert_plan_workspace.restype = [i64, i32, i32], sz
+    L.bsr_expert_plan.argtypes = [P, i64, i32, i32, P, P, P, P, sz, P]
+    L.bsr_expert_fwd.argtypes = [P, i64, i64, i32, i32, i32, P, P, P, P, P, P]
+    L.bsr_expert_bwd_input.argtypes = [P, i64, i32, i32, i32, P, P, P, P]
+    L.bsr_expert_bwd_weight.argtypes = [P, P, i64, i64, i32, i32, i32, P, P, P, P, P]
+    L.bsr_expert_combine_fwd.argtypes = [P, i64, i32, i32, P, P, P, P]
+    L.bsr_expert_combine_bwd.argtypes = [P, P, i64, i32, i32, i32, P, P, P, P, P, P]
+    L.bsr_mx4_quantize.argtypes = [P, i64, i32, P, P, P, P]
+    L.bsr_mx4_dequantize.argtypes = [P, P, i64, i32, P, P]
+    L.bsr_expert_fwd_mx4.argtypes = [P, i64, i64, i32, i32, i32, P, P, P, P, P, P, P]
+    L.bsr_expert_fwd_mx4_mx4.argtypes = [P, P, i64, i64, i32, i32, i32, P, P, P, P, P, P, P]
+    for f in ("bsr_router_fwd", "bsr_router_bwd", "bsr_expert_plan", "bsr_expert_fwd", "bsr_expert_bwd_input",
+              "bsr_expert_bwd_weight", "bsr_expert_combine_fwd", "bsr_expert_combine_bwd", "bsr_mx4_quantize",
+              "bsr_mx4_dequantize", "bsr_expert_fwd_mx4", "bsr_expert_fwd_mx4_mx4"):
+        getattr(L, f).restype = i32
     for f in ("bsr_pattern_create_from_mask", "bsr_pattern_create_from_csr", "bsr_pattern_info",
               "bsr_pattern_export", "bsr_linear_fwd", "bsr_linear_bwd_input", "bsr_linear_bwd_weight",
               "bsr_linear_bwd_weight_noalloc",
