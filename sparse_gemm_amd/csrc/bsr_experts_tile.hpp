@@ -1,0 +1,348 @@
+// bsr_experts_tile.hpp -- the pipelined tile product behind the bf16 products grouped by expert.
+//
+//   out[m][n] = sum over c < C of A(m, c) B(n, c)
+// A work-group of NW waves owns a BM x BN tile of out and walks the contraction in steps of 64. An
+// operand lies in memory either with c contiguous (kRows: one row per m or n) or with m or n
+// contiguous (kCols: one row per c); both are staged as they are by direct-to-LDS loads, 4 a wave and
+// step, and read as matrix-core fragments, kCols ones by transposing reads.
+//   kRows tile: [BM rows][8 chunks of 16 bytes], chunk q of row r at q ^ swz8(r)
+//   kCols tile: [64 rows][BM / 8 chunks], chunk q of row r at q ^ (4 (r & 3)): the 4 rows that a
+//               transposing read takes lie in the 4 quarters of the 64 banks
+// Of A three stages are held, of B two (160 KB at 256 x 256): during step s the A loads of step s + 2 are issued
+// between the products of its first two 16-deep chunks; then every wave waits for its LDS reads of
+// s and for its loads of s + 1, a barrier publishes those, and the B loads of s + 2 go between the
+// products of the last chunk, after the first fragments of s + 1 have been read. So a load has about one
+// step to land, and the products never wait for an LDS read right behind a barrier.
+#pragma once
+
+#include <algorithm>
+
+#include "bsr_device.hpp"
+
+namespace bsr {
+namespace dev {
+
+enum Operand { kRows, kCols };
+
+constexpr uint32_t kPast = 0xF0000000u;   // an offset at or past the end of every operand: such a load reads zeros
+
+// p[i] for a uniform i by a scalar load: a vector load would share the counter of the direct-to-LDS loads
+// and its wait would wait for those too.
+__device__ __forceinline__ int scalar_load(const int32_t *p, int i) {
+    return ((const __attribute__((address_space(4))) int32_t *)(uintptr_t)p)[i];
+}
+
+// One operand of a tile: `at` is its first row (kRows) or column (kCols).
+struct Side {
+    const uint16_t *p;
+    uint32_t bytes;          // size of the matrix behind p; loads past it read zeros
+    int ld;                  // elements a row
+    int at, rows;            // kRows: first row of the tile, rows that exist
+    const int32_t *gather;   // row of the matrix for row i of the operand (kRows: m or n, kCols: c), or NULL
+    int gcount, gmax;        // entries of gather, rows of the matrix
+};
+
+template <Operand O, int BM, int NW>
+struct Stager {
+    static constexpr int kBytes = BM * 128;
+    static constexpr int kRowChunks = BM / 8, kRowsPerLoad = 64 / kRowChunks;   // kCols: a row's chunks, rows of one 1 KB load
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t off[4];       // byte offset of this lane's 16 bytes of load j at step 0
+    uint32_t step;         // bytes between steps
+    int lim[4];            // steps in which load j's 16 bytes exist: from step lim[j] on it reads zeros
+    // gathered kCols: rows come from the plan, 64 of them a step
+    const int32_t *gather;
+    int gcount, gmax, C;
+    uint32_t ld2;
+    uint32_t rowoff[4];    // this lane's row offset of load j of the step being issued
+
+    __device__ __forceinline__ void init(const Side &s, int C_) {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        rsrc = make_rsrc(s.p, s.bytes);
+        gather = s.gather;
+        gcount = s.gcount;
+        gmax = s.gmax;
+        C = C_;
+        ld2 = (uint32_t)s.ld * 2u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = wave + NW * j;
+            if constexpr (O == kRows) {
+                const int lr = 8 * i + (lane >> 3), q = (lane & 7) ^ swz8(lr), row = s.at + lr;
+                uint32_t src = (uint32_t)row;
+                bool ok = row < s.rows;
+                if (s.gather) {
+                    const int t = ok ? s.gather[row] : -1;
+                    ok = (unsigned)t < (unsigned)s.gmax;
+                    src = (uint32_t)t;
+                }
+                off[j] = src * ld2 + (uint32_t)q * 16u;
+                lim[j] = ok ? (C_ - 8 * q + 63) / 64 : 0;
+            } else {
+                const int lr = kRowsPerLoad * i + lane / kRowChunks, q = (lane % kRowChunks) ^ ((lr & 3) << 2);
+                // a column past the matrix reads the next row's values, or zeros: they only reach
+                // outputs that do not exist. Rows past C read zeros by themselves.
+                off[j] = (s.gather ? 0u : (uint32_t)lr * ld2) + (uint32_t)(s.at + 8 * q) * 2u;
+                lim[j] = (C_ + 63) / 64;
+            }
+        }
+        step = O == kRows ? 128u : 64u * ld2;
+    }
+    // Row offsets of a gathered kCols operand for step s, from scalar loads (rows past C and tokens
+    // out of range read zeros).
+    __device__ __forceinline__ void fetch(int s) {
+        if constexpr (O == kCols) {
+            if (!gather) return;   // (uniform; steps past the last one give rows past C)
+            const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c0 = s * 64 + kRowsPerLoad * (wave + NW * j);
+                uint32_t o[kRowsPerLoad];
+#pragma unroll
+                for (int r = 0; r < kRowsPerLoad; ++r) {
+                    const int t = scalar_load(gather, min(c0 + r, gcount - 1));
+                    o[r] = c0 + r < C && (unsigned)t < (unsigned)gmax ? (uint32_t)t * ld2 : kPast;
+                }
+                uint32_t v = o[0];
+#pragma unroll
+                for (int r = 1; r < kRowsPerLoad; ++r) v = lane / kRowChunks == r ? o[r] : v;
+                rowoff[j] = v;
+            }
+        }
+    }
+    // Load j of step s into the stage at LDS byte address m0. Steps past the last one read zeros: the
+    // loops issue them too, so that their bodies have no branch that products could be moved across.
+    __device__ __forceinline__ void issue(uint32_t m0, int s, int j) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        uint32_t o;
+        if (O == kCols && gather) o = rowoff[j] + off[j];
+        else o = s < lim[j] ? off[j] + (uint32_t)s * step : kPast;
+        dma16(rsrc, m0 + (uint32_t)(wave + NW * j) * 1024u, o, 0);
+    }
+    // Fragment of rows / columns t0 .. t0 + 31 of a staged tile for 16-deep chunk kc.
+    static __device__ __forceinline__ bf16x8 frag(const unsigned char *tile, int t0, int kc) {
+        const int lane = threadIdx.x & 63;
+        if constexpr (O == kRows) {
+            const int r = t0 + (lane & 31);
+            return *reinterpret_cast<const bf16x8 *>(tile + r * 128 + (((2 * kc + (lane >> 5)) ^ swz8(r)) << 4));
+        } else {
+            const int gq = lane >> 4, s16 = lane & 15;
+            const int R = kc * 16 + (gq >> 1) * 8 + (s16 >> 2), col = t0 + (gq & 1) * 16 + 4 * (s16 & 3);
+            auto at = [&](int row) {
+                return (lds_i16x4 *)(tile + row * (BM * 2) + ((((col >> 3) ^ ((row & 3) << 2)) << 4) | ((col & 7) << 1)));
+            };
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(R));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(R + 4));
+            const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            return __builtin_bit_cast(bf16x8, v);
+        }
+    }
+};
+
+template <int BM, int BN>
+constexpr int tile_lds() {
+    const int stages = 3 * BM * 128 + 2 * BN * 128, out = BM * (BN * 2 + 16);
+    return stages > out ? stages : out;
+}
+
+// Stores a tile from the waves' accumulators: item v of lane l of acc[r][t] is column n0 + 32 t + 8 (v / 4) +
+// 4 (l / 32) + v % 4 of row m0 + 32 r + l % 32. Bias in fp32, one rounding to bf16, then whole rows from LDS
+// in 16-byte pieces. Row m of out at out + m * ldo; om rows and on (a multiple of 8) columns of it exist.
+template <int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[BM / WM / 32][BN / WN / 32], const uint16_t *bias,
+                                           uint16_t *out, int ldo, int om, int on, unsigned char *smem) {
+    constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32, kPitch = BN * 2 + 16;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN);
+    __syncthreads();   // the stages are free for the output tile
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int n = n0 + 32 * t + 8 * q + 4 * (lane >> 5);
+            f32x4 b4 = {0.f, 0.f, 0.f, 0.f};
+            if (bias && n < on) b4 = add_bias4(b4, bias + n);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const f32x4 v = quad(acc[r][t], q) + b4;
+                store4_bf16(reinterpret_cast<uint16_t *>(smem + (m0 + 32 * r + (lane & 31)) * kPitch + n * 2), v[0], v[1],
+                            v[2], v[3]);
+            }
+        }
+    __syncthreads();
+    constexpr int kPieces = BN / 8, kRowsOnce = NW * 64 / kPieces;
+    const int piece = threadIdx.x % kPieces;
+    if (piece * 8 < on) {
+        for (int m = threadIdx.x / kPieces; m < min(om, BM); m += kRowsOnce) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(smem + m * kPitch + piece * 16);
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(out + (int64_t)m * ldo + piece * 8));
+        }
+    }
+}
+
+// The tile's product and its store. WM x WN waves, each RT x 2 accumulators of 32 x 32.
+template <Operand OA, Operand OB, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int C, const uint16_t *bias, uint16_t *out,
+                                             int ldo, int om, int on, unsigned char *smem) {
+    constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32;
+    static_assert(CT == 2, "the schedule issues two loads after each of two column tiles");
+    constexpr int AB = BM * 128, BB = BN * 128;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN);
+    const uint32_t base = lds_addr(smem);
+
+    f32x16 acc[RT][CT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[r][t][v] = 0.f;
+
+    bf16x8 fa[2][RT], fb[2][CT];
+    auto read_frags = [&](int set, int xs, int vs, int kc) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) fa[set][r] = Stager<OA, BM, NW>::frag(smem + xs * AB, m0 + 32 * r, kc);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) fb[set][t] = Stager<OB, BN, NW>::frag(smem + 3 * AB + vs * BB, n0 + 32 * t, kc);
+    };
+    auto products = [&](int kc, auto &&after) __attribute__((always_inline)) {
+        const int cur = kc & 1;
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[r][t] = mfma32(fb[cur][t], fa[cur][r], acc[r][t]);
+            __builtin_amdgcn_sched_barrier(0);
+            after(t);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    const int steps = (C + 63) / 64;
+    if (steps > 0) {
+        Stager<OA, BM, NW> ga;
+        Stager<OB, BN, NW> gb;
+        ga.init(sa, C);
+        gb.init(sb, C);
+        auto issue_a = [&](int xs, int s, int j) __attribute__((always_inline)) {
+            ga.issue(base + (uint32_t)xs * AB, s, j);
+        };
+        auto issue_b = [&](int vs, int s, int j) __attribute__((always_inline)) {
+            gb.issue(base + 3 * AB + (uint32_t)vs * BB, s, j);
+        };
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            gb.fetch(s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) issue_a(s, s, j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) issue_b(s, s, j);
+        }
+        gb.fetch(2);
+        wait_vm<8, 8>(8);
+        __syncthreads();
+        read_frags(0, 0, 0, 0);
+        int xs = 0, vs = 0;
+        for (int s = 0; s < steps; ++s) {
+            const int x2 = xs == 0 ? 2 : xs - 1;   // A stage of s + 2 (that of s - 1)
+#pragma unroll
+            for (int kc = 0; kc < 3; ++kc) {
+                read_frags((kc + 1) & 1, xs, vs, kc + 1);
+                products(kc, [&](int t) __attribute__((always_inline)) {
+                    if (kc < 2) issue_a(x2, s + 2, 2 * kc + t);
+                });
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
+            wait_vm<4, 4>(4);                                     // all but the A loads of s + 2 have landed
+            __syncthreads();
+            const int xn = xs == 2 ? 0 : xs + 1, vn = vs ^ 1;
+            read_frags(0, xn, vn, 0);
+            products(3, [&](int t) __attribute__((always_inline)) {
+                issue_b(vs, s + 2, 2 * t);
+                issue_b(vs, s + 2, 2 * t + 1);
+            });
+            gb.fetch(s + 3);
+            xs = xn;
+            vs = vn;
+        }
+        wait_vm<0, 0>(0);   // the last loads (of zeros) leave the stages before the output tile takes their place
+    }
+    store_tile<BM, BN, WM, WN>(acc, bias, out, ldo, om, on, smem);
+}
+
+// ------------------------------------------------------------------------------------------
+// Rows of experts
+// ------------------------------------------------------------------------------------------
+struct Rows {
+    int e, at, n;   // expert (E: rows past the plan), first row, rows
+};
+
+__device__ __forceinline__ int clamp_row(int v, int R) { return min(max(v, 0), R); }
+
+// Tiles of up to BM rows, counted expert by expert; the rows past the plan come last.
+template <int BM>
+struct RowTiles {
+    const int32_t *offsets;
+    int E, R;
+
+    __device__ __forceinline__ int lane_rows(int base, int *lo) const {
+        const int e = base + (int)(threadIdx.x & 63);
+        if (e >= E) {
+            *lo = 0;
+            return 0;
+        }
+        *lo = clamp_row(offsets[e], R);
+        return max(clamp_row(offsets[e + 1], R) - *lo, 0);
+    }
+    static __device__ __forceinline__ int tiles_of(int n) { return (n + BM - 1) / BM; }
+    static __device__ __forceinline__ int prefix(int v) {   // inclusive, over the wave
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(v, d);
+            if (lane >= d) v += o;
+        }
+        return v;
+    }
+    __device__ __forceinline__ int total() const {
+        int sum = 0, lo;
+        for (int base = 0; base < E; base += 64)
+            sum += __builtin_amdgcn_readlane(prefix(tiles_of(lane_rows(base, &lo))), 63);
+        return sum + tiles_of(R - clamp_row(__builtin_amdgcn_readfirstlane(offsets[E]), R));
+    }
+    // The want-th tile; n <= 0 if there is none.
+    __device__ __forceinline__ Rows find(int want) const {
+        for (int base = 0; base < E; base += 64) {
+            int lo;
+            const int n = lane_rows(base, &lo), tiles = tiles_of(n), upto = prefix(tiles);
+            const uint64_t past = __ballot(upto > want);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                const int skip = (want - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l))) * BM;
+                return {base + l, __builtin_amdgcn_readlane(lo, l) + skip, min(BM, __builtin_amdgcn_readlane(n, l) - skip)};
+            }
+            want -= __builtin_amdgcn_readlane(upto, 63);
+        }
+        const int lo = clamp_row(__builtin_amdgcn_readfirstlane(offsets[E]), R) + want * BM;
+        return {E, lo, min(BM, R - lo)};
+    }
+};
+
+// Row tiles that share their activations and weights in an XCD's L2: `per` of them by all column tiles.
+struct TileOrder {
+    int row, col;
+};
+__device__ __forceinline__ TileOrder tile_order(int L, int rows, int cols, int per) {
+    const int chunk = L / (per * cols), r = L % (per * cols);
+    const int n = min(per, rows - per * chunk);
+    return {per * chunk + r % n, r / n};
+}
+
+constexpr int kRowsTogether = 4;
+
+}  // namespace dev
+
+// Row tiles that R rows in E groups and the rows past the plan can need.
+inline int64_t max_row_tiles(int64_t R, int64_t E, int64_t bm) { return (R + std::min(E + 1, R) * (bm - 1)) / bm; }
+
+}  // namespace bsr

@@ -1,0 +1,406 @@
+// bsr_mx4_gemm.hip -- products grouped by expert on microscaled 4-bit weights (include/bsr_mx4.h).
+//
+//   out[m][n] = sum over c of A(m, c) B(n, c), for each expert e:
+//     forward       m row, n output column, c input column:   A = x(row)[c], B = W[e][n][c]
+//     input grad    m row, n input column, c output column:   A = dY[row][c], B = W[e][c][n]
+//     weight grad   m output column, n input column, c row:   A = dY[c][m],   B = x(c)[n]
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "bsr_experts_internal.hpp"
+#include "bsr_experts_tile.hpp"
+#include "bsr_mx4_device.hpp"
+
+namespace bsr {
+namespace {
+
+using namespace dev;
+
+constexpr int kBM = 128, kBN = 128, kBK = 64;
+constexpr int kTileBytes = 128 * kBK * 2;
+
+enum Form { kBf16, kMx4 };
+
+struct Part {
+    const void *p;             // first element of this expert's / tile's matrix
+    uint32_t bytes;            // its size
+    const uint8_t *scales;     // kMx4
+    int ld;                    // elements (kMx4: rows of the scale array)
+    const int32_t *gather;     // token of each row (kBf16: output rows; kCols: contraction rows), or NULL
+    int gmax;                  // tokens
+    int rows;                  // rows (kBf16, kMx4) or columns (kCols) that exist
+    int at;                    // first of them in this tile
+};
+
+// Stages the 128 x 64 tile of contraction step c0 .. c0 + 63 (of C) at LDS byte address `to`.
+template <Form O>
+__device__ __forceinline__ void stage(const Part &s, int c0, int C, unsigned char *to) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (O == kMx4) {
+        const int r = s.at + (threadIdx.x >> 1), g = (c0 >> 5) + (threadIdx.x & 1);
+        float v[32];
+        int64_t row = r < s.rows && g * 32 < C ? r : -1;
+        if (row >= 0 && s.gather) {
+            row = s.gather[r];
+            if (row >= s.gmax) row = -1;
+        }
+        if (row >= 0) {
+            const u32x4 codes = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(s.p) + row * (C / 2) + g * 16);
+            mx4_expand(codes, s.scales[((int64_t)(g >> 3) * s.ld + row) * 8 + (g & 7)], v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        const int lr = threadIdx.x >> 1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            u32x4 o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = (uint32_t)to_bf16(v[8 * q + 2 * i]) | ((uint32_t)to_bf16(v[8 * q + 2 * i + 1]) << 16);
+            *reinterpret_cast<u32x4 *>(to + lr * 128 + (((4 * (threadIdx.x & 1) + q) ^ swz8(lr)) << 4)) = o;
+        }
+        return;
+    }
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(s.p, s.bytes);
+    const uint32_t m0 = lds_addr(to);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = wave + 4 * j;
+        uint32_t off;
+        if constexpr (O == kBf16) {
+            const int lr = 8 * i + (lane >> 3), row = s.at + lr, c = c0 + 8 * ((lane & 7) ^ swz8(lr));
+            int src = row;
+            bool ok = row < s.rows && c < C;
+            if (s.gather) {
+                src = row < s.rows ? s.gather[row] : -1;
+                ok = ok && (unsigned)src < (unsigned)s.gmax;
+            }
+            off = ok ? (uint32_t)src * (uint32_t)s.ld * 2u + (uint32_t)c * 2u : kPast;
+        }
+        dma16(r, m0 + (uint32_t)i * 1024u, off, 0);
+    }
+}
+
+// Fragment of rows / columns t0 .. t0 + 31 of a staged tile for contraction chunk kc (16 deep).
+template <Form O>
+__device__ __forceinline__ bf16x8 frag(const unsigned char *tile, int t0, int kc) {
+    const int lane = threadIdx.x & 63;
+    const int r = t0 + (lane & 31);
+    return *reinterpret_cast<const bf16x8 *>(tile + r * 128 + (((2 * kc + (lane >> 5)) ^ swz8(r)) << 4));
+}
+
+// One 128 x 128 tile of out (leading dimension ldo, `om` rows and `on` columns of it exist).
+template <Form OA, Form OB>
+__device__ __forceinline__ void simple_product(const Part &a, const Part &b, int C, const uint16_t *bias, uint16_t *out,
+                                             int ldo, int om, int on, unsigned char *smem) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+    f32x16 acc[2][2];   // [n tile][m tile]
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    const int steps = (C + kBK - 1) / kBK;
+    auto load = [&](int s) __attribute__((always_inline)) {
+        unsigned char *to = smem + (s & 1) * 2 * kTileBytes;
+        stage<OA>(a, s * kBK, C, to);
+        stage<OB>(b, s * kBK, C, to + kTileBytes);
+    };
+    if (steps > 0) load(0);
+    for (int s = 0; s < steps; ++s) {
+        wait_vm<0, 0>(0);
+        __syncthreads();
+        if (s + 1 < steps) load(s + 1);
+        const unsigned char *ta = smem + (s & 1) * 2 * kTileBytes, *tb = ta + kTileBytes;
+#pragma unroll
+        for (int kc = 0; kc < 4; ++kc) {
+            bf16x8 fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fa[i] = frag<OA>(ta, wm + 32 * i, kc);
+                fb[i] = frag<OB>(tb, wn + 32 * i, kc);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(fb[i], fa[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int m = wm + 32 * j + (lane & 31);
+        if (m >= om) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = wn + 32 * i + 8 * q + 4 * (lane >> 5);
+                if (n >= on) continue;
+                f32x4 v = quad(acc[i][j], q);
+                if (bias) v = add_bias4(v, bias + n);
+                store4_bf16(out + (int64_t)m * ldo + n, v[0], v[1], v[2], v[3]);
+            }
+    }
+}
+
+struct GemmArgs {
+    const void *act, *w;
+    const uint8_t *act_scales, *w_scales;
+    const uint16_t *bias;
+    uint16_t *out;
+    const int32_t *offsets, *gather;
+    int T, R, E, Nout, C;   // output columns, contraction length
+};
+
+// Forward and input gradient: one 128-row x 128-column tile a work-group.
+template <Form OA, Form OB>
+__global__ __launch_bounds__(256) void k_expert_simple(GemmArgs g, int ntiles) {
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * kTileBytes];
+    const int nt = blockIdx.x % ntiles;
+    const Rows t = RowTiles<kBM>{g.offsets, g.E, g.R}.find(blockIdx.x / ntiles);
+    if (t.n <= 0) return;
+    const bool live = t.e < g.E;
+    const int C = live ? g.C : 0;
+    const int e = live ? t.e : 0;
+    const int64_t wsize = (int64_t)g.Nout * g.C;
+    Part a{}, b{};
+    if constexpr (OA == kMx4) {
+        a = {g.act, 0, g.act_scales, g.gather ? g.T : g.R, g.gather, g.T, t.at + t.n, t.at};
+    } else if (g.gather) {
+        a = {g.act, (uint32_t)((int64_t)g.T * g.C * 2), nullptr, g.C, g.gather, g.T, t.at + t.n, t.at};
+    } else {   // the tile's own rows
+        a = {static_cast<const uint16_t *>(g.act) + (int64_t)t.at * g.C, (uint32_t)((int64_t)t.n * g.C * 2), nullptr, g.C,
+             nullptr, 0, t.n, 0};
+    }
+    if constexpr (OB == kMx4) {
+        const int64_t kb = (g.C + 255) / 256;
+        b = {static_cast<const uint8_t *>(g.w) + e * wsize / 2, 0, g.w_scales + e * kb * g.Nout * 8, g.Nout, nullptr, 0,
+             g.Nout, nt * kBN};
+    } else {
+        b = {static_cast<const uint16_t *>(g.w) + e * wsize, (uint32_t)(wsize * 2), nullptr, g.C,
+             nullptr, 0, g.Nout, nt * kBN};
+    }
+    simple_product<OA, OB>(a, b, C, live && g.bias ? g.bias + (int64_t)e * g.Nout + nt * kBN : nullptr,
+                         g.out + (int64_t)t.at * g.Nout + nt * kBN, g.Nout, t.n, g.Nout - nt * kBN, smem);
+}
+
+// ------------------------------------------------------------------------------------------
+// Both sides in 4 bits, on the scaled matrix cores (v_mfma_scale_f32_32x32x64_f8f6f4: 32 x 32 x 64 products
+// of codes, one scale byte per 32 of them on each side, fp32 sums).
+//
+// Steps of 256 columns: a row's 128 bytes of codes are staged exactly like 64 bf16 columns (8 chunks of 16
+// bytes, one group each), its 8 scale bytes beside them. Half-wave h of a fragment takes the groups 4 h + j,
+// j = 0 .. 3 being the step's four products, so that its four scale bytes are one 32-bit word whose byte j the j-th
+// product selects. Two stages a side: the loads of step s + 2 are issued behind the barrier that ends the
+// reads of step s, among the products of its last chunk.
+// ------------------------------------------------------------------------------------------
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ i32x8 codes8(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+template <int J>
+__device__ __forceinline__ f32x16 mfma_mx4(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(codes8(a), codes8(b), c, 4, 4, J, sa, J, sb);
+}
+
+// Direct-to-LDS load of 4 bytes a lane (see dma16).
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t m0, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(r)
+                 : "memory", "m0");
+}
+
+template <int BM, int BN>
+constexpr int mx4_lds() {
+    const int stages = 2 * (BM + BN) * 136, out = BM * (BN * 2 + 16);
+    return stages > out ? stages : out;
+}
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM *WN * 64, 1) void k_mx4_mx4(GemmArgs g, int ntiles) {
+    constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32;
+    static_assert(BM == NW * 32 && BN == NW * 32 && CT == 2, "one load of scales a wave and side");
+    constexpr int AB = BM * 128, BB = BN * 128, AS = 2 * (AB + BB), BS = AS + 2 * BM * 8;   // LDS: A, B, scales of A, of B
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[mx4_lds<BM, BN>()];
+    const RowTiles<BM> tiles{g.offsets, g.E, g.R};
+    const int total = tiles.total();
+    if ((int64_t)blockIdx.x >= (int64_t)total * ntiles) return;
+    const TileOrder o = tile_order(xcd_remap(blockIdx.x, total * ntiles), total, ntiles, kRowsTogether);
+    const Rows t = tiles.find(o.row);
+    if (t.n <= 0) return;
+    const bool live = t.e < g.E;
+    const int e = live ? t.e : 0, kb = (g.C + 255) / 256, steps = live ? kb : 0;
+    const int64_t wbytes = (int64_t)g.Nout * (g.C / 2), abytes = (int64_t)(g.gather ? g.T : g.R) * (g.C / 2);
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN), lh = lane >> 5;
+    const uint32_t base = lds_addr(smem);
+
+    f32x16 acc[RT][CT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[r][c][v] = 0.f;
+
+    if (steps > 0) {
+        // codes: 16-bit units, 128 bytes a row and step
+        Stager<kRows, BM, NW> ga;
+        Stager<kRows, BN, NW> gb;
+        ga.init({static_cast<const uint16_t *>(g.act), (uint32_t)abytes, g.C / 4, t.at, t.at + t.n, g.gather, g.R, g.T}, g.C / 4);
+        gb.init({static_cast<const uint16_t *>(g.w) + e * (wbytes / 2), (uint32_t)wbytes, g.C / 4, o.col * BN, g.Nout, nullptr, 0,
+                 0}, g.C / 4);
+        // scale words: lane 2 r + h of wave w loads word h of row 32 w + r
+        const int arows = g.gather ? g.T : g.R, half = lane & 1;
+        const __amdgpu_buffer_rsrc_t rsa = make_rsrc(g.act_scales, (uint32_t)((int64_t)kb * arows * 8));
+        const __amdgpu_buffer_rsrc_t rsb = make_rsrc(g.w_scales + (int64_t)e * kb * g.Nout * 8, (uint32_t)((int64_t)kb * g.Nout * 8));
+        const int ar = wave * 32 + (lane >> 1), br = o.col * BN + ar;
+        const int arow = ar >= t.n ? -1 : g.gather ? g.gather[t.at + ar] : t.at + ar;
+        const int sa_lim = (unsigned)arow < (unsigned)arows ? steps : 0, sb_lim = br < g.Nout ? steps : 0;
+        const uint32_t sa_off = (uint32_t)arow * 8u + 4u * half, sb_off = (uint32_t)br * 8u + 4u * half;
+        const uint32_t sa_step = (uint32_t)arows * 8u, sb_step = (uint32_t)g.Nout * 8u;
+        auto issue_scales = [&](int st, int s) __attribute__((always_inline)) {
+            dma4(rsa, base + AS + (uint32_t)st * (BM * 8) + (uint32_t)wave * 256u, s < sa_lim ? sa_off + (uint32_t)s * sa_step : kPast);
+            dma4(rsb, base + BS + (uint32_t)st * (BN * 8) + (uint32_t)wave * 256u, s < sb_lim ? sb_off + (uint32_t)s * sb_step : kPast);
+        };
+        auto issue_a = [&](int st, int s, int j) __attribute__((always_inline)) {
+            ga.issue(base + (uint32_t)st * AB, s, j);
+        };
+        auto issue_b = [&](int st, int s, int j) __attribute__((always_inline)) {
+            gb.issue(base + 2 * AB + (uint32_t)st * BB, s, j);
+        };
+        // words of the last step whose groups do not exist are dropped byte by byte
+        const int left = g.C / 32 - (kb - 1) * 8 - 4 * lh;   // groups of this half in the last step
+        const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+
+        i32x4 fa[2][RT], fb[2][CT];
+        int wa[RT], wb[CT], na[RT], nb[CT];
+        auto frag = [&](const unsigned char *tile, int row, int j) __attribute__((always_inline)) {
+            const int r = row + (lane & 31);
+            return *reinterpret_cast<const i32x4 *>(tile + r * 128 + (((4 * lh + j) ^ swz8(r)) << 4));
+        };
+        auto read_frags = [&](int set, int st, int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) fa[set][r] = frag(smem + st * AB, m0 + 32 * r, j);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) fb[set][c] = frag(smem + 2 * AB + st * BB, n0 + 32 * c, j);
+        };
+        auto read_scales = [&](int st, int s) __attribute__((always_inline)) {
+            const uint32_t mask = s == steps - 1 ? keep : 0xFFFFFFFFu;
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                na[r] = (int)(*reinterpret_cast<const uint32_t *>(smem + AS + st * (BM * 8) + (m0 + 32 * r + (lane & 31)) * 8 + 4 * lh) & mask);
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                nb[c] = (int)(*reinterpret_cast<const uint32_t *>(smem + BS + st * (BN * 8) + (n0 + 32 * c + (lane & 31)) * 8 + 4 * lh) & mask);
+        };
+        auto take_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) wa[r] = na[r];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) wb[c] = nb[c];
+        };
+        auto products = [&](auto jc, auto &&after) __attribute__((always_inline)) {
+            constexpr int J = decltype(jc)::value, set = J & 1;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r) acc[r][c] = mfma_mx4<J>(fb[set][c], fa[set][r], acc[r][c], wb[c], wa[r]);
+                __builtin_amdgcn_sched_barrier(0);
+                after(c);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        auto nothing = [](int) {};
+        auto load = [&](int st, int s) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) issue_a(st, s, j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) issue_b(st, s, j);
+            issue_scales(st, s);
+        };
+        load(0, 0);
+        load(1, 1);
+        wait_vm<10, 10>(10);
+        __syncthreads();
+        read_frags(0, 0, 0);
+        read_scales(0, 0);
+        take_scales();
+        for (int s = 0; s < steps; ++s) {
+            const int st = s & 1;
+            read_frags(1, st, 1);
+            products(std::integral_constant<int, 0>{}, nothing);
+            read_frags(0, st, 2);
+            products(std::integral_constant<int, 1>{}, nothing);
+            read_frags(1, st, 3);
+            products(std::integral_constant<int, 2>{}, nothing);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
+            wait_vm<0, 0>(0);                                     // step s + 1 has landed
+            __syncthreads();
+            read_frags(0, st ^ 1, 0);
+            read_scales(st ^ 1, s + 1);
+            products(std::integral_constant<int, 3>{}, [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (c == 0) issue_a(st, s + 2, j);
+                    else issue_b(st, s + 2, j);
+                }
+                if (c == 1) issue_scales(st, s + 2);
+            });
+            take_scales();
+        }
+        wait_vm<0, 0>(0);
+    }
+    store_tile<BM, BN, WM, WN>(acc, live && g.bias ? g.bias + (int64_t)e * g.Nout + o.col * BN : nullptr,
+                               g.out + (int64_t)t.at * g.Nout + o.col * BN, g.Nout, t.n, g.Nout - o.col * BN, smem);
+}
+
+int32_t launched(const char *what) {
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return fail(BSR_ERR_HIP, std::string(what) + ": " + hipGetErrorString(err));
+    return BSR_OK;
+}
+
+// 256 x 256 tiles with 8 waves where the groups fill them, else 128 x 128 with 4.
+bool wide(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 + 1) * ((cols + 255) / 256) >= 192; }
+
+template <Form OA, Form OB>
+int32_t launch_rows(const GemmArgs &g, void *stream, const char *what) {
+    const int64_t ntiles = (g.Nout + kBN - 1) / kBN, blocks = max_row_tiles(g.R, g.E, kBM) * ntiles;
+    if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, std::string(what) + ": too many tiles");
+    hipLaunchKernelGGL((k_expert_simple<OA, OB>), dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), g,
+                       (int)ntiles);
+    return launched(what);
+}
+
+}  // namespace
+
+int32_t launch_expert_fwd_mx4(const ExpertShape &s, const uint16_t *X, const uint8_t *codes, const uint8_t *scales,
+                              const uint16_t *bias, uint16_t *Y, void *stream) {
+    const GemmArgs g{X, codes, nullptr, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
+    return launch_rows<kBf16, kMx4>(g, stream, "bsr_expert_fwd_mx4");
+}
+
+int32_t launch_expert_fwd_mx4_mx4(const ExpertShape &s, const uint8_t *xcodes, const uint8_t *xscales,
+                                  const uint8_t *codes, const uint8_t *scales, const uint16_t *bias, uint16_t *Y,
+                                  void *stream) {
+    const GemmArgs g{xcodes, codes, xscales, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool w = wide(s.R, s.E, s.N);
+    const int64_t bm = w ? 256 : 128, ntiles = (s.N + bm - 1) / bm, blocks = max_row_tiles(s.R, s.E, bm) * ntiles;
+    if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, "bsr_expert_fwd_mx4_mx4: too many tiles");
+    if (w)
+        hipLaunchKernelGGL((k_mx4_mx4<256, 256, 2, 4>), dim3((unsigned)blocks), dim3(512), 0, st, g, (int)ntiles);
+    else
+        hipLaunchKernelGGL((k_mx4_mx4<128, 128, 2, 2>), dim3((unsigned)blocks), dim3(256), 0, st, g, (int)ntiles);
+    return launched("bsr_expert_fwd_mx4_mx4");
+}
+
+}  // namespace bsr

@@ -138,6 +138,10 @@ PRODUCTS = [("ragged", 1, 1, 1, 8, 8), ("ragged", 1, 2, 4, 136, 72), ("ragged", 
             ("dropped", 2050, 2, 3, 512, 512)]
 
 
+# enough rows and columns for 256 x 256 tiles: (T, k, E, N, K) of the forward; the input gradient swaps N and K
+WIDE = [("one", 530, 1, 1, 16392, 72), ("ragged", 400, 2, 2, 12296, 200), ("dropped", 700, 2, 3, 16400, 264)]
+
+
 def product_inputs(kind, T, k, E, N, K, gather, seed=0):
     index, p, (off, tok, row) = a_plan(kind, T, k, E, seed + T)
     g = gen(seed + 7)
@@ -157,7 +161,7 @@ def product_inputs(kind, T, k, E, N, K, gather, seed=0):
     return p, off, live, X, W, dY, x
 
 
-@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS)
+@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + WIDE)
 @pytest.mark.parametrize("gather", [False, True])
 def test_expert_fwd(kind, T, k, E, N, K, gather):
     say(f"case expert_fwd {kind} T={T} k={k} E={E} N={N} K={K} gather={gather}")
@@ -171,7 +175,7 @@ def test_expert_fwd(kind, T, k, E, N, K, gather):
         assert (f64(y)[live:] == 0).all()
 
 
-@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS)
+@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + [(kind, T, k, E, K, N) for kind, T, k, E, N, K in WIDE])
 def test_expert_bwd_input(kind, T, k, E, N, K):
     say(f"case expert_bwd_input {kind} T={T} k={k} E={E} N={N} K={K}")
     p, off, live, _, W, dY, _ = product_inputs(kind, T, k, E, N, K, False)
@@ -183,7 +187,8 @@ def test_expert_bwd_input(kind, T, k, E, N, K):
     near_bf16(dX, Y, S, N)
 
 
-@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS)
+@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + [("ragged", 130, 2, 3, 2056, 2056), ("dropped", 300, 1, 25, 776, 520),
+                                                         ("ragged", 500, 2, 7, 1032, 1544)])
 @pytest.mark.parametrize("gather", [False, True])
 def test_expert_bwd_weight(kind, T, k, E, N, K, gather):
     say(f"case expert_bwd_weight {kind} T={T} k={k} E={E} N={N} K={K} gather={gather}")
