@@ -29,8 +29,8 @@ struct GemmArgs {
 template <Operand OB, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_rows(GemmArgs g, int ntiles) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[tile_lds<BM, BN>()];
-    const RowTiles<BM> tiles{g.offsets, g.E, g.R};
-    const int total = tiles.total();
+    const RowTiles<BM> tiles(g.offsets, g.E, g.R);
+    const int total = tiles.total;
     if ((int64_t)blockIdx.x >= (int64_t)total * ntiles) return;
     const TileOrder o = tile_order(xcd_remap(blockIdx.x, total * ntiles), total, ntiles, kRowsTogether);
     const Rows t = tiles.find(o.row);
@@ -120,6 +120,7 @@ int32_t launch_rows(const GemmArgs &g, void *stream, const char *what) {
 
 int32_t launch_expert_fwd(const ExpertShape &s, const uint16_t *X, const uint16_t *W, const uint16_t *bias, uint16_t *Y,
                           void *stream) {
+    if (few_rows(s.R, s.E)) return launch_expert_fwd_few(s, X, W, bias, Y, stream);
     return launch_rows<kRows>({X, W, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K}, stream, "bsr_expert_fwd");
 }
 

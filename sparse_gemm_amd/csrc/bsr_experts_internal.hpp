@@ -35,6 +35,12 @@ struct ExpertShape {
 
 int32_t launch_expert_fwd(const ExpertShape &s, const uint16_t *X, const uint16_t *W, const uint16_t *bias, uint16_t *Y,
                           void *stream);
+// Few rows an expert: 16-row tiles that stream the weights.
+inline bool few_rows(int64_t R, int64_t E) { return R <= 24 * E; }
+int32_t launch_expert_fwd_few(const ExpertShape &s, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
+                              uint16_t *Y, void *stream);
+int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, const uint16_t *X, const uint8_t *codes, const uint8_t *scales,
+                                  const uint16_t *bias, uint16_t *Y, void *stream);
 int32_t launch_expert_bwd_input(const ExpertShape &s, const uint16_t *dY, const uint16_t *W, uint16_t *dX, void *stream);
 int32_t launch_expert_bwd_weight(const ExpertShape &s, const uint16_t *dY, const uint16_t *X, uint16_t *dW,
                                  uint16_t *dbias, void *stream);

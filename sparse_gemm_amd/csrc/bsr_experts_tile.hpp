@@ -26,6 +26,12 @@ enum Operand { kRows, kCols };
 
 constexpr uint32_t kPast = 0xF0000000u;   // an offset at or past the end of every operand: such a load reads zeros
 
+// Direct-to-LDS load of 4 bytes a lane (see dma16).
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t m0, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(r)
+                 : "memory", "m0");
+}
+
 // p[i] for a uniform i by a scalar load: a vector load would share the counter of the direct-to-LDS loads
 // and its wait would wait for those too.
 __device__ __forceinline__ int scalar_load(const int32_t *p, int i) {
@@ -279,52 +285,57 @@ struct Rows {
 
 __device__ __forceinline__ int clamp_row(int v, int R) { return min(max(v, 0), R); }
 
-// Tiles of up to BM rows, counted expert by expert; the rows past the plan come last.
+// Tiles of up to BM rows, counted expert by expert; the rows past the plan come last. Lane l keeps expert l of
+// the first 64: up to 64 experts offsets is read once.
 template <int BM>
 struct RowTiles {
     const int32_t *offsets;
     int E, R;
+    int live, lo, n, upto;   // rows of all experts; this lane's expert: first row, rows, tiles up to and with it
+    int total;               // tiles of the experts and of the rows past the plan
 
-    __device__ __forceinline__ int lane_rows(int base, int *lo) const {
-        const int e = base + (int)(threadIdx.x & 63);
-        if (e >= E) {
-            *lo = 0;
-            return 0;
+    __device__ __forceinline__ RowTiles(const int32_t *offsets_, int E_, int R_) : offsets(offsets_), E(E_), R(R_) {
+        live = clamp_row(scalar_load(offsets, E), R);
+        load(0);
+        total = __builtin_amdgcn_readlane(upto, 63);
+        for (int base = 64; base < E; base += 64) {
+            RowTiles more = *this;
+            more.load(base);
+            total += __builtin_amdgcn_readlane(more.upto, 63);
         }
-        *lo = clamp_row(offsets[e], R);
-        return max(clamp_row(offsets[e + 1], R) - *lo, 0);
+        total += tiles_of(R - live);
     }
-    static __device__ __forceinline__ int tiles_of(int n) { return (n + BM - 1) / BM; }
-    static __device__ __forceinline__ int prefix(int v) {   // inclusive, over the wave
-        const int lane = threadIdx.x & 63;
+    static __device__ __forceinline__ int tiles_of(int rows) { return (rows + BM - 1) / BM; }
+    __device__ __forceinline__ void load(int base) {
+        const int lane = threadIdx.x & 63, e = base + lane;
+        lo = n = 0;
+        if (e < E) {
+            lo = clamp_row(offsets[e], R);
+            n = max(clamp_row(offsets[e + 1], R) - lo, 0);
+        }
+        upto = tiles_of(n);
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(v, d);
-            if (lane >= d) v += o;
+            const int o = __shfl_up(upto, d);
+            if (lane >= d) upto += o;
         }
-        return v;
-    }
-    __device__ __forceinline__ int total() const {
-        int sum = 0, lo;
-        for (int base = 0; base < E; base += 64)
-            sum += __builtin_amdgcn_readlane(prefix(tiles_of(lane_rows(base, &lo))), 63);
-        return sum + tiles_of(R - clamp_row(__builtin_amdgcn_readfirstlane(offsets[E]), R));
     }
     // The want-th tile; n <= 0 if there is none.
     __device__ __forceinline__ Rows find(int want) const {
-        for (int base = 0; base < E; base += 64) {
-            int lo;
-            const int n = lane_rows(base, &lo), tiles = tiles_of(n), upto = prefix(tiles);
-            const uint64_t past = __ballot(upto > want);
+        RowTiles c = *this;
+        for (int base = 0;;) {
+            const uint64_t past = __ballot(c.upto > want);
             if (past) {
-                const int l = __builtin_ctzll(past);
-                const int skip = (want - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l))) * BM;
-                return {base + l, __builtin_amdgcn_readlane(lo, l) + skip, min(BM, __builtin_amdgcn_readlane(n, l) - skip)};
+                const int l = __builtin_ctzll(past), rows = __builtin_amdgcn_readlane(c.n, l);
+                const int skip = (want - (__builtin_amdgcn_readlane(c.upto, l) - tiles_of(rows))) * BM;
+                return {base + l, __builtin_amdgcn_readlane(c.lo, l) + skip, min(BM, rows - skip)};
             }
-            want -= __builtin_amdgcn_readlane(upto, 63);
+            want -= __builtin_amdgcn_readlane(c.upto, 63);
+            base += 64;
+            if (base >= E) break;
+            c.load(base);
         }
-        const int lo = clamp_row(__builtin_amdgcn_readfirstlane(offsets[E]), R) + want * BM;
-        return {E, lo, min(BM, R - lo)};
+        return {E, live + want * BM, min(BM, R - live - want * BM)};
     }
 };
 

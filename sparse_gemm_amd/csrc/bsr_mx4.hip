@@ -32,30 +32,13 @@ __global__ __launch_bounds__(256) void k_quantize(const uint16_t *__restrict__ X
     const int field = (int)(top >> 7);   // exponent field
     const bool bad = field == 255;
     const int byte = bad ? 255 : max(field - 2, 0);
-    const float inv = __uint_as_float((uint32_t)(254 - min(byte, 253)) << 23);   // 2^(127 - byte)
-    const float scale = mx4_scale((uint32_t)byte);
-    uint32_t packed = 0;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t h = (x[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-        const float a = __uint_as_float((h & 0x7FFFu) << 16) * inv;
-        // nearest magnitude, ties to the even code
-        uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
-        c |= (h >> 15) << 3;
-        if (bad) c = 0;
-        packed |= c << (4 * j);
-        const float m = mx4_magnitude(c & 7u) * scale;
-        v[j] = (c & 8u) ? -m : m;
-    }
+    const float scale = mx4_scale_bits((uint32_t)byte);
+    const uint32_t packed = bad ? 0u : mx4_quantize8(x, scale);
     if ((part & 3) == 0) scales[((int64_t)cb * rows + row) * 8 + (part >> 2)] = (uint8_t)byte;
     if (col < K) {
         *reinterpret_cast<uint32_t *>(codes + (row * K + col) / 2) = packed;
         if (values) {
-            u32x4 o;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = (uint32_t)to_bf16(v[2 * j]) | ((uint32_t)to_bf16(v[2 * j + 1]) << 16);
-            *reinterpret_cast<u32x4 *>(values + row * K + col) = o;
+            *reinterpret_cast<bf16x8 *>(values + row * K + col) = mx4_expand8(packed, scale);
         }
     }
 }
@@ -68,16 +51,10 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *__restrict__ 
     if (i >= rows * groups) return;
     const int64_t row = i / groups;
     const int g = (int)(i % groups);
-    float v[32];
-    mx4_expand(*reinterpret_cast<const u32x4 *>(codes + i * 16), scales[((int64_t)(g >> 3) * rows + row) * 8 + (g & 7)], v);
+    const u32x4 c = *reinterpret_cast<const u32x4 *>(codes + i * 16);
+    const float scale = mx4_scale_bits(scales[((int64_t)(g >> 3) * rows + row) * 8 + (g & 7)]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        u32x4 o;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            o[j] = (uint32_t)to_bf16(v[8 * q + 2 * j]) | ((uint32_t)to_bf16(v[8 * q + 2 * j + 1]) << 16);
-        *reinterpret_cast<u32x4 *>(values + i * 32 + 8 * q) = o;
-    }
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<bf16x8 *>(values + i * 32 + 8 * q) = mx4_expand8(c[q], scale);
 }
 
 int32_t launched(const char *what) {

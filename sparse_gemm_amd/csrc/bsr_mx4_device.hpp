@@ -6,27 +6,32 @@
 namespace bsr {
 namespace dev {
 
-// 2^(byte - 127): an exponent field, except for byte 0 (2^-127 is subnormal) and 255 (NaN).
-__device__ __forceinline__ float mx4_scale(uint32_t byte) {
-    if (byte == 0) return __uint_as_float(0x00400000u);
-    if (byte == 255) return __builtin_nanf("");
-    return __uint_as_float(byte << 23);
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// The conversion instructions of gfx950 take the scale as a 32-bit float's exponent field: field b is
+// 2^(b - 127) for b up to 254, 2^-127 for b = 0 as well, and NaN for b = 255. Expansion is exact; quantisation divides by
+// the scale and rounds to the nearest magnitude, ties to the even code, and saturates (checked for every code,
+// scale byte and bf16 value).
+__device__ __forceinline__ float mx4_scale_bits(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// The 8 values of 4 bytes of codes, element 2i in the low half of byte i.
+__device__ __forceinline__ bf16x8 mx4_expand8(uint32_t codes, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Magnitude of the low 3 bits of a code: 0, 0.5, 1, 1.5, 2, 3, 4, 6.
-__device__ __forceinline__ float mx4_magnitude(uint32_t m) {
-    return m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-}
+__device__ __forceinline__ bf16x2 bf16_pair(uint32_t w) { return __builtin_bit_cast(bf16x2, w); }
 
-// The 32 values of one group: element 2i in the low half of byte i.
-__device__ __forceinline__ void mx4_expand(u32x4 codes, uint32_t byte, float *v) {
-    const float scale = mx4_scale(byte);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const uint32_t c = codes[i >> 3] >> (4 * (i & 7));
-        const float m = mx4_magnitude(c & 7u) * scale;
-        v[i] = (c & 8u) ? -m : m;
-    }
+// The codes of 8 bf16 values (two in each word of x).
+__device__ __forceinline__ uint32_t mx4_quantize8(u32x4 x, float scale) {
+    uint32_t q = 0;
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, bf16_pair(x[0]), scale, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, bf16_pair(x[1]), scale, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, bf16_pair(x[2]), scale, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, bf16_pair(x[3]), scale, 3);
 }
 
 }  // namespace dev

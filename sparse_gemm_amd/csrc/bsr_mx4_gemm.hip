@@ -40,28 +40,21 @@ __device__ __forceinline__ void stage(const Part &s, int c0, int C, unsigned cha
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if constexpr (O == kMx4) {
         const int r = s.at + (threadIdx.x >> 1), g = (c0 >> 5) + (threadIdx.x & 1);
-        float v[32];
+        u32x4 codes = {0, 0, 0, 0};
+        float scale = 0.f;
         int64_t row = r < s.rows && g * 32 < C ? r : -1;
         if (row >= 0 && s.gather) {
             row = s.gather[r];
             if (row >= s.gmax) row = -1;
         }
         if (row >= 0) {
-            const u32x4 codes = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(s.p) + row * (C / 2) + g * 16);
-            mx4_expand(codes, s.scales[((int64_t)(g >> 3) * s.ld + row) * 8 + (g & 7)], v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            codes = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(s.p) + row * (C / 2) + g * 16);
+            scale = mx4_scale_bits(s.scales[((int64_t)(g >> 3) * s.ld + row) * 8 + (g & 7)]);
         }
         const int lr = threadIdx.x >> 1;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            u32x4 o;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = (uint32_t)to_bf16(v[8 * q + 2 * i]) | ((uint32_t)to_bf16(v[8 * q + 2 * i + 1]) << 16);
-            *reinterpret_cast<u32x4 *>(to + lr * 128 + (((4 * (threadIdx.x & 1) + q) ^ swz8(lr)) << 4)) = o;
-        }
+        for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<bf16x8 *>(to + lr * 128 + (((4 * (threadIdx.x & 1) + q) ^ swz8(lr)) << 4)) = mx4_expand8(codes[q], scale);
         return;
     }
     const __amdgpu_buffer_rsrc_t r = make_rsrc(s.p, s.bytes);
@@ -163,7 +156,7 @@ template <Form OA, Form OB>
 __global__ __launch_bounds__(256) void k_expert_simple(GemmArgs g, int ntiles) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * kTileBytes];
     const int nt = blockIdx.x % ntiles;
-    const Rows t = RowTiles<kBM>{g.offsets, g.E, g.R}.find(blockIdx.x / ntiles);
+    const Rows t = RowTiles<kBM>(g.offsets, g.E, g.R).find(blockIdx.x / ntiles);
     if (t.n <= 0) return;
     const bool live = t.e < g.E;
     const int C = live ? g.C : 0;
@@ -210,12 +203,6 @@ __device__ __forceinline__ f32x16 mfma_mx4(i32x4 a, i32x4 b, f32x16 c, int sa, i
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(codes8(a), codes8(b), c, 4, 4, J, sa, J, sb);
 }
 
-// Direct-to-LDS load of 4 bytes a lane (see dma16).
-__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t m0, uint32_t voff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0), "v"(voff), "s"(r)
-                 : "memory", "m0");
-}
-
 template <int BM, int BN>
 constexpr int mx4_lds() {
     const int stages = 2 * (BM + BN) * 136, out = BM * (BN * 2 + 16);
@@ -228,8 +215,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_mx4_mx4(GemmArgs g, int ntil
     static_assert(BM == NW * 32 && BN == NW * 32 && CT == 2, "one load of scales a wave and side");
     constexpr int AB = BM * 128, BB = BN * 128, AS = 2 * (AB + BB), BS = AS + 2 * BM * 8;   // LDS: A, B, scales of A, of B
     __shared__ __attribute__((aligned(1024))) unsigned char smem[mx4_lds<BM, BN>()];
-    const RowTiles<BM> tiles{g.offsets, g.E, g.R};
-    const int total = tiles.total();
+    const RowTiles<BM> tiles(g.offsets, g.E, g.R);
+    const int total = tiles.total;
     if ((int64_t)blockIdx.x >= (int64_t)total * ntiles) return;
     const TileOrder o = tile_order(xcd_remap(blockIdx.x, total * ntiles), total, ntiles, kRowsTogether);
     const Rows t = tiles.find(o.row);
@@ -384,6 +371,7 @@ int32_t launch_rows(const GemmArgs &g, void *stream, const char *what) {
 
 int32_t launch_expert_fwd_mx4(const ExpertShape &s, const uint16_t *X, const uint8_t *codes, const uint8_t *scales,
                               const uint16_t *bias, uint16_t *Y, void *stream) {
+    if (few_rows(s.R, s.E)) return launch_expert_fwd_few_mx4(s, X, codes, scales, bias, Y, stream);
     const GemmArgs g{X, codes, nullptr, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
     return launch_rows<kBf16, kMx4>(g, stream, "bsr_expert_fwd_mx4");
 }
