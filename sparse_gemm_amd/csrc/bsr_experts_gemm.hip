@@ -47,17 +47,19 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_rows(GemmArgs g, int 
                                             smem);
 }
 
-// Weight gradient: one BM x BN tile of one expert's dW a work-group, over all rows of the expert.
+// Weight gradient: one BM x BN tile of one expert's dW a work-group, over all rows of the expert. Every XCD takes an eighth of every expert's tiles: the experts' row counts
+// differ, and whole experts a XCD would leave some of them idle.
 template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_weight(const uint16_t *__restrict__ dY, const uint16_t *__restrict__ X,
                                                                const int32_t *__restrict__ offsets,
                                                                const int32_t *__restrict__ gather, int T, int R, int N,
                                                                int K, uint16_t *__restrict__ dW, int mtiles, int ntiles) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[tile_lds<BM, BN>()];
-    const int per = mtiles * ntiles, L = xcd_remap(blockIdx.x, gridDim.x), e = L / per;
-    const TileOrder o = tile_order(L % per, mtiles, ntiles, kRowsTogether);
-    const int lo = clamp_row(__builtin_amdgcn_readfirstlane(offsets[e]), R);
-    const int n = max(clamp_row(__builtin_amdgcn_readfirstlane(offsets[e + 1]), R) - lo, 0);
+    const int per = mtiles * ntiles, share = (per + kXCDs - 1) / kXCDs, slot = blockIdx.x / kXCDs;
+    const int e = slot / share, tile = (blockIdx.x % kXCDs) * share + slot % share;
+    if (tile >= per) return;
+    const TileOrder o = tile_order(tile, mtiles, ntiles, kRowsTogether);
+    const int lo = clamp_row(scalar_load(offsets, e), R), n = max(clamp_row(scalar_load(offsets, e + 1), R) - lo, 0);
     const Side a{dY + (int64_t)lo * N, (uint32_t)((int64_t)n * N * 2), N, o.row * BM, N, nullptr, 0, 0};
     const Side b = gather ? Side{X, (uint32_t)((int64_t)T * K * 2), K, o.col * BN, K, gather + lo, R - lo, T}
                           : Side{X + (int64_t)lo * K, (uint32_t)((int64_t)n * K * 2), K, o.col * BN, K, nullptr, 0, 0};
@@ -65,15 +67,19 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_weight(const uint16_t
                                                N - o.row * BM, K - o.col * BN, smem);
 }
 
-// Bias gradient: 64 columns of one expert a work-group; 8 columns a thread, 32 threads over the rows.
-__global__ __launch_bounds__(256) void k_expert_bias(const uint16_t *__restrict__ dY, const int32_t *__restrict__ offsets,
-                                                     int R, int N, uint16_t *__restrict__ dbias) {
-    __shared__ float part[32][64];
-    const int e = blockIdx.y, c = blockIdx.x * 64 + (threadIdx.x & 7) * 8, rl = threadIdx.x >> 3;
-    const int lo = clamp_row(offsets[e], R), hi = clamp_row(offsets[e + 1], R);
+// Bias gradient: 64 columns (whole cache lines) of one expert a work-group, 8 columns a thread and 128 threads over
+// the rows; their sums meet in LDS, in a fixed order.
+constexpr int kBiasRows = 128;
+
+__global__ __launch_bounds__(8 * kBiasRows) void k_expert_bias(const uint16_t *__restrict__ dY,
+                                                               const int32_t *__restrict__ offsets, int R, int N,
+                                                               uint16_t *__restrict__ dbias) {
+    __shared__ float part[kBiasRows][64 + 1];
+    const int e = blockIdx.y, sub = threadIdx.x & 7, c = blockIdx.x * 64 + sub * 8, rl = threadIdx.x >> 3;
+    const int lo = clamp_row(scalar_load(offsets, e), R), hi = clamp_row(scalar_load(offsets, e + 1), R);
     float s[8] = {};
     if (c < N) {
-        for (int r = lo + rl; r < hi; r += 32) {
+        for (int r = lo + rl; r < hi; r += kBiasRows) {
             const u32x4 v = *reinterpret_cast<const u32x4 *>(dY + (int64_t)r * N + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -83,13 +89,18 @@ __global__ __launch_bounds__(256) void k_expert_bias(const uint16_t *__restrict_
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[rl][(threadIdx.x & 7) * 8 + i] = s[i];
+    for (int i = 0; i < 8; ++i) part[rl][sub * 8 + i] = s[i];
     __syncthreads();
-    if (threadIdx.x < 64) {
+    for (int half = kBiasRows / 2; half >= 16; half >>= 1) {
+        for (int i = threadIdx.x; i < half * 64; i += 8 * kBiasRows) part[i >> 6][i & 63] += part[half + (i >> 6)][i & 63];
+        __syncthreads();
+    }
+    const int col = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && col < N) {
         float t = 0.f;
-        for (int r = 0; r < 32; ++r) t += part[r][threadIdx.x];
-        const int col = blockIdx.x * 64 + threadIdx.x;
-        if (col < N) dbias[(int64_t)e * N + col] = to_bf16(t);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) t += part[r][threadIdx.x];
+        dbias[(int64_t)e * N + col] = to_bf16(t);
     }
 }
 
@@ -134,17 +145,17 @@ int32_t launch_expert_bwd_weight(const ExpertShape &s, const uint16_t *dY, const
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const bool w = (int64_t)s.E * ((s.N + 255) / 256) * ((s.K + 255) / 256) >= 192;
     const int64_t bm = w ? 256 : 128, mt = (s.N + bm - 1) / bm, nt = (s.K + bm - 1) / bm;
-    if (mt * nt * s.E > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, "bsr_expert_bwd_weight: too many tiles");
-    const dim3 grid((unsigned)(mt * nt * s.E));
-    if (w)
-        hipLaunchKernelGGL((k_expert_weight<256, 256, 2, 4>), grid, dim3(512), 0, st, dY, X, s.offsets, s.row_token, s.T,
+    const int64_t blocks = (mt * nt + 7) / 8 * 8 * s.E;
+    if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, "bsr_expert_bwd_weight: too many tiles");
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(w ? 512 : 256), 0, st, dY, X, s.offsets, s.row_token, s.T,
                            s.R, s.N, s.K, dW, (int)mt, (int)nt);
-    else
-        hipLaunchKernelGGL((k_expert_weight<128, 128, 2, 2>), grid, dim3(256), 0, st, dY, X, s.offsets, s.row_token, s.T,
-                           s.R, s.N, s.K, dW, (int)mt, (int)nt);
+    };
+    if (w) run(k_expert_weight<256, 256, 2, 4>);
+    else run(k_expert_weight<128, 128, 2, 2>);
     if (dbias)
-        hipLaunchKernelGGL(k_expert_bias, dim3((unsigned)((s.N + 63) / 64), (unsigned)s.E), dim3(256), 0, st, dY, s.offsets,
-                           s.R, s.N, dbias);
+        hipLaunchKernelGGL(k_expert_bias, dim3((unsigned)((s.N + 63) / 64), (unsigned)s.E), dim3(8 * kBiasRows), 0, st, dY,
+                           s.offsets, s.R, s.N, dbias);
     return launched("bsr_expert_bwd_weight");
 }
 

@@ -60,6 +60,7 @@ struct Stager {
     const int32_t *gather;
     int gcount, gmax, C;
     uint32_t ld2;
+    int tok[4][kRowsPerLoad > 0 ? kRowsPerLoad : 1];   // tokens of the loads' rows
     uint32_t rowoff[4];    // this lane's row offset of load j of the step being issued
 
     __device__ __forceinline__ void init(const Side &s, int C_) {
@@ -94,24 +95,32 @@ struct Stager {
         }
         step = O == kRows ? 128u : 64u * ld2;
     }
-    // Row offsets of a gathered kCols operand for step s, from scalar loads (rows past C and tokens
-    // out of range read zeros).
-    __device__ __forceinline__ void fetch(int s) {
+    // Rows of a gathered kCols operand: tokens(s) issues scalar loads of step s's entries, which are not waited
+    // for; rows(s) turns them into this lane's offsets (rows past C and tokens out of range read zeros).
+    __device__ __forceinline__ void tokens(int s) {
         if constexpr (O == kCols) {
-            if (!gather) return;   // (uniform; steps past the last one give rows past C)
+            if (!gather) return;   // uniform
+            const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < kRowsPerLoad; ++r)
+                    tok[j][r] = scalar_load(gather, min(s * 64 + kRowsPerLoad * (wave + NW * j) + r, gcount - 1));
+        }
+    }
+    __device__ __forceinline__ void rows(int s) {
+        if constexpr (O == kCols) {
+            if (!gather) return;
             const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c0 = s * 64 + kRowsPerLoad * (wave + NW * j);
-                uint32_t o[kRowsPerLoad];
+                uint32_t v = 0;
 #pragma unroll
                 for (int r = 0; r < kRowsPerLoad; ++r) {
-                    const int t = scalar_load(gather, min(c0 + r, gcount - 1));
-                    o[r] = c0 + r < C && (unsigned)t < (unsigned)gmax ? (uint32_t)t * ld2 : kPast;
+                    const uint32_t o = c0 + r < C && (unsigned)tok[j][r] < (unsigned)gmax ? (uint32_t)tok[j][r] * ld2 : kPast;
+                    v = r == 0 || lane / kRowChunks == r ? o : v;
                 }
-                uint32_t v = o[0];
-#pragma unroll
-                for (int r = 1; r < kRowsPerLoad; ++r) v = lane / kRowChunks == r ? o[r] : v;
                 rowoff[j] = v;
             }
         }
@@ -238,13 +247,14 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
         };
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            gb.fetch(s);
+            gb.tokens(s);
 #pragma unroll
             for (int j = 0; j < 4; ++j) issue_a(s, s, j);
+            gb.rows(s);
 #pragma unroll
             for (int j = 0; j < 4; ++j) issue_b(s, s, j);
         }
-        gb.fetch(2);
+        gb.tokens(2);
         wait_vm<8, 8>(8);
         __syncthreads();
         read_frags(0, 0, 0, 0);
@@ -259,6 +269,8 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
                 });
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
+            gb.rows(s + 2);
+            gb.tokens(s + 3);   // with no LDS read outstanding: scalar loads share their counter and return out of order
             wait_vm<4, 4>(4);                                     // all but the A loads of s + 2 have landed
             __syncthreads();
             const int xn = xs == 2 ? 0 : xs + 1, vn = vs ^ 1;
@@ -267,7 +279,6 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
                 issue_b(vs, s + 2, 2 * t);
                 issue_b(vs, s + 2, 2 * t + 1);
             });
-            gb.fetch(s + 3);
             xs = xn;
             vs = vn;
         }
