@@ -1,9 +1,6 @@
 // bsr_mx4_gemm.hip -- products grouped by expert on microscaled 4-bit weights (include/bsr_mx4.h).
 //
-//   out[m][n] = sum over c of A(m, c) B(n, c), for each expert e:
-//     forward       m row, n output column, c input column:   A = x(row)[c], B = W[e][n][c]
-//     input grad    m row, n input column, c output column:   A = dY[row][c], B = W[e][c][n]
-//     weight grad   m output column, n input column, c row:   A = dY[c][m],   B = x(c)[n]
+// out[m][n] = sum over c of A(m, c) B(n, c) for each expert: m row, n output column, c input column.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -18,130 +15,6 @@ namespace {
 
 using namespace dev;
 
-constexpr int kBM = 128, kBN = 128, kBK = 64;
-constexpr int kTileBytes = 128 * kBK * 2;
-
-enum Form { kBf16, kMx4 };
-
-struct Part {
-    const void *p;             // first element of this expert's / tile's matrix
-    uint32_t bytes;            // its size
-    const uint8_t *scales;     // kMx4
-    int ld;                    // elements (kMx4: rows of the scale array)
-    const int32_t *gather;     // token of each row (kBf16: output rows; kCols: contraction rows), or NULL
-    int gmax;                  // tokens
-    int rows;                  // rows (kBf16, kMx4) or columns (kCols) that exist
-    int at;                    // first of them in this tile
-};
-
-// Stages the 128 x 64 tile of contraction step c0 .. c0 + 63 (of C) at LDS byte address `to`.
-template <Form O>
-__device__ __forceinline__ void stage(const Part &s, int c0, int C, unsigned char *to) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if constexpr (O == kMx4) {
-        const int r = s.at + (threadIdx.x >> 1), g = (c0 >> 5) + (threadIdx.x & 1);
-        u32x4 codes = {0, 0, 0, 0};
-        float scale = 0.f;
-        int64_t row = r < s.rows && g * 32 < C ? r : -1;
-        if (row >= 0 && s.gather) {
-            row = s.gather[r];
-            if (row >= s.gmax) row = -1;
-        }
-        if (row >= 0) {
-            codes = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(s.p) + row * (C / 2) + g * 16);
-            scale = mx4_scale_bits(s.scales[((int64_t)(g >> 3) * s.ld + row) * 8 + (g & 7)]);
-        }
-        const int lr = threadIdx.x >> 1;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<bf16x8 *>(to + lr * 128 + (((4 * (threadIdx.x & 1) + q) ^ swz8(lr)) << 4)) = mx4_expand8(codes[q], scale);
-        return;
-    }
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(s.p, s.bytes);
-    const uint32_t m0 = lds_addr(to);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int i = wave + 4 * j;
-        uint32_t off;
-        if constexpr (O == kBf16) {
-            const int lr = 8 * i + (lane >> 3), row = s.at + lr, c = c0 + 8 * ((lane & 7) ^ swz8(lr));
-            int src = row;
-            bool ok = row < s.rows && c < C;
-            if (s.gather) {
-                src = row < s.rows ? s.gather[row] : -1;
-                ok = ok && (unsigned)src < (unsigned)s.gmax;
-            }
-            off = ok ? (uint32_t)src * (uint32_t)s.ld * 2u + (uint32_t)c * 2u : kPast;
-        }
-        dma16(r, m0 + (uint32_t)i * 1024u, off, 0);
-    }
-}
-
-// Fragment of rows / columns t0 .. t0 + 31 of a staged tile for contraction chunk kc (16 deep).
-template <Form O>
-__device__ __forceinline__ bf16x8 frag(const unsigned char *tile, int t0, int kc) {
-    const int lane = threadIdx.x & 63;
-    const int r = t0 + (lane & 31);
-    return *reinterpret_cast<const bf16x8 *>(tile + r * 128 + (((2 * kc + (lane >> 5)) ^ swz8(r)) << 4));
-}
-
-// One 128 x 128 tile of out (leading dimension ldo, `om` rows and `on` columns of it exist).
-template <Form OA, Form OB>
-__device__ __forceinline__ void simple_product(const Part &a, const Part &b, int C, const uint16_t *bias, uint16_t *out,
-                                             int ldo, int om, int on, unsigned char *smem) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
-    f32x16 acc[2][2];   // [n tile][m tile]
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    const int steps = (C + kBK - 1) / kBK;
-    auto load = [&](int s) __attribute__((always_inline)) {
-        unsigned char *to = smem + (s & 1) * 2 * kTileBytes;
-        stage<OA>(a, s * kBK, C, to);
-        stage<OB>(b, s * kBK, C, to + kTileBytes);
-    };
-    if (steps > 0) load(0);
-    for (int s = 0; s < steps; ++s) {
-        wait_vm<0, 0>(0);
-        __syncthreads();
-        if (s + 1 < steps) load(s + 1);
-        const unsigned char *ta = smem + (s & 1) * 2 * kTileBytes, *tb = ta + kTileBytes;
-#pragma unroll
-        for (int kc = 0; kc < 4; ++kc) {
-            bf16x8 fa[2], fb[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fa[i] = frag<OA>(ta, wm + 32 * i, kc);
-                fb[i] = frag<OB>(tb, wn + 32 * i, kc);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(fb[i], fa[j], acc[i][j]);
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int m = wm + 32 * j + (lane & 31);
-        if (m >= om) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = wn + 32 * i + 8 * q + 4 * (lane >> 5);
-                if (n >= on) continue;
-                f32x4 v = quad(acc[i][j], q);
-                if (bias) v = add_bias4(v, bias + n);
-                store4_bf16(out + (int64_t)m * ldo + n, v[0], v[1], v[2], v[3]);
-            }
-    }
-}
-
 struct GemmArgs {
     const void *act, *w;
     const uint8_t *act_scales, *w_scales;
@@ -151,36 +24,90 @@ struct GemmArgs {
     int T, R, E, Nout, C;   // output columns, contraction length
 };
 
-// Forward and input gradient: one 128-row x 128-column tile a work-group.
-template <Form OA, Form OB>
-__global__ __launch_bounds__(256) void k_expert_simple(GemmArgs g, int ntiles) {
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * kTileBytes];
-    const int nt = blockIdx.x % ntiles;
-    const Rows t = RowTiles<kBM>(g.offsets, g.E, g.R).find(blockIdx.x / ntiles);
+// ------------------------------------------------------------------------------------------
+// bf16 activations: one 128 x 128 tile a work-group of 4 waves, steps of 64 columns. The codes are staged as they
+// are (32 bytes a row and step) and turned into bf16 fragments in registers: half-wave h of a row takes the
+// group of columns 32 h .. 32 h + 31, one 16-byte read a step whose word i is its operand of the i-th product, so
+// the activation fragments take the columns 32 h + 8 i + 0 .. 7. Three stages a side, loads two steps ahead.
+// ------------------------------------------------------------------------------------------
+constexpr int kA = 128 * 128, kB = 128 * 32, kS = 128 * 8, kStage = kA + kB + kS;
+
+__global__ __launch_bounds__(256, 2) void k_mx4_rows(GemmArgs g, int ntiles) {
+    constexpr int BM = 128, BN = 128, out = BM * (BN * 2 + 16);
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[3 * kStage > out ? 3 * kStage : out];
+    const RowTiles<BM> tiles(g.offsets, g.E, g.R);
+    const int total = tiles.total;
+    if ((int64_t)blockIdx.x >= (int64_t)total * ntiles) return;
+    const TileOrder o = tile_order(xcd_remap(blockIdx.x, total * ntiles), total, ntiles, kRowsTogether);
+    const Rows t = tiles.find(o.row);
     if (t.n <= 0) return;
     const bool live = t.e < g.E;
-    const int C = live ? g.C : 0;
-    const int e = live ? t.e : 0;
-    const int64_t wsize = (int64_t)g.Nout * g.C;
-    Part a{}, b{};
-    if constexpr (OA == kMx4) {
-        a = {g.act, 0, g.act_scales, g.gather ? g.T : g.R, g.gather, g.T, t.at + t.n, t.at};
-    } else if (g.gather) {
-        a = {g.act, (uint32_t)((int64_t)g.T * g.C * 2), nullptr, g.C, g.gather, g.T, t.at + t.n, t.at};
-    } else {   // the tile's own rows
-        a = {static_cast<const uint16_t *>(g.act) + (int64_t)t.at * g.C, (uint32_t)((int64_t)t.n * g.C * 2), nullptr, g.C,
-             nullptr, 0, t.n, 0};
+    const int e = live ? t.e : 0, kb = (g.C + 255) / 256, steps = live ? (g.C + 63) / 64 : 0;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = (wave & 1) * 64, n0 = (wave >> 1) * 64, l32 = lane & 31, lh = lane >> 5;
+    const uint32_t base = lds_addr(smem);
+
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[r][c][v] = 0.f;
+
+    if (steps > 0) {
+        Stager<kRows, BM, 4> ga;
+        ga.init({static_cast<const uint16_t *>(g.act), (uint32_t)((int64_t)(g.gather ? g.T : g.R) * g.C * 2), g.C, t.at, t.at + t.n,
+                 g.gather, g.R, g.T}, g.C);
+        const int64_t wbytes = (int64_t)g.Nout * (g.C / 2);
+        const __amdgpu_buffer_rsrc_t rw = make_rsrc(static_cast<const uint8_t *>(g.w) + e * wbytes, (uint32_t)wbytes);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(g.w_scales + (int64_t)e * kb * g.Nout * 8, (uint32_t)((int64_t)kb * g.Nout * 8));
+        // lane 2 r + h of wave w loads the h-th group's codes and, every fourth step, the h-th scale word of row 32 w + r
+        const int row = o.col * BN + wave * 32 + (lane >> 1), h = lane & 1;
+        const uint32_t boff = (uint32_t)row * (uint32_t)(g.C / 2) + 16u * h, soff = (uint32_t)row * 8u + 4u * h;
+        const int blim = row < g.Nout ? (g.C / 2 - 16 * h + 31) / 32 : 0, slim = row < g.Nout ? steps : 0;
+        auto issue = [&](int s) __attribute__((always_inline)) {
+            const uint32_t to = base + (uint32_t)(s % 3) * kStage;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ga.issue(to, s, j);
+            dma16(rw, to + kA + (uint32_t)wave * 1024u, s < blim ? boff + (uint32_t)s * 32u : kPast, 0);
+            dma4(rs, to + kA + kB + (uint32_t)wave * 256u, s < slim ? soff + (uint32_t)(s >> 2) * (uint32_t)g.Nout * 8u : kPast);
+        };
+        issue(0);
+        issue(1);
+        for (int s = 0; s < steps; ++s) {
+            wait_vm<6, 6>(6);   // step s has landed
+            __syncthreads();
+            issue(s + 2);       // into the stage of step s - 1, which every wave has read
+            const unsigned char *ta = smem + (s % 3) * kStage, *tb = ta + kA, *ts = tb + kB;
+            u32x4 codes[2];
+            float scale[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = n0 + 32 * c + l32;
+                codes[c] = *reinterpret_cast<const u32x4 *>(tb + r * 32 + 16 * lh);
+                const uint32_t byte = *(ts + r * 8 + 2 * (s & 3) + lh);
+                scale[c] = mx4_scale_bits((2 * s + lh) * 32 < g.C ? byte : 0);   // bytes past K may hold anything
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                bf16x8 fa[2], fb[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int r = m0 + 32 * c + l32;
+                    fa[c] = *reinterpret_cast<const bf16x8 *>(ta + r * 128 + (((4 * lh + i) ^ swz8(r)) << 4));
+                    fb[c] = mx4_expand8(codes[c][i], scale[c]);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) acc[r][c] = mfma32(fb[c], fa[r], acc[r][c]);
+            }
+        }
+        wait_vm<0, 0>(0);
     }
-    if constexpr (OB == kMx4) {
-        const int64_t kb = (g.C + 255) / 256;
-        b = {static_cast<const uint8_t *>(g.w) + e * wsize / 2, 0, g.w_scales + e * kb * g.Nout * 8, g.Nout, nullptr, 0,
-             g.Nout, nt * kBN};
-    } else {
-        b = {static_cast<const uint16_t *>(g.w) + e * wsize, (uint32_t)(wsize * 2), nullptr, g.C,
-             nullptr, 0, g.Nout, nt * kBN};
-    }
-    simple_product<OA, OB>(a, b, C, live && g.bias ? g.bias + (int64_t)e * g.Nout + nt * kBN : nullptr,
-                         g.out + (int64_t)t.at * g.Nout + nt * kBN, g.Nout, t.n, g.Nout - nt * kBN, smem);
+    store_tile<BM, BN, 2, 2>(acc, live && g.bias ? g.bias + (int64_t)e * g.Nout + o.col * BN : nullptr,
+                             g.out + (int64_t)t.at * g.Nout + o.col * BN, g.Nout, t.n, g.Nout - o.col * BN, smem);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -358,22 +285,16 @@ int32_t launched(const char *what) {
 // 256 x 256 tiles with 8 waves where the groups fill them, else 128 x 128 with 4.
 bool wide(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 + 1) * ((cols + 255) / 256) >= 192; }
 
-template <Form OA, Form OB>
-int32_t launch_rows(const GemmArgs &g, void *stream, const char *what) {
-    const int64_t ntiles = (g.Nout + kBN - 1) / kBN, blocks = max_row_tiles(g.R, g.E, kBM) * ntiles;
-    if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, std::string(what) + ": too many tiles");
-    hipLaunchKernelGGL((k_expert_simple<OA, OB>), dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), g,
-                       (int)ntiles);
-    return launched(what);
-}
-
 }  // namespace
 
 int32_t launch_expert_fwd_mx4(const ExpertShape &s, const uint16_t *X, const uint8_t *codes, const uint8_t *scales,
                               const uint16_t *bias, uint16_t *Y, void *stream) {
     if (few_rows(s.R, s.E)) return launch_expert_fwd_few_mx4(s, X, codes, scales, bias, Y, stream);
     const GemmArgs g{X, codes, nullptr, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
-    return launch_rows<kBf16, kMx4>(g, stream, "bsr_expert_fwd_mx4");
+    const int64_t ntiles = (s.N + 127) / 128, blocks = max_row_tiles(s.R, s.E, 128) * ntiles;
+    if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, "bsr_expert_fwd_mx4: too many tiles");
+    hipLaunchKernelGGL(k_mx4_rows, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), g, (int)ntiles);
+    return launched("bsr_expert_fwd_mx4");
 }
 
 int32_t launch_expert_fwd_mx4_mx4(const ExpertShape &s, const uint8_t *xcodes, const uint8_t *xscales,
