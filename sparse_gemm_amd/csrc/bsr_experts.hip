@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "bsr_device.hpp"
 #include "bsr_experts_internal.hpp"
@@ -36,140 +37,209 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// Router forward, one wave a token: lane l holds the logits of experts l + 64 i. k rounds of a wave-wide
-// maximum over (key, lowest expert); a taken expert's key becomes 0, below every logit's.
+// The value behind a key (NaN for the largest key).
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return key == 0xFFFFFFFFu ? __builtin_nanf("") : __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
+// Rotation by D lanes within each row of 16 lanes, on the vector units (no LDS crossbar).
+template <int D>
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + D, 0xF, 0xF, true);
+}
+// Maximum and sum over each group of G = 16 or 64 lanes.
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    v = max(v, row_rotate<8>(v));
+    v = max(v, row_rotate<4>(v));
+    v = max(v, row_rotate<2>(v));
+    v = max(v, row_rotate<1>(v));
+    if constexpr (G == 64) {
+        v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+        v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+    }
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+    v += __uint_as_float(row_rotate<8>(__float_as_uint(v)));
+    v += __uint_as_float(row_rotate<4>(__float_as_uint(v)));
+    v += __uint_as_float(row_rotate<2>(__float_as_uint(v)));
+    v += __uint_as_float(row_rotate<1>(__float_as_uint(v)));
+    if constexpr (G == 64) {
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+    }
+    return v;
+}
+
+// The NV logits of experts first .. first + NV - 1 (-infinity past E). whole: rows are whole 16-byte pieces.
 template <typename L, int NV>
+__device__ __forceinline__ void load_logits(const L *row, int first, int E, bool whole, float *v) {
+    constexpr int kPiece = 16 / sizeof(L);
+    if constexpr (NV % kPiece == 0) {
+        if (whole) {
+#pragma unroll
+            for (int p = 0; p < NV / kPiece; ++p) {
+                u32x4 w = {0, 0, 0, 0};
+                const bool in = first + p * kPiece < E;
+                if (in) w = *reinterpret_cast<const u32x4 *>(row + first + p * kPiece);
+#pragma unroll
+                for (int i = 0; i < kPiece; ++i) {
+                    const uint32_t word = w[i * sizeof(L) / 4];
+                    const float f = sizeof(L) == 4 ? __uint_as_float(word) : __uint_as_float((i & 1) ? word & 0xFFFF0000u : word << 16);
+                    v[p * kPiece + i] = in ? f : kNegInf;
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = first + i < E ? load_logit(row + first + i) : kNegInf;
+}
+
+// Router forward: a token takes a group of G lanes, lane l the experts l NV .. l NV + NV - 1. k rounds: the
+// largest key of the group, then the lowest lane and expert that holds it (ties to the lowest expert); a taken key
+// becomes 0, below every logit's. Slot j stays with lane j until the end. 16 lanes a token (up to 256 experts and
+// 16 slots) keep the rounds on row rotations: 16390 x 128 bf16, k = 8: 21 us with a wave a token and shuffles.
+template <typename L, int NV, int G>
 __global__ __launch_bounds__(256) void k_router_fwd(const L *__restrict__ logits, int T, int E, int k, int renorm,
-                                                    int32_t *__restrict__ index, float *__restrict__ weight) {
-    const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= T) return;
+                                                    bool whole, int32_t *__restrict__ index, float *__restrict__ weight) {
+    const int lane = threadIdx.x & 63, gl = lane & (G - 1), g0 = lane & ~(G - 1);
+    const int t = blockIdx.x * (256 / G) + threadIdx.x / G;
+    const bool in = t < T;
     float v[NV];
     uint32_t key[NV];
+    load_logits<L, NV>(logits + (int64_t)min(t, T - 1) * E, gl * NV, E, whole, v);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 64 * i;
-        v[i] = e < E ? load_logit(logits + (int64_t)t * E + e) : kNegInf;
-        key[i] = e < E ? order_key(v[i]) : 0;
-    }
-    float top = 0.f, mine = kNegInf;   // mine: the logit of slot `lane`
+    for (int i = 0; i < NV; ++i) key[i] = gl * NV + i < E ? order_key(v[i]) : 0;
+    uint32_t top = 0, mine = 0;
     int pick = -1;
     for (int j = 0; j < k; ++j) {
-        uint64_t best = 0;
+        uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const uint64_t c = ((uint64_t)key[i] << 32) | (uint32_t)~(lane + 64 * i);
-            best = c > best ? c : best;
-        }
+        for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+        const uint32_t all = group_max<G>(best);
+        const bool some = all > kKeyNegInf;   // else nothing but -infinity is left
+        const uint64_t have = __ballot(best == all) >> g0;
+        const int owner = __builtin_ctzll(have);
+        int at = -1;
+        if (some && gl == owner) {
 #pragma unroll
-        for (int d = 32; d; d >>= 1) {
-            const uint64_t o = __shfl_xor(best, d);
-            best = o > best ? o : best;
-        }
-        const uint32_t bk = (uint32_t)(best >> 32);
-        if (bk <= kKeyNegInf) break;   // nothing but -infinity is left
-        const int e = (int)~(uint32_t)best;
-        float val = 0.f;
+            for (int i = NV - 1; i >= 0; --i) at = key[i] == all ? i : at;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (e == lane + 64 * i) {
-                val = v[i];
-                key[i] = 0;
-            }
+            for (int i = 0; i < NV; ++i) key[i] = i == at ? 0 : key[i];
         }
-        val = __shfl(val, e & 63);
-        if (j == 0) top = val;
-        if (lane == j) {
+        const int e = __shfl(at, g0 + owner) + owner * NV;
+        if (j == 0) top = all;
+        if (some && gl == j) {
             pick = e;
-            mine = val;
+            mine = all;
         }
     }
     // Weights in 32 bits. top is a real logit, +infinity or NaN whenever any slot was filled.
-    float ex = pick >= 0 ? expf(mine - top) : 0.f, den = ex;
+    const float m = top > kKeyNegInf ? key_value(top) : 0.f;
+    const float ex = pick >= 0 ? expf(key_value(mine) - m) : 0.f;
+    float den = ex;
     if (!renorm) {
         den = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) den += expf(v[i] - top);   // -infinity gives 0
+        for (int i = 0; i < NV; ++i) den += expf(v[i] - m);   // -infinity gives 0
     }
-    den = wave_sum(den);
-    if (lane < k) {
-        index[(int64_t)t * k + lane] = pick;
-        weight[(int64_t)t * k + lane] = pick >= 0 ? ex / den : 0.f;
+    den = group_sum<G>(den);
+    if (in && gl < k) {
+        index[(int64_t)t * k + gl] = pick;
+        weight[(int64_t)t * k + gl] = pick >= 0 ? ex / den : 0.f;
     }
 }
 
-// Router backward, one wave a token. Not renormalised: p is computed again from the logits.
-template <typename L, int NV>
+// Router backward, the same lanes. Not renormalised: p is computed again from the logits.
+template <typename L, int NV, int G>
 __global__ __launch_bounds__(256) void k_router_bwd(const L *__restrict__ logits, int T, int E, int k, int renorm,
-                                                    const int32_t *__restrict__ index, const float *__restrict__ weight,
-                                                    const float *__restrict__ dweight, L *__restrict__ dlogits) {
-    const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= T) return;
+                                                    bool whole, const int32_t *__restrict__ index,
+                                                    const float *__restrict__ weight, const float *__restrict__ dweight,
+                                                    L *__restrict__ dlogits) {
+    const int lane = threadIdx.x & 63, gl = lane & (G - 1), g0 = lane & ~(G - 1);
+    const int t = blockIdx.x * (256 / G) + threadIdx.x / G;
+    const bool in = t < T;
     int pick = -1;
     float w = 0.f, g = 0.f;
-    if (lane < k) {
-        pick = index[(int64_t)t * k + lane];
+    if (in && gl < k) {
+        pick = index[(int64_t)t * k + gl];
         if ((unsigned)pick < (unsigned)E) {
-            w = weight[(int64_t)t * k + lane];
-            g = dweight[(int64_t)t * k + lane];
+            w = weight[(int64_t)t * k + gl];
+            g = dweight[(int64_t)t * k + gl];
         } else {
             pick = -1;
         }
     }
-    const float inner = wave_sum(w * g);
+    const float inner = group_sum<G>(w * g);
     float v[NV], d[NV];
     if (!renorm) {
-        float m = kNegInf;
-        bool nan = false;
+        load_logits<L, NV>(logits + (int64_t)min(t, T - 1) * E, gl * NV, E, whole, v);
+        uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = lane + 64 * i;
-            v[i] = e < E ? load_logit(logits + (int64_t)t * E + e) : kNegInf;
-            nan |= v[i] != v[i];
-            m = fmaxf(m, v[i]);
-        }
-#pragma unroll
-        for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-        if (__any(nan)) m = __builtin_nanf("");
-        const bool none = m == kNegInf;
+        for (int i = 0; i < NV; ++i) best = max(best, gl * NV + i < E ? order_key(v[i]) : 0u);
+        const uint32_t top = group_max<G>(best);
+        const bool none = top <= kKeyNegInf;
+        const float m = none ? 0.f : key_value(top);
         float den = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            v[i] = none ? 0.f : expf(v[i] - m);
+            v[i] = expf(v[i] - m);
             den += v[i];
         }
-        den = wave_sum(den);
-        const float scale = none ? 0.f : 1.f / den;
+        den = group_sum<G>(den);
+        const float scale = none ? 0.f : inner / den;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] = -(v[i] * scale) * inner;
+        for (int i = 0; i < NV; ++i) d[i] = -v[i] * scale;
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) d[i] = 0.f;
     }
     const float add = renorm ? w * (g - inner) : w * g;
     for (int j = 0; j < k; ++j) {
-        const int e = __shfl(pick, j);
-        const float a = __shfl(add, j);
+        const int e = __shfl(pick, g0 + j) - gl * NV;
+        const float a = __shfl(add, g0 + j);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (e == lane + 64 * i) d[i] += a;
+        for (int i = 0; i < NV; ++i) d[i] += e == i ? a : 0.f;
+    }
+    if (!in) return;
+    L *out = dlogits + (int64_t)t * E + gl * NV;
+    constexpr int kPiece = 16 / sizeof(L);
+    if constexpr (NV % kPiece == 0) {
+        if (whole) {
+#pragma unroll
+            for (int p = 0; p < NV / kPiece; ++p) {
+                if (gl * NV + p * kPiece >= E) break;
+                u32x4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float *f = d + p * kPiece;
+                    o[i] = sizeof(L) == 4 ? __float_as_uint(f[i])
+                                          : (uint32_t)to_bf16(f[(2 * i) % kPiece]) | ((uint32_t)to_bf16(f[(2 * i + 1) % kPiece]) << 16);
+                }
+                *reinterpret_cast<u32x4 *>(out + p * kPiece) = o;
+            }
+            return;
+        }
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 64 * i;
-        if (e < E) store_logit(dlogits + (int64_t)t * E + e, d[i]);
-    }
+    for (int i = 0; i < NV; ++i)
+        if (gl * NV + i < E) store_logit(out + i, d[i]);
 }
 
 // ------------------------------------------------------------------------------------------
 // The plan: a stable counting sort of S = T k slots by expert.
-// Chunks of 1024 slots (16 waves): a slot's row is offsets[e] + the slots of e in earlier chunks + those in
-// earlier waves of the chunk + those in lower lanes of its wave (a ballot for each bit of e).
-// Up to one chunk, one work-group does everything; beyond that, a launch counts each chunk, a second one
-// turns the counts into first rows and offsets, and a third one writes.
+// A slot's row is offsets[e] + the slots of e in earlier chunks + those in earlier rounds of 1024 slots of its
+// chunk + those in earlier waves of the round + those in lower lanes of its wave (a ballot for each bit of e).
+// Up to 1024 slots, one work-group does everything. Beyond that one launch counts each chunk's slots, and in
+// a second one every chunk adds up the counts that it needs by itself; chunks have as many rounds as keep
+// their number within 256, so that this stays a few loads a thread.
 // ------------------------------------------------------------------------------------------
-constexpr int kPlanChunk = 1024;
+constexpr int kPlanRound = 1024, kPlanChunks = 256;
 
-// Counts of this chunk's waves in cnt[16][E] (16-bit) and this slot's rank among its wave's.
+// Counts of this round's waves in cnt[16][E] (16-bit) and this slot's rank among its wave's.
 __device__ __forceinline__ int plan_rank(int e, int E, int bits, uint16_t *cnt) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     uint64_t same = ~0ull;
@@ -210,95 +280,98 @@ __device__ __forceinline__ int block_prefix(int v, int *scratch, int *total) {
     return before + x - v;
 }
 
-__global__ __launch_bounds__(kPlanChunk) void k_plan_one(const int32_t *__restrict__ index, int S, int k, int E, int bits,
-                                                         int32_t *__restrict__ offsets, int32_t *__restrict__ row_token,
-                                                         int32_t *__restrict__ slot_row) {
-    extern __shared__ uint16_t cnt[];   // [16][E]
-    __shared__ int scratch[16];
-    __shared__ int first[kMaxExperts];
-    const int tid = threadIdx.x, wave = tid >> 6;
-    for (int i = tid; i < 16 * E; i += kPlanChunk) cnt[i] = 0;
-    __syncthreads();
-    const int e = plan_expert(index, tid, S, E);
-    const int rank = plan_rank(e, E, bits, cnt);
-    __syncthreads();
-    int mine = 0;
-    if (tid < E) {
-        for (int w = 0; w < 16; ++w) {
-            const int c = cnt[w * E + tid];
-            cnt[w * E + tid] = (uint16_t)mine;
-            mine += c;
-        }
-    }
-    int live;
-    const int before = block_prefix(mine, scratch, &live);
-    if (tid < E) {
-        first[tid] = before;
-        offsets[tid] = before;
-    }
-    if (tid == 0) offsets[E] = live;
-    __syncthreads();
-    if (tid < S) {
-        const int row = e < E ? first[e] + cnt[wave * E + e] + rank : -1;
-        slot_row[tid] = row;
-        if (row >= 0) row_token[row] = tid / k;
-        if (tid >= live) row_token[tid] = -1;
-    }
-}
-
-__global__ __launch_bounds__(kPlanChunk) void k_plan_count(const int32_t *__restrict__ index, int64_t S, int E,
+__global__ __launch_bounds__(kPlanRound) void k_plan_count(const int32_t *__restrict__ index, int64_t S, int E, int rounds,
                                                            int32_t *__restrict__ counts) {
     __shared__ int hist[kMaxExperts];
     const int tid = threadIdx.x;
-    for (int i = tid; i < E; i += kPlanChunk) hist[i] = 0;
+    for (int i = tid; i < E; i += kPlanRound) hist[i] = 0;
     __syncthreads();
-    const int e = plan_expert(index, (int64_t)blockIdx.x * kPlanChunk + tid, S, E);
-    if (e < E) atomicAdd(&hist[e], 1);   // whole numbers: the order does not matter
+    const int64_t s0 = (int64_t)blockIdx.x * rounds * kPlanRound;
+    for (int r = 0; r < rounds; ++r) {
+        const int e = plan_expert(index, s0 + (int64_t)r * kPlanRound + tid, S, E);
+        if (e < E) atomicAdd(&hist[e], 1);   // whole numbers: the order does not matter
+    }
     __syncthreads();
-    for (int i = tid; i < E; i += kPlanChunk) counts[(int64_t)blockIdx.x * E + i] = hist[i];
+    for (int i = tid; i < E; i += kPlanRound) counts[(int64_t)blockIdx.x * E + i] = hist[i];
 }
 
-// counts[chunk][e] -> the rows of e in earlier chunks; offsets from the totals. One work-group.
-__global__ __launch_bounds__(kPlanChunk) void k_plan_first(int32_t *__restrict__ counts, int chunks, int E,
-                                                           int32_t *__restrict__ offsets) {
+// counts: [chunks][E], or NULL for a single chunk of one round.
+__global__ __launch_bounds__(kPlanRound) void k_plan_write(const int32_t *__restrict__ index, int64_t S, int k, int E,
+                                                           int bits, int rounds, int chunks,
+                                                           const int32_t *__restrict__ counts,
+                                                           int32_t *__restrict__ offsets, int32_t *__restrict__ row_token,
+                                                           int32_t *__restrict__ slot_row) {
+    extern __shared__ uint16_t cnt[];   // [16][E]
     __shared__ int scratch[16];
-    const int tid = threadIdx.x;
-    int mine = 0;
-    if (tid < E) {
-        for (int c = 0; c < chunks; ++c) {
-            const int n = counts[(int64_t)c * E + tid];
-            counts[(int64_t)c * E + tid] = mine;
-            mine += n;
+    __shared__ int first[kMaxExperts], all[kMaxExperts];   // next row of each expert in this chunk; its slots
+    const int tid = threadIdx.x, wave = tid >> 6;
+    for (int i = tid; i < 16 * E; i += kPlanRound) cnt[i] = 0;
+    int before_chunk = 0, mine = 0;
+    int e = 0, rank = 0;
+    if (counts) {
+        if (tid < E) first[tid] = all[tid] = 0;
+        __syncthreads();
+        // thread (part, expert): every parts-th chunk
+        const int parts = kPlanRound / E, part = tid / E, ex = tid - part * E;
+        if (part < parts) {
+            int b = 0, a = 0;
+#pragma unroll 8
+            for (int c = part; c < chunks; c += parts) {
+                const int n = counts[(int64_t)c * E + ex];
+                a += n;
+                b += c < (int)blockIdx.x ? n : 0;
+            }
+            atomicAdd(&all[ex], a);
+            atomicAdd(&first[ex], b);
         }
+        __syncthreads();
+        if (tid < E) {
+            mine = all[tid];
+            before_chunk = first[tid];
+        }
+    } else {
+        __syncthreads();
+        e = plan_expert(index, tid, S, E);
+        rank = plan_rank(e, E, bits, cnt);
+        __syncthreads();
+        if (tid < E)
+            for (int w = 0; w < 16; ++w) mine += cnt[w * E + tid];
     }
     int live;
     const int before = block_prefix(mine, scratch, &live);
-    if (tid < E) offsets[tid] = before;
-    if (tid == 0) offsets[E] = live;
-}
-
-__global__ __launch_bounds__(kPlanChunk) void k_plan_write(const int32_t *__restrict__ index, int64_t S, int k, int E,
-                                                           int bits, const int32_t *__restrict__ counts,
-                                                           const int32_t *__restrict__ offsets,
-                                                           int32_t *__restrict__ row_token,
-                                                           int32_t *__restrict__ slot_row) {
-    extern __shared__ uint16_t cnt[];   // [16][E]
-    const int tid = threadIdx.x, wave = tid >> 6;
-    for (int i = tid; i < 16 * E; i += kPlanChunk) cnt[i] = 0;
-    __syncthreads();
-    const int64_t s = (int64_t)blockIdx.x * kPlanChunk + tid;
-    const int e = plan_expert(index, s, S, E);
-    const int rank = plan_rank(e, E, bits, cnt);
-    __syncthreads();
-    if (s >= S) return;
-    int row = -1;
-    if (e < E) {
-        row = offsets[e] + counts[(int64_t)blockIdx.x * E + e] + rank;
-        for (int w = 0; w < wave; ++w) row += cnt[w * E + e];
+    if (tid < E) {
+        first[tid] = before + before_chunk;
+        if (blockIdx.x == 0) offsets[tid] = before;
     }
-    slot_row[s] = row;
-    if (row >= 0) row_token[row] = (int32_t)(s / k);
-    if (s >= offsets[E]) row_token[s] = -1;
+    if (tid == 0 && blockIdx.x == 0) offsets[E] = live;
+    __syncthreads();
+    for (int r = 0; r < rounds; ++r) {
+        const int64_t s = ((int64_t)blockIdx.x * rounds + r) * kPlanRound + tid;
+        if (counts) {
+            e = plan_expert(index, s, S, E);
+            rank = plan_rank(e, E, bits, cnt);
+            __syncthreads();
+        }
+        int row = -1;
+        if (e < E) {
+            row = first[e] + rank;
+            for (int w = 0; w < wave; ++w) row += cnt[w * E + e];
+        }
+        if (s < S) {
+            slot_row[s] = row;
+            if (row >= 0) row_token[row] = (int32_t)(s / k);
+            if (s >= live) row_token[s] = -1;
+        }
+        if (r + 1 < rounds) {
+            __syncthreads();
+            if (tid < E)
+                for (int w = 0; w < 16; ++w) {
+                    first[tid] += cnt[w * E + tid];
+                    cnt[w * E + tid] = 0;
+                }
+            __syncthreads();
+        }
+    }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -384,20 +457,23 @@ int bits_for(int E) {   // bits that tell 0 .. E apart
 template <typename L>
 int32_t router(bool fwd, const void *logits, int T, int E, int k, bool renorm, int32_t *index, float *weight,
                const float *dweight, void *dlogits, hipStream_t st) {
-    const dim3 grid((unsigned)((T + 3) / 4)), block(256);
     const L *lg = static_cast<const L *>(logits);
-    auto run = [&](auto nv) {
-        constexpr int NV = decltype(nv)::value;
+    const bool whole = (int64_t)E * sizeof(L) % 16 == 0;
+    auto run = [&](auto nv, auto group) {
+        constexpr int NV = decltype(nv)::value, G = decltype(group)::value;
+        const dim3 grid((unsigned)((T + 256 / G - 1) / (256 / G))), block(256);
         if (fwd)
-            hipLaunchKernelGGL((k_router_fwd<L, NV>), grid, block, 0, st, lg, T, E, k, (int)renorm, index, weight);
+            hipLaunchKernelGGL((k_router_fwd<L, NV, G>), grid, block, 0, st, lg, T, E, k, (int)renorm, whole, index, weight);
         else
-            hipLaunchKernelGGL((k_router_bwd<L, NV>), grid, block, 0, st, lg, T, E, k, (int)renorm, index, weight,
+            hipLaunchKernelGGL((k_router_bwd<L, NV, G>), grid, block, 0, st, lg, T, E, k, (int)renorm, whole, index, weight,
                                dweight, static_cast<L *>(dlogits));
     };
-    if (E <= 64) run(std::integral_constant<int, 1>{});
-    else if (E <= 128) run(std::integral_constant<int, 2>{});
-    else if (E <= 256) run(std::integral_constant<int, 4>{});
-    else run(std::integral_constant<int, 16>{});
+    using std::integral_constant;
+    if (E > 256) run(integral_constant<int, 16>{}, integral_constant<int, 64>{});
+    else if (k > 16) run(integral_constant<int, 4>{}, integral_constant<int, 64>{});
+    else if (E <= 64) run(integral_constant<int, 4>{}, integral_constant<int, 16>{});
+    else if (E <= 128) run(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+    else run(integral_constant<int, 16>{}, integral_constant<int, 16>{});
     return launched(fwd ? "bsr_router_fwd" : "bsr_router_bwd");
 }
 
@@ -420,28 +496,26 @@ int32_t launch_router_bwd(const void *logits, int32_t type, int T, int E, int k,
                                   : router<uint16_t>(false, logits, T, E, k, renorm, ix, w, dweight, dlogits, st);
 }
 
+static int plan_rounds(int64_t slots) { return (int)((slots + kPlanRound * kPlanChunks - 1) / (kPlanRound * kPlanChunks)); }
+
 size_t expert_plan_workspace_bytes(int64_t slots, int E) {
-    if (slots <= kPlanChunk) return 0;
-    return (size_t)((slots + kPlanChunk - 1) / kPlanChunk) * E * sizeof(int32_t);
+    if (slots <= kPlanRound) return 0;
+    const int64_t chunk = (int64_t)plan_rounds(slots) * kPlanRound;
+    return (size_t)((slots + chunk - 1) / chunk) * E * sizeof(int32_t);
 }
 
 int32_t launch_expert_plan(const int32_t *index, int T, int k, int E, int32_t *offsets, int32_t *row_token,
                            int32_t *slot_row, void *workspace, void *stream) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t S = (int64_t)T * k;
-    const int bits = bits_for(E);
+    const int bits = bits_for(E), rounds = std::max(1, plan_rounds(S));
+    const int chunks = std::max<int>(1, (int)((S + rounds * kPlanRound - 1) / (rounds * kPlanRound)));
     const size_t lds = 16 * (size_t)E * sizeof(uint16_t);
-    if (S <= kPlanChunk) {
-        hipLaunchKernelGGL(k_plan_one, dim3(1), dim3(kPlanChunk), lds, st, index, (int)S, k, E, bits, offsets, row_token,
-                           slot_row);
-        return launched("bsr_expert_plan");
-    }
-    const int chunks = (int)((S + kPlanChunk - 1) / kPlanChunk);
-    int32_t *counts = static_cast<int32_t *>(workspace);
-    hipLaunchKernelGGL(k_plan_count, dim3(chunks), dim3(kPlanChunk), 0, st, index, S, E, counts);
-    hipLaunchKernelGGL(k_plan_first, dim3(1), dim3(kPlanChunk), 0, st, counts, chunks, E, offsets);
-    hipLaunchKernelGGL(k_plan_write, dim3(chunks), dim3(kPlanChunk), lds, st, index, S, k, E, bits, counts, offsets,
-                       row_token, slot_row);
+    int32_t *counts = S <= kPlanRound ? nullptr : static_cast<int32_t *>(workspace);
+    if (counts)
+        hipLaunchKernelGGL(k_plan_count, dim3(chunks), dim3(kPlanRound), 0, st, index, S, E, rounds, counts);
+    hipLaunchKernelGGL(k_plan_write, dim3(chunks), dim3(kPlanRound), lds, st, index, S, k, E, bits, rounds, chunks, counts,
+                       offsets, row_token, slot_row);
     return launched("bsr_expert_plan");
 }
 

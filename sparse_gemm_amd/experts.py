@@ -34,14 +34,17 @@ def device_of(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the stream's handle alone: current_stream() builds an object
+
+
 def call(f, what: str, device: torch.device, *args) -> None:
     """f(*args, current stream of device), with that device current; raises BsrError on a status."""
     index = device.index
-    if index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(index).cuda_stream)
+    if index == torch._C._cuda_getDevice():
+        status = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = f(*args, torch.cuda.current_stream(index).cuda_stream)
+            status = f(*args, _raw_stream(index))
     if status:
         _lib.check(status, what)
 

@@ -35,7 +35,8 @@ def some_logits(T, E, dtype, seed):
 
 
 ROUTES = [(1, 1, 1), (1, 8, 2), (5, 2, 2), (64, 8, 2), (37, 60, 6), (130, 64, 8), (33, 65, 4), (20, 128, 8), (9, 255, 8),
-          (7, 256, 1), (6, 1000, 32), (8, 1024, 16)]
+          (7, 256, 1), (6, 1000, 32), (8, 1024, 16), (19, 64, 17),
+          (21, 200, 32), (100, 120, 16)]
 
 
 @pytest.mark.parametrize("T,E,k", ROUTES)
@@ -97,7 +98,7 @@ def test_router_not_finite(dtype, renorm):
 
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 8, 64), (3, 2, 5), (64, 2, 8), (128, 8, 64), (129, 8, 64), (1024, 1, 3),
-                                   (1025, 1, 1024), (700, 6, 60), (4099, 4, 16), (2500, 32, 1000)])
+                                   (1025, 1, 1024), (700, 6, 60), (4099, 4, 16), (2500, 32, 1000), (33000, 8, 9), (300000, 2, 300)])
 def test_plan(T, k, E):
     say(f"case plan T={T} k={k} E={E}")
     index = torch.randint(-1, E, (T, k), generator=gen(T + k), dtype=torch.int32)
