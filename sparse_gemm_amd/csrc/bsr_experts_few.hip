@@ -1,8 +1,8 @@
 // bsr_experts_few.hip -- the grouped forward for few rows an expert (decode), on bf16 weights
 // (include/bsr_experts.h) and on microscaled 4-bit weights (include/bsr_mx4.h).
 //
-// Bound by the weights' bytes. A work-group owns up to 16 rows of one expert and BN output columns, and
-// streams the BN weight rows in steps of 256 columns (512 bytes of bf16 or 128 bytes of codes a row, whole
+// Bound by the weights' bytes. A work-group owns up to 16 MT rows of one expert and BN output columns, and
+// streams the BN weight rows (or, for the input gradient, 128 bytes of every contraction row) in steps of 256 columns (512 bytes of bf16 or 128 bytes of codes a row, whole
 // cache lines) through a ring of NS LDS stages by direct-to-LDS loads, NS - 1 steps ahead. Its four waves
 // split each step's columns, 64 each, for all BN columns of the output (16 x 16 x 32 products, fp32 sums)
 // and add their sums through LDS at the end, in a fixed order: with the contraction split inside
@@ -30,65 +30,86 @@ struct FewArgs {
     const uint16_t *bias;
     uint16_t *Y;
     const int32_t *offsets, *gather;
-    int T, R, E, N, K;
+    int T, R, E, N, C;   // output columns, contraction length
 };
 
-constexpr int kFewRows = 16;
+// Weights of a tile: bf16 with the contraction contiguous (forward), bf16 with the output columns contiguous
+// (input gradient), 4-bit codes with the contraction contiguous.
+enum Weights { kRowsW, kColsW, kMx4W };
 
-template <bool MX4, int BN, int NS>
+template <Weights W, int MT, int BN, int NS>
 struct FewLayout {
-    static constexpr int kA = kFewRows * 512, kB = MX4 ? BN * 128 : BN * 512, kS = MX4 ? BN * 8 : 0;
-    static constexpr int kStage = kA + kB + kS, kRed = 4 * kFewRows * (BN + 4) * 4;
+    static constexpr int kM = 16 * MT;
+    static constexpr int kA = kM * 512, kB = W == kMx4W ? BN * 128 : BN * 512, kS = W == kMx4W ? BN * 8 : 0;
+    static constexpr int kStage = kA + kB + kS, kRed = 4 * kM * (BN + 4) * 4;
     static constexpr int kLds = NS * kStage > kRed ? NS * kStage : kRed;
-    static constexpr int kALoads = 2, kBLoads = kB / 4096, kLoads = kALoads + kBLoads + (MX4 ? 1 : 0);   // a wave and stage
+    static constexpr int kALoads = 2 * MT, kBLoads = kB / 4096, kLoads = kALoads + kBLoads + (W == kMx4W ? 1 : 0);   // a wave and stage
+    static constexpr int kGroups = kLds <= 80 * 1024 ? 2 : 1;   // work-groups a CU
 };
 
-template <bool MX4, int BN, int NS>
-__global__ __launch_bounds__(256, 2) void k_expert_few(FewArgs g, int ntiles) {
-    using L = FewLayout<MX4, BN, NS>;
-    static_assert(L::kB % 4096 == 0 && (!MX4 || BN == 64), "whole loads a wave; two waves' scale words");
+// kColsW tile: [256 rows][8 chunks of 16 bytes], chunk q of row r at q ^ cswz(r): the 4 rows of a transposing read,
+// and the 8 rows of two of them, fall on different banks.
+__device__ __forceinline__ int cswz(int r) { return (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2); }
+
+template <Weights W, int MT, int BN, int NS>
+__global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_expert_few(FewArgs g, int ntiles) {
+    using L = FewLayout<W, MT, BN, NS>;
+    constexpr bool MX4 = W == kMx4W, COLS = W == kColsW;
+    static_assert(L::kB % 4096 == 0 && (W == kRowsW || BN == 64), "whole loads a wave; whole lines or two waves' scale words");
     constexpr int NT = BN / 16;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[L::kLds];
-    const RowTiles<kFewRows> tiles(g.offsets, g.E, g.R);
+    const RowTiles<L::kM> tiles(g.offsets, g.E, g.R);
     if ((int64_t)blockIdx.x >= (int64_t)tiles.total * ntiles) return;
     const TileOrder o = tile_order(xcd_remap(blockIdx.x, tiles.total * ntiles), tiles.total, ntiles, kRowsTogether);
     const Rows t = tiles.find(o.row);
     if (t.n <= 0) return;
     const bool live = t.e < g.E;
-    const int e = live ? t.e : 0, n0 = o.col * BN, steps = live ? (g.K + 255) / 256 : 0;
+    const int e = live ? t.e : 0, n0 = o.col * BN, steps = live ? (g.C + 255) / 256 : 0;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, gq = lane >> 4;
     const uint32_t base = lds_addr(smem);
 
-    f32x4 acc[NT];
+    f32x4 acc[MT][NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[m][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if (steps > 0) {
-        const int64_t wrow = MX4 ? g.K / 2 : (int64_t)g.K * 2;   // bytes of a weight row
+        const int64_t wrow = MX4 ? g.C / 2 : COLS ? (int64_t)g.N * 2 : (int64_t)g.C * 2;   // bytes of a weight row
+        const int64_t wbytes = wrow * (COLS ? g.C : g.N);
         const int xrows = g.gather ? g.T : g.R;
-        const __amdgpu_buffer_rsrc_t rx = make_rsrc(g.X, (uint32_t)((int64_t)xrows * g.K * 2));
-        const __amdgpu_buffer_rsrc_t rw = make_rsrc(static_cast<const uint8_t *>(g.W) + e * g.N * wrow, (uint32_t)(g.N * wrow));
+        const __amdgpu_buffer_rsrc_t rx =
+            g.gather ? make_rsrc(g.X, (uint32_t)((int64_t)xrows * g.C * 2))
+                     : make_rsrc(g.X + (int64_t)t.at * g.C, (uint32_t)((int64_t)t.n * g.C * 2));   // the tile's own rows
+        const __amdgpu_buffer_rsrc_t rw = make_rsrc(static_cast<const uint8_t *>(g.W) + e * wbytes, (uint32_t)wbytes);
         // Each load: byte offset at step 0 and the number of steps in which its bytes exist.
         uint32_t aoff[L::kALoads], boff[L::kBLoads];
         int alim[L::kALoads], blim[L::kBLoads];
 #pragma unroll
-        for (int j = 0; j < L::kALoads; ++j) {   // 2 rows of 512 bytes a load, chunk q of row r at q ^ r
-            const int r = 2 * (wave + 4 * j) + (lane >> 5), q = (lane & 31) ^ r;
-            const int src = r >= t.n ? -1 : g.gather ? g.gather[t.at + r] : t.at + r;
-            aoff[j] = (uint32_t)src * (uint32_t)g.K * 2u + (uint32_t)q * 16u;
-            alim[j] = (unsigned)src < (unsigned)xrows ? (g.K * 2 - 16 * q + 511) / 512 : 0;
+        for (int j = 0; j < L::kALoads; ++j) {   // 2 rows of 512 bytes a load, chunk q of row r at q ^ (r % 16)
+            const int r = 2 * (wave + 4 * j) + (lane >> 5), q = (lane & 31) ^ (r & 15);
+            const int src = r >= t.n ? -1 : g.gather ? g.gather[t.at + r] : r;
+            aoff[j] = (uint32_t)src * (uint32_t)g.C * 2u + (uint32_t)q * 16u;
+            alim[j] = (unsigned)src < (unsigned)(g.gather ? xrows : t.n) ? (g.C * 2 - 16 * q + 511) / 512 : 0;
         }
 #pragma unroll
         for (int j = 0; j < L::kBLoads; ++j) {
             const int i = wave + 4 * j;
-            const int r = MX4 ? 8 * i + (lane >> 3) : 2 * i + (lane >> 5);
-            const int q = MX4 ? (lane & 7) ^ swz8(r) : (lane & 31) ^ (r & 15);
-            boff[j] = (uint32_t)(n0 + r) * (uint32_t)wrow + (uint32_t)q * 16u;
-            blim[j] = n0 + r >= g.N ? 0 : MX4 ? (g.K / 2 - 16 * q + 127) / 128 : (g.K * 2 - 16 * q + 511) / 512;
+            if constexpr (COLS) {   // 8 contraction rows of 128 bytes a load
+                const int r = 8 * i + (lane >> 3), q = (lane & 7) ^ cswz(r);
+                boff[j] = (uint32_t)r * (uint32_t)wrow + (uint32_t)(n0 + 8 * q) * 2u;
+                blim[j] = n0 + 8 * q < g.N ? (g.C - r + 255) / 256 : 0;
+            } else {
+                const int r = MX4 ? 8 * i + (lane >> 3) : 2 * i + (lane >> 5);
+                const int q = MX4 ? (lane & 7) ^ swz8(r) : (lane & 31) ^ (r & 15);
+                boff[j] = (uint32_t)(n0 + r) * (uint32_t)wrow + (uint32_t)q * 16u;
+                blim[j] = n0 + r >= g.N ? 0 : MX4 ? (g.C / 2 - 16 * q + 127) / 128 : (g.C * 2 - 16 * q + 511) / 512;
+            }
         }
+        const uint32_t bstep = MX4 ? 128u : COLS ? 256u * (uint32_t)wrow : 512u;
         // 4-bit: word h of row 32 w + r (w = wave % 2: two waves load the same words)
-        const int kb = (g.K + 255) / 256, srow = n0 + (wave & 1) * 32 + (lane >> 1);
+        const int kb = (g.C + 255) / 256, srow = n0 + (wave & 1) * 32 + (lane >> 1);
         const __amdgpu_buffer_rsrc_t rs = MX4 ? make_rsrc(g.scales + (int64_t)e * kb * g.N * 8, (uint32_t)((int64_t)kb * g.N * 8)) : rw;
         const uint32_t soff = (uint32_t)srow * 8u + 4u * (lane & 1);
         const int slim = srow < g.N ? steps : 0;
@@ -99,7 +120,7 @@ __global__ __launch_bounds__(256, 2) void k_expert_few(FewArgs g, int ntiles) {
                 dma16(rx, to + (uint32_t)(wave + 4 * j) * 1024u, s < alim[j] ? aoff[j] + (uint32_t)s * 512u : kPast, 0);
 #pragma unroll
             for (int j = 0; j < L::kBLoads; ++j)
-                dma16(rw, to + L::kA + (uint32_t)(wave + 4 * j) * 1024u, s < blim[j] ? boff[j] + (uint32_t)s * (MX4 ? 128u : 512u) : kPast, 0);
+                dma16(rw, to + L::kA + (uint32_t)(wave + 4 * j) * 1024u, s < blim[j] ? boff[j] + (uint32_t)s * bstep : kPast, 0);
             if constexpr (MX4)
                 dma4(rs, to + L::kA + L::kB + (uint32_t)(wave & 1) * 256u, s < slim ? soff + (uint32_t)s * (uint32_t)g.N * 8u : kPast);
         };
@@ -110,58 +131,79 @@ __global__ __launch_bounds__(256, 2) void k_expert_few(FewArgs g, int ntiles) {
             __syncthreads();
             issue(s + NS - 1);   // into the stage of step s - 1, which every wave has read
             const unsigned char *ta = smem + (s % NS) * L::kStage, *tb = ta + L::kA;
-            bf16x8 fa[2];
+            bf16x8 fa[MT][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int q = MX4 ? wave * 8 + 2 * gq + i : wave * 8 + 4 * i + gq;
-                fa[i] = *reinterpret_cast<const bf16x8 *>(ta + r16 * 512 + ((q ^ r16) << 4));
-            }
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int q = MX4 ? wave * 8 + 2 * gq + i : wave * 8 + 4 * i + gq;
+                    fa[m][i] = *reinterpret_cast<const bf16x8 *>(ta + (16 * m + r16) * 512 + ((q ^ r16) << 4));
+                }
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
-                const int r = c * 16 + r16;
+                bf16x8 fb[2];
                 if constexpr (MX4) {
-                    const int q = 2 * wave + (gq >> 1);   // the group
+                    const int r = c * 16 + r16, q = 2 * wave + (gq >> 1);   // the group
                     const uint2 codes = *reinterpret_cast<const uint2 *>(tb + r * 128 + ((q ^ swz8(r)) << 4) + 8 * (gq & 1));
                     uint32_t byte = *(ta + L::kA + L::kB + r * 8 + q);
-                    byte = (s * 8 + q) * 32 < g.K ? byte : 0;   // bytes past K may hold anything
+                    byte = (s * 8 + q) * 32 < g.C ? byte : 0;   // bytes past the contraction may hold anything
                     const float scale = mx4_scale_bits(byte);
-                    acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx4_expand8(codes.x, scale), fa[0], acc[c], 0, 0, 0);
-                    acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx4_expand8(codes.y, scale), fa[1], acc[c], 0, 0, 0);
-                } else {
+                    fb[0] = mx4_expand8(codes.x, scale);
+                    fb[1] = mx4_expand8(codes.y, scale);
+                } else if constexpr (COLS) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int q = wave * 8 + 4 * i + gq;
-                        const bf16x8 fb = *reinterpret_cast<const bf16x8 *>(tb + r * 512 + ((q ^ r16) << 4));
-                        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa[i], acc[c], 0, 0, 0);
+                        const int r = 64 * wave + 32 * i + 8 * gq + (r16 >> 2), col = 16 * c + 4 * (r16 & 3);
+                        auto at = [&](int row) {
+                            return (lds_i16x4 *)(tb + row * 128 + ((((col >> 3) ^ cswz(row)) << 4) | ((col & 7) << 1)));
+                        };
+                        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(r));
+                        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(r + 4));
+                        const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                        fb[i] = __builtin_bit_cast(bf16x8, v);
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        fb[i] = *reinterpret_cast<const bf16x8 *>(tb + (16 * c + r16) * 512 + (((wave * 8 + 4 * i + gq) ^ r16) << 4));
                 }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[i], fa[m][i], acc[m][c], 0, 0, 0);
             }
         }
         wait_vm<0, 0>(0);   // the last loads (of zeros) leave the stages
     }
     __syncthreads();
 
-    // Item v of lane l of acc[c] is column 16 c + 4 (l / 16) + v of row l % 16.
+    // Item v of lane l of acc[m][c] is column 16 c + 4 (l / 16) + v of row 16 m + l % 16.
     float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int c = 0; c < NT; ++c)
-        *reinterpret_cast<f32x4 *>(red + (wave * kFewRows + r16) * (BN + 4) + 16 * c + 4 * gq) = acc[c];
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+            *reinterpret_cast<f32x4 *>(red + (wave * L::kM + 16 * m + r16) * (BN + 4) + 16 * c + 4 * gq) = acc[m][c];
     __syncthreads();
-    const int m = threadIdx.x / (BN / 4), n = (threadIdx.x % (BN / 4)) * 4;
-    if (m < t.n && n0 + n < g.N) {
+    const int n = (threadIdx.x % (BN / 4)) * 4;
+    if (n0 + n >= g.N) return;
+    f32x4 b4 = {0.f, 0.f, 0.f, 0.f};
+    if (live && g.bias) b4 = add_bias4(b4, g.bias + (int64_t)e * g.N + n0 + n);
+    for (int m = threadIdx.x / (BN / 4); m < t.n; m += 1024 / BN) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4 *>(red + (w * kFewRows + m) * (BN + 4) + n);
-        if (live && g.bias) v = add_bias4(v, g.bias + (int64_t)e * g.N + n0 + n);
+        for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4 *>(red + (w * L::kM + m) * (BN + 4) + n);
+        v += b4;
         store4_bf16(g.Y + (int64_t)(t.at + m) * g.N + n0 + n, v[0], v[1], v[2], v[3]);
     }
 }
 
-template <bool MX4, int BN, int NS>
+template <Weights W, int MT, int BN, int NS>
 int32_t launch(const FewArgs &g, void *stream, const char *what) {
-    const int64_t ntiles = (g.N + BN - 1) / BN, blocks = max_row_tiles(g.R, g.E, kFewRows) * ntiles;
+    const int64_t ntiles = (g.N + BN - 1) / BN, blocks = max_row_tiles(g.R, g.E, 16 * MT) * ntiles;
     if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, std::string(what) + ": too many tiles");
-    hipLaunchKernelGGL((k_expert_few<MX4, BN, NS>), dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
+    hipLaunchKernelGGL((k_expert_few<W, MT, BN, NS>), dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
                        g, (int)ntiles);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return fail(BSR_ERR_HIP, std::string(what) + ": " + hipGetErrorString(err));
@@ -170,16 +212,28 @@ int32_t launch(const FewArgs &g, void *stream, const char *what) {
 
 }  // namespace
 
-int32_t launch_expert_fwd_few(const ExpertShape &s, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
+int32_t launch_expert_fwd_few(const ExpertShape &s, int mt, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
                               uint16_t *Y, void *stream) {
-    return launch<false, 32, 3>({X, W, nullptr, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K}, stream,
-                                "bsr_expert_fwd");
+    const FewArgs g{X, W, nullptr, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
+    const char *what = "bsr_expert_fwd";
+    return mt == 1 ? launch<kRowsW, 1, 32, 3>(g, stream, what)
+                   : mt == 2 ? launch<kRowsW, 2, 32, 4>(g, stream, what) : launch<kRowsW, 4, 32, 3>(g, stream, what);
 }
 
-int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, const uint16_t *X, const uint8_t *codes, const uint8_t *scales,
-                                  const uint16_t *bias, uint16_t *Y, void *stream) {
-    return launch<true, 64, 4>({X, codes, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K}, stream,
-                               "bsr_expert_fwd_mx4");
+int32_t launch_expert_bwd_input_few(const ExpertShape &s, int mt, const uint16_t *dY, const uint16_t *W, uint16_t *dX,
+                                    void *stream) {
+    const FewArgs g{dY, W, nullptr, nullptr, dX, s.offsets, nullptr, s.T, s.R, s.E, s.K, s.N};
+    const char *what = "bsr_expert_bwd_input";
+    return mt == 1 ? launch<kColsW, 1, 64, 3>(g, stream, what)
+                   : mt == 2 ? launch<kColsW, 2, 64, 3>(g, stream, what) : launch<kColsW, 4, 64, 2>(g, stream, what);
+}
+
+int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, int mt, const uint16_t *X, const uint8_t *codes,
+                                  const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream) {
+    const FewArgs g{X, codes, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
+    const char *what = "bsr_expert_fwd_mx4";
+    return mt == 1 ? launch<kMx4W, 1, 64, 4>(g, stream, what)
+                   : mt == 2 ? launch<kMx4W, 2, 64, 3>(g, stream, what) : launch<kMx4W, 4, 64, 3>(g, stream, what);
 }
 
 }  // namespace bsr

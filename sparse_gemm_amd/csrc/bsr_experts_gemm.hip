@@ -111,16 +111,12 @@ int32_t launched(const char *what) {
 }
 
 
-// Tile: 256 x 256 with 8 waves where the groups fill it, else 128 x 128 with 4.
-bool wide(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 + 1) * ((cols + 255) / 256) >= 192; }
-
 template <Operand OB>
-int32_t launch_rows(const GemmArgs &g, void *stream, const char *what) {
+int32_t launch_rows(const GemmArgs &g, int64_t bm, void *stream, const char *what) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const bool w = wide(g.R, g.E, g.Nout);
-    const int64_t bm = w ? 256 : 128, ntiles = (g.Nout + bm - 1) / bm, blocks = max_row_tiles(g.R, g.E, bm) * ntiles;
+    const int64_t ntiles = (g.Nout + bm - 1) / bm, blocks = max_row_tiles(g.R, g.E, bm) * ntiles;
     if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, std::string(what) + ": too many tiles");
-    if (w)
+    if (bm == 256)
         hipLaunchKernelGGL((k_expert_rows<OB, 256, 256, 2, 4>), dim3((unsigned)blocks), dim3(512), 0, st, g, (int)ntiles);
     else
         hipLaunchKernelGGL((k_expert_rows<OB, 128, 128, 2, 2>), dim3((unsigned)blocks), dim3(256), 0, st, g, (int)ntiles);
@@ -131,12 +127,16 @@ int32_t launch_rows(const GemmArgs &g, void *stream, const char *what) {
 
 int32_t launch_expert_fwd(const ExpertShape &s, const uint16_t *X, const uint16_t *W, const uint16_t *bias, uint16_t *Y,
                           void *stream) {
-    if (few_rows(s.R, s.E)) return launch_expert_fwd_few(s, X, W, bias, Y, stream);
-    return launch_rows<kRows>({X, W, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K}, stream, "bsr_expert_fwd");
+    const int tile = best_tile(kFwdTiles, s.R, s.E, s.N, s.K);
+    if (tile <= 4) return launch_expert_fwd_few(s, tile, X, W, bias, Y, stream);
+    return launch_rows<kRows>({X, W, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K}, tile, stream,
+                              "bsr_expert_fwd");
 }
 
 int32_t launch_expert_bwd_input(const ExpertShape &s, const uint16_t *dY, const uint16_t *W, uint16_t *dX, void *stream) {
-    return launch_rows<kCols>({dY, W, nullptr, dX, s.offsets, nullptr, s.T, s.R, s.E, s.K, s.N}, stream,
+    const int tile = best_tile(kBwdInputTiles, s.R, s.E, s.K, s.N);
+    if (tile <= 4) return launch_expert_bwd_input_few(s, tile, dY, W, dX, stream);
+    return launch_rows<kCols>({dY, W, nullptr, dX, s.offsets, nullptr, s.T, s.R, s.E, s.K, s.N}, tile, stream,
                               "bsr_expert_bwd_input");
 }
 

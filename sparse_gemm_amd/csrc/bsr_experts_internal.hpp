@@ -2,6 +2,8 @@
 // microscaled 4-bit kernels (include/bsr_mx4.h).
 #pragma once
 
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "bsr_experts.h"
@@ -35,12 +37,54 @@ struct ExpertShape {
 
 int32_t launch_expert_fwd(const ExpertShape &s, const uint16_t *X, const uint16_t *W, const uint16_t *bias, uint16_t *Y,
                           void *stream);
-// Few rows an expert: 16-row tiles that stream the weights.
-inline bool few_rows(int64_t R, int64_t E) { return R <= 24 * E; }
-int32_t launch_expert_fwd_few(const ExpertShape &s, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
+// Which tile a grouped product takes. R rows of E experts are known on the host, the experts' shares are not: the rule
+// takes equal groups and compares the tiles' estimated times, rounds of work-groups * (steps * time of a
+// step + 2 us for a tile's start and end). The times are measured (a product of one expert whose tiles fill the card
+// once or twice, 4096 x 4096 and 4096 -> 14336): `alone` with one work-group a CU, `shared` with `slots` of them on
+// the card. Measured both sides of the rule, us (rows an expert: few-row tiles | 128 x 128):
+//   forward 4096 -> 4096, E = 1     16: 8 | 34    64: 10 | 35    128: 15 | 35    256: 28 | 36    384: 40 | 36
+//   forward 1024 -> 2048, E = 8     16: 9 | 13    32: 12 | 13    48: 13 | 13     64: 22 | 13
+//   forward 4096 -> 14336, E = 8    16: 160 | 166   24: 203 | 196   32: 208 | 169
+//   input gradient of 4096 -> 14336, E = 1   16: 38 | 108    128: 43 | 108    384: 114 | 109
+//   4-bit forward 4096 -> 14336, E = 8       16: 54 | 105    24: 61 | 105     48: 99 | 110     64: 132 | 116
+struct TileKind {
+    int id, rows, cols, step, slots;
+    double alone, shared;
+};
+
+inline double tile_time(const TileKind &k, int64_t R, int64_t E, int64_t cols, int64_t C) {
+    const double groups = (double)std::min(E, R), each = (double)R / groups;
+    const double row_tiles = E == 1 ? std::ceil(each / k.rows) : groups * std::max(1.0, each / k.rows + 0.5);
+    const double tiles = row_tiles * std::ceil((double)cols / k.cols), steps = std::ceil((double)C / k.step);
+    const bool one = tiles <= 256;
+    const double rounds = tiles / (one ? 256 : k.slots);
+    return (rounds <= 2 ? std::ceil(rounds) : rounds) * (steps * (one ? k.alone : k.shared) + 2.0);
+}
+
+template <int n>
+int best_tile(const TileKind (&kinds)[n], int64_t R, int64_t E, int64_t cols, int64_t C) {
+    int best = 0;
+    for (int i = 1; i < n; ++i)
+        if (tile_time(kinds[i], R, E, cols, C) < tile_time(kinds[best], R, E, cols, C)) best = i;
+    return kinds[best].id;
+}
+
+// ids 1, 2, 4: 16 * id-row tiles that stream the weights (bsr_experts_few.hip); 128, 256: the square tiles
+constexpr TileKind kFwdTiles[] = {{1, 16, 32, 256, 512, 0.40, 0.62}, {2, 32, 32, 256, 256, 0.50, 0.50},
+                                  {4, 64, 32, 256, 256, 0.80, 0.84}, {128, 128, 128, 64, 512, 0.52, 1.00},
+                                  {256, 256, 256, 64, 256, 1.55, 1.55}};
+constexpr TileKind kBwdInputTiles[] = {{1, 16, 64, 256, 256, 0.65, 0.65}, {2, 32, 64, 256, 256, 0.75, 0.75},
+                                       {4, 64, 64, 256, 256, 1.05, 1.05}, {128, 128, 128, 64, 512, 0.50, 1.00},
+                                       {256, 256, 256, 64, 256, 1.60, 1.60}};
+constexpr TileKind kFwdMx4Tiles[] = {{1, 16, 64, 256, 512, 0.50, 0.75}, {2, 32, 64, 256, 512, 0.60, 0.90},
+                                     {4, 64, 64, 256, 256, 0.90, 0.90}, {128, 128, 128, 64, 512, 0.56, 1.00}};
+
+int32_t launch_expert_fwd_few(const ExpertShape &s, int mt, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
                               uint16_t *Y, void *stream);
-int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, const uint16_t *X, const uint8_t *codes, const uint8_t *scales,
-                                  const uint16_t *bias, uint16_t *Y, void *stream);
+int32_t launch_expert_bwd_input_few(const ExpertShape &s, int mt, const uint16_t *dY, const uint16_t *W, uint16_t *dX,
+                                    void *stream);
+int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, int mt, const uint16_t *X, const uint8_t *codes,
+                                  const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream);
 int32_t launch_expert_bwd_input(const ExpertShape &s, const uint16_t *dY, const uint16_t *W, uint16_t *dX, void *stream);
 int32_t launch_expert_bwd_weight(const ExpertShape &s, const uint16_t *dY, const uint16_t *X, uint16_t *dW,
                                  uint16_t *dbias, void *stream);

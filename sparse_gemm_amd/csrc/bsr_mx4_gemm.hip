@@ -289,7 +289,8 @@ bool wide(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 
 
 int32_t launch_expert_fwd_mx4(const ExpertShape &s, const uint16_t *X, const uint8_t *codes, const uint8_t *scales,
                               const uint16_t *bias, uint16_t *Y, void *stream) {
-    if (few_rows(s.R, s.E)) return launch_expert_fwd_few_mx4(s, X, codes, scales, bias, Y, stream);
+    const int tile = best_tile(kFwdMx4Tiles, s.R, s.E, s.N, s.K);
+    if (tile <= 4) return launch_expert_fwd_few_mx4(s, tile, X, codes, scales, bias, Y, stream);
     const GemmArgs g{X, codes, nullptr, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
     const int64_t ntiles = (s.N + 127) / 128, blocks = max_row_tiles(s.R, s.E, 128) * ntiles;
     if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, "bsr_expert_fwd_mx4: too many tiles");
