@@ -13,53 +13,79 @@ from . import _lib
 from .binding import lib
 
 _LOGITS = {torch.float32: 0, torch.bfloat16: 1}
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def check(t: torch.Tensor, name: str, shape, dtype, device: torch.device) -> int:
-    """Data pointer of a contiguous tensor of that shape and type on that device; raises otherwise."""
+class _Calls:
+    """The library's functions, each looked up once (the library is loaded on first use)."""
+
+    def __getattr__(self, name):
+        f = getattr(lib(), name)
+        setattr(self, name, f)
+        return f
+
+
+C = _Calls()
+
+# What a call of a few microseconds spends on the host is most of its time. The current stream's handle and the
+# current device come without building objects for them, and outputs from the allocation call that torch's
+# compiled graphs use, where this torch has it.
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    _empty_strided_cuda = None
+
+
+def pointer(t: torch.Tensor, name: str, shape, dtype, device: int) -> int:
+    """Data pointer of a contiguous tensor of that shape and type on GPU `device`; raises otherwise."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def device_of(t: torch.Tensor, name: str) -> torch.device:
+def device_of(t: torch.Tensor, name: str) -> int:
+    """Index of the GPU that t is on; raises if it is on none."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
-    return t.device
+    return t.get_device()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # the stream's handle alone: current_stream() builds an object
+def output(out: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> torch.Tensor:
+    """`out`, checked, or a new tensor of that shape (1 to 4 dimensions) and type."""
+    if out is not None:
+        pointer(out, name, shape, dtype, device)
+        return out
+    if _empty_strided_cuda is None or device != _current_device():
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+    strides = (1,)
+    for n in shape[:0:-1]:
+        strides = (n * strides[0], *strides)
+    return _empty_strided_cuda(shape, strides, dtype)
 
 
-def call(f, what: str, device: torch.device, *args) -> None:
-    """f(*args, current stream of device), with that device current; raises BsrError on a status."""
-    index = device.index
-    if index == torch._C._cuda_getDevice():
-        status = f(*args, _raw_stream(index))
+def call(f, what: str, device: int, *args) -> None:
+    """f(*args, current stream of GPU `device`), with that device current; raises BsrError on a status."""
+    if device == _current_device():
+        status = f(*args, _raw_stream(device))
     else:
-        with torch.cuda.device(index):
-            status = f(*args, _raw_stream(index))
+        with torch.cuda.device(device):
+            status = f(*args, _raw_stream(device))
     if status:
         _lib.check(status, what)
 
 
 def _sizes(t: torch.Tensor, name: str, dims: int) -> torch.Size:
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    return t.shape
-
-
-def _out(out: Optional[torch.Tensor], name: str, shape, dtype, device) -> Tuple[torch.Tensor, int]:
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-        return out, out.data_ptr()
-    return out, check(out, name, shape, dtype, device)
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
+    return shape
 
 
 def router_fwd(logits: torch.Tensor, k: int, renormalize: bool = True, out=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -67,13 +93,15 @@ def router_fwd(logits: torch.Tensor, k: int, renormalize: bool = True, out=None)
     lowest expert, and their softmax weights, over all experts or over the chosen ones, via bsr_router_fwd.
     Experts at -infinity are never chosen: index -1, weight 0."""
     T, E = _sizes(logits, "logits", 2)
-    if logits.dtype not in _LOGITS:
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     d = device_of(logits, "logits")
-    lp = check(logits, "logits", (T, E), logits.dtype, d)
-    index, ip = _out(out[0] if out else None, "index", (T, k), torch.int32, d)
-    weight, wp = _out(out[1] if out else None, "weight", (T, k), torch.float32, d)
-    call(lib().bsr_router_fwd, "bsr_router_fwd", d, lp, _LOGITS[logits.dtype], T, E, k, int(renormalize), ip, wp)
+    lp = pointer(logits, "logits", (T, E), logits.dtype, d)
+    index, weight = out if out else (None, None)
+    index = output(index, "index", (T, k), _I32, d)
+    weight = output(weight, "weight", (T, k), _F32, d)
+    call(C.bsr_router_fwd, "bsr_router_fwd", d, lp, kind, T, E, k, int(renormalize), index.data_ptr(), weight.data_ptr())
     return index, weight
 
 
@@ -82,31 +110,33 @@ def router_bwd(logits: torch.Tensor, index: torch.Tensor, weight: torch.Tensor, 
     """dlogits [T, E] (the logits' type) of router_fwd's weights, via bsr_router_bwd."""
     T, E = _sizes(logits, "logits", 2)
     k = _sizes(index, "index", 2)[1]
-    if logits.dtype not in _LOGITS:
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     d = device_of(logits, "logits")
-    lp = check(logits, "logits", (T, E), logits.dtype, d)
-    ip = check(index, "index", (T, k), torch.int32, d)
-    wp = check(weight, "weight", (T, k), torch.float32, d)
-    gp = check(dweight, "dweight", (T, k), torch.float32, d)
-    out, op = _out(out, "out", (T, E), logits.dtype, d)
-    call(lib().bsr_router_bwd, "bsr_router_bwd", d, lp, _LOGITS[logits.dtype], T, E, k, int(renormalize), ip, wp, gp, op)
+    lp = pointer(logits, "logits", (T, E), logits.dtype, d)
+    ip = pointer(index, "index", (T, k), _I32, d)
+    wp = pointer(weight, "weight", (T, k), _F32, d)
+    gp = pointer(dweight, "dweight", (T, k), _F32, d)
+    out = output(out, "out", (T, E), logits.dtype, d)
+    call(C.bsr_router_bwd, "bsr_router_bwd", d, lp, kind, T, E, k, int(renormalize), ip, wp, gp, out.data_ptr())
     return out
 
 
 class ExpertPlan:
-    """Which rows belong to which expert, on the device: offsets [E+1], row_token [T*k], slot_row [T, k] (int32)."""
+    """Which rows belong to which expert, on the device: offsets [E+1], row_token [T*k], slot_row [T, k] (int32).
+    The three tensors are not to be replaced or moved afterwards (their addresses are kept)."""
 
-    __slots__ = ("offsets", "row_token", "slot_row", "T", "k", "E", "R", "device")
+    __slots__ = ("offsets", "row_token", "slot_row", "T", "k", "E", "R", "device", "_offsets", "_token", "_row")
 
     def __init__(self, offsets: torch.Tensor, row_token: torch.Tensor, slot_row: torch.Tensor):
-        self.T, self.k = _sizes(slot_row, "slot_row", 2)
-        self.R = self.T * self.k
-        self.E = _sizes(offsets, "offsets", 1)[0] - 1
-        self.device = device_of(offsets, "offsets")
-        check(offsets, "offsets", (self.E + 1,), torch.int32, self.device)
-        check(row_token, "row_token", (self.R,), torch.int32, self.device)
-        check(slot_row, "slot_row", (self.T, self.k), torch.int32, self.device)
+        T, k = _sizes(slot_row, "slot_row", 2)
+        E = _sizes(offsets, "offsets", 1)[0] - 1
+        d = device_of(offsets, "offsets")
+        self.T, self.k, self.R, self.E, self.device = T, k, T * k, E, d
+        self._offsets = pointer(offsets, "offsets", (E + 1,), _I32, d)
+        self._token = pointer(row_token, "row_token", (T * k,), _I32, d)
+        self._row = pointer(slot_row, "slot_row", (T, k), _I32, d)
         self.offsets, self.row_token, self.slot_row = offsets, row_token, slot_row
 
     @classmethod
@@ -114,47 +144,44 @@ class ExpertPlan:
         """The plan of index [T, k] int32 (entries outside [0, E) are dropped), via bsr_expert_plan."""
         T, k = _sizes(index, "index", 2)
         d = device_of(index, "index")
-        ip = check(index, "index", (T, k), torch.int32, d)
+        ip = pointer(index, "index", (T, k), _I32, d)
         self = cls.__new__(cls)
         self.T, self.k, self.R, self.E, self.device = T, k, T * k, E, d
-        self.offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=d)
-        self.row_token = torch.empty((self.R,), dtype=torch.int32, device=d)
-        self.slot_row = torch.empty((T, k), dtype=torch.int32, device=d)
-        need = lib().bsr_expert_plan_workspace(T, k, E)
-        ws = torch.empty((need,), dtype=torch.uint8, device=d) if need else None
-        call(lib().bsr_expert_plan, "bsr_expert_plan", d, ip, T, k, E, self.offsets.data_ptr(),
-             self.row_token.data_ptr(), self.slot_row.data_ptr(), ws.data_ptr() if need else None, need)
+        self.offsets = output(None, "offsets", (max(E, 0) + 1,), _I32, d)
+        self.row_token = output(None, "row_token", (T * k,), _I32, d)
+        self.slot_row = output(None, "slot_row", (T, k), _I32, d)
+        self._offsets, self._token, self._row = self.offsets.data_ptr(), self.row_token.data_ptr(), self.slot_row.data_ptr()
+        need = C.bsr_expert_plan_workspace(T, k, E)
+        ws = output(None, "workspace", (need,), torch.uint8, d) if need else None
+        call(C.bsr_expert_plan, "bsr_expert_plan", d, ip, T, k, E, self._offsets, self._token, self._row,
+             ws.data_ptr() if need else None, need)
         return self
-
-
-def rows_of(plan: ExpertPlan, gather: bool) -> int:
-    return plan.T if gather else plan.R
 
 
 def expert_fwd(plan: ExpertPlan, X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
                gather: bool = True, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y [R, N] bf16: row r of expert e is x(r) . W[e]^T + bias[e]; W [E, N, K], bias [E, N] or None, via
     bsr_expert_fwd. gather: X is [T, K] by token; otherwise [R, K], sorted like Y."""
-    E, N, K = _sizes(W, "W", 3)
-    d = plan.device
-    xp = check(X, "X", (rows_of(plan, gather), K), torch.bfloat16, d)
-    wp = check(W, "W", (plan.E, N, K), torch.bfloat16, d)
-    bp = None if bias is None else check(bias, "bias", (E, N), torch.bfloat16, d)
-    out, op = _out(out, "out", (plan.R, N), torch.bfloat16, d)
-    call(lib().bsr_expert_fwd, "bsr_expert_fwd", d, xp, plan.T, plan.R, E, N, K, plan.offsets.data_ptr(),
-         plan.row_token.data_ptr() if gather else None, wp, bp, op)
+    _, N, K = _sizes(W, "W", 3)
+    T, R, E, d = plan.T, plan.R, plan.E, plan.device
+    xp = pointer(X, "X", (T if gather else R, K), _BF16, d)
+    wp = pointer(W, "W", (E, N, K), _BF16, d)
+    bp = None if bias is None else pointer(bias, "bias", (E, N), _BF16, d)
+    out = output(out, "out", (R, N), _BF16, d)
+    call(C.bsr_expert_fwd, "bsr_expert_fwd", d, xp, T, R, E, N, K, plan._offsets, plan._token if gather else None, wp, bp,
+         out.data_ptr())
     return out
 
 
 def expert_bwd_input(plan: ExpertPlan, dY: torch.Tensor, W: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX [R, K] = dY . W[e] by rows sorted like dY [R, N], via bsr_expert_bwd_input. For a gathered X sum a
     token's rows: combine_fwd(plan, dX, None)."""
-    E, N, K = _sizes(W, "W", 3)
-    d = plan.device
-    gp = check(dY, "dY", (plan.R, N), torch.bfloat16, d)
-    wp = check(W, "W", (plan.E, N, K), torch.bfloat16, d)
-    out, op = _out(out, "out", (plan.R, K), torch.bfloat16, d)
-    call(lib().bsr_expert_bwd_input, "bsr_expert_bwd_input", d, gp, plan.R, E, N, K, plan.offsets.data_ptr(), wp, op)
+    _, N, K = _sizes(W, "W", 3)
+    R, E, d = plan.R, plan.E, plan.device
+    gp = pointer(dY, "dY", (R, N), _BF16, d)
+    wp = pointer(W, "W", (E, N, K), _BF16, d)
+    out = output(out, "out", (R, K), _BF16, d)
+    call(C.bsr_expert_bwd_input, "bsr_expert_bwd_input", d, gp, R, E, N, K, plan._offsets, wp, out.data_ptr())
     return out
 
 
@@ -162,13 +189,13 @@ def expert_bwd_weight(plan: ExpertPlan, dY: torch.Tensor, X: torch.Tensor, gathe
                       out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """(dW [E, N, K], dbias [E, N] or None) via bsr_expert_bwd_weight; X and gather as for expert_fwd."""
     N, K = _sizes(dY, "dY", 2)[1], _sizes(X, "X", 2)[1]
-    d = plan.device
-    gp = check(dY, "dY", (plan.R, N), torch.bfloat16, d)
-    xp = check(X, "X", (rows_of(plan, gather), K), torch.bfloat16, d)
-    dW, op = _out(out, "out", (plan.E, N, K), torch.bfloat16, d)
-    db = torch.empty((plan.E, N), dtype=torch.bfloat16, device=d) if want_dbias else None
-    call(lib().bsr_expert_bwd_weight, "bsr_expert_bwd_weight", d, gp, xp, plan.T, plan.R, plan.E, N, K,
-         plan.offsets.data_ptr(), plan.row_token.data_ptr() if gather else None, op, db.data_ptr() if want_dbias else None)
+    T, R, E, d = plan.T, plan.R, plan.E, plan.device
+    gp = pointer(dY, "dY", (R, N), _BF16, d)
+    xp = pointer(X, "X", (T if gather else R, K), _BF16, d)
+    dW = output(out, "out", (E, N, K), _BF16, d)
+    db = output(None, "dbias", (E, N), _BF16, d) if want_dbias else None
+    call(C.bsr_expert_bwd_weight, "bsr_expert_bwd_weight", d, gp, xp, T, R, E, N, K, plan._offsets,
+         plan._token if gather else None, dW.data_ptr(), db.data_ptr() if want_dbias else None)
     return dW, db
 
 
@@ -177,11 +204,11 @@ def combine_fwd(plan: ExpertPlan, Y: torch.Tensor, weight: Optional[torch.Tensor
     """out [T, N] = sum over a token's slots of weight [T, k] (f32; None: 1) times its rows of Y [R, N], via
     bsr_expert_combine_fwd."""
     N = _sizes(Y, "Y", 2)[1]
-    d = plan.device
-    yp = check(Y, "Y", (plan.R, N), torch.bfloat16, d)
-    wp = None if weight is None else check(weight, "weight", (plan.T, plan.k), torch.float32, d)
-    out, op = _out(out, "out", (plan.T, N), torch.bfloat16, d)
-    call(lib().bsr_expert_combine_fwd, "bsr_expert_combine_fwd", d, yp, plan.T, plan.k, N, plan.slot_row.data_ptr(), wp, op)
+    T, k, d = plan.T, plan.k, plan.device
+    yp = pointer(Y, "Y", (plan.R, N), _BF16, d)
+    wp = None if weight is None else pointer(weight, "weight", (T, k), _F32, d)
+    out = output(out, "out", (T, N), _BF16, d)
+    call(C.bsr_expert_combine_fwd, "bsr_expert_combine_fwd", d, yp, T, k, N, plan._row, wp, out.data_ptr())
     return out
 
 
@@ -189,12 +216,12 @@ def combine_bwd(plan: ExpertPlan, dout: torch.Tensor, Y: torch.Tensor,
                 weight: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(dY [R, N] bf16, dweight [T, k] f32) of combine_fwd, via bsr_expert_combine_bwd."""
     N = _sizes(Y, "Y", 2)[1]
-    d = plan.device
-    gp = check(dout, "dout", (plan.T, N), torch.bfloat16, d)
-    yp = check(Y, "Y", (plan.R, N), torch.bfloat16, d)
-    wp = None if weight is None else check(weight, "weight", (plan.T, plan.k), torch.float32, d)
-    dY = torch.empty((plan.R, N), dtype=torch.bfloat16, device=d)
-    dw = torch.empty((plan.T, plan.k), dtype=torch.float32, device=d)
-    call(lib().bsr_expert_combine_bwd, "bsr_expert_combine_bwd", d, gp, yp, plan.T, plan.k, plan.E, N,
-         plan.offsets.data_ptr(), plan.slot_row.data_ptr(), wp, dY.data_ptr(), dw.data_ptr())
+    T, k, R, d = plan.T, plan.k, plan.R, plan.device
+    gp = pointer(dout, "dout", (T, N), _BF16, d)
+    yp = pointer(Y, "Y", (R, N), _BF16, d)
+    wp = None if weight is None else pointer(weight, "weight", (T, k), _F32, d)
+    dY = output(None, "dY", (R, N), _BF16, d)
+    dw = output(None, "dweight", (T, k), _F32, d)
+    call(C.bsr_expert_combine_bwd, "bsr_expert_combine_bwd", d, gp, yp, T, k, plan.E, N, plan._offsets, plan._row, wp,
+         dY.data_ptr(), dw.data_ptr())
     return dY, dw

@@ -6,9 +6,9 @@ from typing import Optional, Union
 
 import torch
 
-from .binding import lib
-from .experts import ExpertPlan, _out, _sizes, call, check, device_of, rows_of
+from .experts import C, ExpertPlan, _sizes, call, device_of, output, pointer
 
+_BF16, _U8 = torch.bfloat16, torch.uint8
 GROUP = 32      # elements that share a scale
 CHUNK = 256     # columns whose 8 scale bytes lie side by side
 
@@ -55,19 +55,20 @@ def quantize(X: torch.Tensor, want_values: bool = False):
         if want_values:
             raise ValueError("want_values needs X of 2 dimensions")
         E, rows, K = X.shape
-        codes = torch.empty((E, rows, K // 2), dtype=torch.uint8, device=d)
-        scales = torch.empty((E, chunks(K), rows, 8), dtype=torch.uint8, device=d)
-        xp = check(X, "X", (E, rows, K), torch.bfloat16, d)
+        xp = pointer(X, "X", (E, rows, K), _BF16, d)
+        codes = output(None, "codes", (E, rows, K // 2), _U8, d)
+        scales = output(None, "scales", (E, chunks(K), rows, 8), _U8, d)
+        cp, sp = codes.data_ptr(), scales.data_ptr()
         for e in range(E):
-            call(lib().bsr_mx4_quantize, "bsr_mx4_quantize", d, xp + e * rows * K * 2, rows, K, codes[e].data_ptr(),
-                 scales[e].data_ptr(), None)
+            call(C.bsr_mx4_quantize, "bsr_mx4_quantize", d, xp + e * rows * K * 2, rows, K, cp + e * rows * (K // 2),
+                 sp + e * chunks(K) * rows * 8, None)
         return Mx4(codes, scales)
     rows, K = _sizes(X, "X", 2)
-    xp = check(X, "X", (rows, K), torch.bfloat16, d)
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=d)
-    scales = torch.empty((chunks(K), rows, 8), dtype=torch.uint8, device=d)
-    values = torch.empty((rows, K), dtype=torch.bfloat16, device=d) if want_values else None
-    call(lib().bsr_mx4_quantize, "bsr_mx4_quantize", d, xp, rows, K, codes.data_ptr(), scales.data_ptr(),
+    xp = pointer(X, "X", (rows, K), _BF16, d)
+    codes = output(None, "codes", (rows, K // 2), _U8, d)
+    scales = output(None, "scales", (chunks(K), rows, 8), _U8, d)
+    values = output(None, "values", (rows, K), _BF16, d) if want_values else None
+    call(C.bsr_mx4_quantize, "bsr_mx4_quantize", d, xp, rows, K, codes.data_ptr(), scales.data_ptr(),
          values.data_ptr() if want_values else None)
     return (Mx4(codes, scales), values) if want_values else Mx4(codes, scales)
 
@@ -79,11 +80,11 @@ def dequantize(q: Mx4) -> torch.Tensor:
     K = 2 * half
     if len(lead) > 1:
         raise ValueError("codes must have 2 or 3 dimensions")
-    cp = check(q.codes, "codes", (*lead, rows, half), torch.uint8, d)
-    sp = check(q.scales, "scales", (*lead, chunks(K), rows, 8), torch.uint8, d)
-    out = torch.empty((*lead, rows, K), dtype=torch.bfloat16, device=d)
+    cp = pointer(q.codes, "codes", (*lead, rows, half), _U8, d)
+    sp = pointer(q.scales, "scales", (*lead, chunks(K), rows, 8), _U8, d)
+    out = output(None, "values", (*lead, rows, K), _BF16, d)
     for e in range(lead[0] if lead else 1):
-        call(lib().bsr_mx4_dequantize, "bsr_mx4_dequantize", d, cp + e * rows * half, sp + e * chunks(K) * rows * 8, rows, K,
+        call(C.bsr_mx4_dequantize, "bsr_mx4_dequantize", d, cp + e * rows * half, sp + e * chunks(K) * rows * 8, rows, K,
              out.data_ptr() + e * rows * K * 2)
     return out
 
@@ -92,19 +93,21 @@ def expert_fwd(plan: ExpertPlan, X: Union[torch.Tensor, Mx4], W: Mx4, bias: Opti
                gather: bool = True, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """experts.expert_fwd with W [E, N, K] in 4 bits: activations in bf16 (bsr_expert_fwd_mx4) or in 4 bits
     (bsr_expert_fwd_mx4_mx4)."""
-    E, N, half = _sizes(W.codes, "W.codes", 3)
-    K, d = 2 * half, plan.device
-    rows = rows_of(plan, gather)
-    cp = check(W.codes, "W.codes", (plan.E, N, half), torch.uint8, d)
-    sp = check(W.scales, "W.scales", (plan.E, chunks(K), N, 8), torch.uint8, d)
-    bp = None if bias is None else check(bias, "bias", (E, N), torch.bfloat16, d)
-    out, op = _out(out, "out", (plan.R, N), torch.bfloat16, d)
-    tail = (plan.T, plan.R, E, N, K, plan.offsets.data_ptr(), plan.row_token.data_ptr() if gather else None, cp, sp, bp, op)
+    _, N, half = _sizes(W.codes, "W.codes", 3)
+    K, T, R, E, d = 2 * half, plan.T, plan.R, plan.E, plan.device
+    rows = T if gather else R
+    cp = pointer(W.codes, "W.codes", (E, N, half), _U8, d)
+    sp = pointer(W.scales, "W.scales", (E, chunks(K), N, 8), _U8, d)
+    bp = None if bias is None else pointer(bias, "bias", (E, N), _BF16, d)
+    out = output(out, "out", (R, N), _BF16, d)
+    token = plan._token if gather else None
     if isinstance(X, Mx4):
-        xc = check(X.codes, "X.codes", (rows, half), torch.uint8, d)
-        xs = check(X.scales, "X.scales", (chunks(K), rows, 8), torch.uint8, d)
-        call(lib().bsr_expert_fwd_mx4_mx4, "bsr_expert_fwd_mx4_mx4", d, xc, xs, *tail)
+        xc = pointer(X.codes, "X.codes", (rows, half), _U8, d)
+        xs = pointer(X.scales, "X.scales", (chunks(K), rows, 8), _U8, d)
+        call(C.bsr_expert_fwd_mx4_mx4, "bsr_expert_fwd_mx4_mx4", d, xc, xs, T, R, E, N, K, plan._offsets, token, cp, sp, bp,
+             out.data_ptr())
     else:
-        xp = check(X, "X", (rows, K), torch.bfloat16, d)
-        call(lib().bsr_expert_fwd_mx4, "bsr_expert_fwd_mx4", d, xp, *tail)
+        xp = pointer(X, "X", (rows, K), _BF16, d)
+        call(C.bsr_expert_fwd_mx4, "bsr_expert_fwd_mx4", d, xp, T, R, E, N, K, plan._offsets, token, cp, sp, bp,
+             out.data_ptr())
     return out
