@@ -22,6 +22,8 @@
 namespace bsr {
 namespace dev {
 
+typedef int i32x8 __attribute__((ext_vector_type(8), aligned(4)));
+
 enum Operand { kRows, kCols };
 
 constexpr uint32_t kPast = 0xF0000000u;   // an offset at or past the end of every operand: such a load reads zeros
@@ -60,7 +62,7 @@ struct Stager {
     const int32_t *gather;
     int gcount, gmax, C;
     uint32_t ld2;
-    int tok[4][kRowsPerLoad > 0 ? kRowsPerLoad : 1];   // tokens of the loads' rows
+    int tok[4 * kRowsPerLoad];   // tokens of this wave's rows
     uint32_t rowoff[4];    // this lane's row offset of load j of the step being issued
 
     __device__ __forceinline__ void init(const Side &s, int C_) {
@@ -73,7 +75,7 @@ struct Stager {
         ld2 = (uint32_t)s.ld * 2u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int i = wave + NW * j;
+            const int i = place(wave, j);
             if constexpr (O == kRows) {
                 const int lr = 8 * i + (lane >> 3), q = (lane & 7) ^ swz8(lr), row = s.at + lr;
                 uint32_t src = (uint32_t)row;
@@ -95,30 +97,42 @@ struct Stager {
         }
         step = O == kRows ? 128u : 64u * ld2;
     }
+    // Which 1 KB of the tile load j of a wave fills. kCols: a wave's four loads take neighbouring rows, so that a gathered
+    // operand's tokens are kWaveRows neighbouring entries of the plan.
+    static constexpr int kWaveRows = 4 * kRowsPerLoad;
+    static __device__ __forceinline__ int place(int wave, int j) { return O == kRows ? wave + NW * j : 4 * wave + j; }
+
     // Rows of a gathered kCols operand: tokens(s) issues scalar loads of step s's entries, which are not waited
     // for; rows(s) turns them into this lane's offsets (rows past C and tokens out of range read zeros).
     __device__ __forceinline__ void tokens(int s) {
         if constexpr (O == kCols) {
             if (!gather) return;   // uniform
-            const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            const int c0 = s * 64 + kWaveRows * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            if (c0 + kWaveRows <= gcount) {   // uniform
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int q = 0; q < kWaveRows / 8; ++q) {
+                    const i32x8 v = ((const __attribute__((address_space(4))) i32x8 *)(uintptr_t)(gather + c0))[q];
 #pragma unroll
-                for (int r = 0; r < kRowsPerLoad; ++r)
-                    tok[j][r] = scalar_load(gather, min(s * 64 + kRowsPerLoad * (wave + NW * j) + r, gcount - 1));
+                    for (int r = 0; r < 8; ++r) tok[8 * q + r] = v[r];
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < kWaveRows; ++r) tok[r] = scalar_load(gather, min(c0 + r, gcount - 1));
+            }
         }
     }
     __device__ __forceinline__ void rows(int s) {
         if constexpr (O == kCols) {
             if (!gather) return;
-            const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            const int lane = threadIdx.x & 63;
+            const int c0 = s * 64 + kWaveRows * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int c0 = s * 64 + kRowsPerLoad * (wave + NW * j);
                 uint32_t v = 0;
 #pragma unroll
                 for (int r = 0; r < kRowsPerLoad; ++r) {
-                    const uint32_t o = c0 + r < C && (unsigned)tok[j][r] < (unsigned)gmax ? (uint32_t)tok[j][r] * ld2 : kPast;
+                    const int i = kRowsPerLoad * j + r;
+                    const uint32_t o = c0 + i < C && (unsigned)tok[i] < (unsigned)gmax ? (uint32_t)tok[i] * ld2 : kPast;
                     v = r == 0 || lane / kRowChunks == r ? o : v;
                 }
                 rowoff[j] = v;
@@ -132,7 +146,7 @@ struct Stager {
         uint32_t o;
         if (O == kCols && gather) o = rowoff[j] + off[j];
         else o = s < lim[j] ? off[j] + (uint32_t)s * step : kPast;
-        dma16(rsrc, m0 + (uint32_t)(wave + NW * j) * 1024u, o, 0);
+        dma16(rsrc, m0 + (uint32_t)place(wave, j) * 1024u, o, 0);
     }
     // Fragment of rows / columns t0 .. t0 + 31 of a staged tile for 16-deep chunk kc.
     static __device__ __forceinline__ bf16x8 frag(const unsigned char *tile, int t0, int kc) {

@@ -120,10 +120,10 @@ __global__ __launch_bounds__(256, 2) void k_mx4_rows(GemmArgs g, int ntiles) {
 // product selects. Two stages a side: the loads of step s + 2 are issued behind the barrier that ends the
 // reads of step s, among the products of its last chunk.
 // ------------------------------------------------------------------------------------------
-typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int codes_x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ i32x8 codes8(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+__device__ __forceinline__ codes_x8 codes8(i32x4 v) { return codes_x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 template <int J>
 __device__ __forceinline__ f32x16 mfma_mx4(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
