@@ -170,43 +170,47 @@ struct Stager {
 
 template <int BM, int BN>
 constexpr int tile_lds() {
-    const int stages = 3 * BM * 128 + 2 * BN * 128, out = BM * (BN * 2 + 16);
+    const int stages = 3 * BM * 128 + 2 * BN * 128, out = BM * BN * 2;
     return stages > out ? stages : out;
 }
 
-// Stores a tile from the waves' accumulators: item v of lane l of acc[r][t] is column n0 + 32 t + 8 (v / 4) +
-// 4 (l / 32) + v % 4 of row m0 + 32 r + l % 32. Bias in fp32, one rounding to bf16, then whole rows from LDS
-// in 16-byte pieces. Row m of out at out + m * ldo; om rows and on (a multiple of 8) columns of it exist.
+// Stores 32 rows x 64 columns of a wave through its 4 KB of LDS: item v of lane l of acc[t] is column 32 t + 8 (v / 4) +
+// 4 (l / 32) + v % 4 of row l % 32. Bias in fp32, one rounding to bf16, then rows of 128 bytes in 16-byte
+// pieces; piece q of row r lies at q ^ (r / 2 % 8), so that 16 rows take different banks.
+__device__ __forceinline__ void store_rows(const f32x16 (&acc)[2], const uint16_t *bias, uint16_t *out, int ldo, int om,
+                                           int on, unsigned char *own) {
+    const int lane = threadIdx.x & 63, r = lane & 31, lh = lane >> 5;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            f32x4 v = quad(acc[t], q);
+            const int n = 32 * t + 8 * q + 4 * lh;
+            if (bias && n < on) v = add_bias4(v, bias + n);
+            store4_bf16(reinterpret_cast<uint16_t *>(own + r * 128 + (((4 * t + q) ^ ((r >> 1) & 7)) << 4) + 8 * lh), v[0], v[1],
+                        v[2], v[3]);
+        }
+    const int q = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = 8 * i + (lane >> 3);
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(own + m * 128 + ((q ^ ((m >> 1) & 7)) << 4));
+        if (m < om && 8 * q < on) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(out + (int64_t)m * ldo + 8 * q));
+    }
+}
+
+// Stores a tile from the waves' accumulators: row m of out at out + m * ldo; om rows and on (a multiple of 8) columns of
+// it exist. Every wave takes its own rows through its own piece of LDS, without waiting for the others.
 template <int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[BM / WM / 32][BN / WN / 32], const uint16_t *bias,
                                            uint16_t *out, int ldo, int om, int on, unsigned char *smem) {
-    constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32, kPitch = BN * 2 + 16;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN);
-    __syncthreads();   // the stages are free for the output tile
+    __syncthreads();   // the stages are free
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int n = n0 + 32 * t + 8 * q + 4 * (lane >> 5);
-            f32x4 b4 = {0.f, 0.f, 0.f, 0.f};
-            if (bias && n < on) b4 = add_bias4(b4, bias + n);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const f32x4 v = quad(acc[r][t], q) + b4;
-                store4_bf16(reinterpret_cast<uint16_t *>(smem + (m0 + 32 * r + (lane & 31)) * kPitch + n * 2), v[0], v[1],
-                            v[2], v[3]);
-            }
-        }
-    __syncthreads();
-    constexpr int kPieces = BN / 8, kRowsOnce = NW * 64 / kPieces;
-    const int piece = threadIdx.x % kPieces;
-    if (piece * 8 < on) {
-        for (int m = threadIdx.x / kPieces; m < min(om, BM); m += kRowsOnce) {
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(smem + m * kPitch + piece * 16);
-            __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(out + (int64_t)m * ldo + piece * 8));
-        }
-    }
+    for (int r = 0; r < BM / WM / 32; ++r)
+        store_rows(acc[r], bias ? bias + n0 : nullptr, out + (int64_t)(m0 + 32 * r) * ldo + n0, ldo, om - m0 - 32 * r,
+                   on - n0, smem + (wave * (BM / WM / 32) + r) * 4096);
 }
 
 // The tile's product and its store. WM x WN waves, each RT x 2 accumulators of 32 x 32.

@@ -33,7 +33,7 @@ struct GemmArgs {
 constexpr int kA = 128 * 128, kB = 128 * 32, kS = 128 * 8, kStage = kA + kB + kS;
 
 __global__ __launch_bounds__(256, 2) void k_mx4_rows(GemmArgs g, int ntiles) {
-    constexpr int BM = 128, BN = 128, out = BM * (BN * 2 + 16);
+    constexpr int BM = 128, BN = 128, out = BM * BN * 2;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[3 * kStage > out ? 3 * kStage : out];
     const RowTiles<BM> tiles(g.offsets, g.E, g.R);
     const int total = tiles.total;
@@ -132,7 +132,7 @@ __device__ __forceinline__ f32x16 mfma_mx4(i32x4 a, i32x4 b, f32x16 c, int sa, i
 
 template <int BM, int BN>
 constexpr int mx4_lds() {
-    const int stages = 2 * (BM + BN) * 136, out = BM * (BN * 2 + 16);
+    const int stages = 2 * (BM + BN) * 136, out = BM * BN * 2;
     return stages > out ? stages : out;
 }
 
