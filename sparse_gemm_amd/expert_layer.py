@@ -84,8 +84,9 @@ class ExpertFFN(nn.Module):
     """y = sum over a token's k experts of weight * down_e(silu(gate_e x) * up_e x).
 
     The router's logits are x . router^T; up holds gate and up weights one after the other ([E, 2 * hidden, dim]).
-    quantize_() replaces the expert weights by their 4-bit form for serving: batches up to `prompt_tokens` tokens then run on
-    bf16 activations, longer ones quantise the activations too."""
+    quantize_() replaces the expert weights by their 4-bit form for serving: batches of up to `prompt_tokens` tokens
+    then keep their activations in bf16, larger ones quantise them too (faster, and less exact: the activations'
+    own rounding to 4 bits)."""
 
     def __init__(self, dim: int, hidden: int, num_experts: int, k: int, renormalize: bool = True, bias: bool = False,
                  prompt_tokens: int = 64, device=None):
@@ -98,7 +99,8 @@ class ExpertFFN(nn.Module):
         self.up, self.down = mk(num_experts, 2 * hidden, dim), mk(num_experts, dim, hidden)
         self.up_bias = mk(num_experts, 2 * hidden) if bias else None
         self.down_bias = mk(num_experts, dim) if bias else None
-        self.up4 = self.down4 = None
+        for name in ("up_codes", "up_scales", "down_codes", "down_scales"):
+            self.register_buffer(name, None)
         self.reset_parameters()
 
     def reset_parameters(self) -> None:
@@ -108,25 +110,37 @@ class ExpertFFN(nn.Module):
                 if p is not None:
                     p.uniform_(-1.0 / math.sqrt(fan), 1.0 / math.sqrt(fan))
 
+    @property
+    def quantized(self) -> bool:
+        return self.up_codes is not None
+
     @torch.no_grad()
     def quantize_(self) -> "ExpertFFN":
         """Hold the expert weights in 4 bits (bsr_mx4_quantize) and drop the bf16 ones; forward only from then on."""
-        self.up4, self.down4 = mx4.quantize(self.up.data), mx4.quantize(self.down.data)
-        self.up = self.down = None
+        if not self.quantized:
+            up, down = mx4.quantize(self.up.data), mx4.quantize(self.down.data)
+            self.up_codes, self.up_scales, self.down_codes, self.down_scales = up.codes, up.scales, down.codes, down.scales
+            self.up = self.down = None
         return self
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if self.quantized and torch.is_grad_enabled() and x.requires_grad:
+            raise RuntimeError("a quantised ExpertFFN has no backward pass")
         lead = x.shape[:-1]
         x = x.reshape(-1, self.dim).to(torch.bfloat16).contiguous()
         index, weight = route(F.linear(x, self.router), self.k, self.renormalize)
         plan = ExpertPlan.from_index(index, self.num_experts)
-        if self.up4 is None:
+        if not self.quantized:
             gate, up = expert_linear(plan, x, self.up, self.up_bias).chunk(2, dim=1)
             y = expert_linear(plan, F.silu(gate) * up, self.down, self.down_bias, gather=False)
             return combine(plan, y, weight).reshape(*lead, self.dim)
-        if torch.is_grad_enabled() and x.requires_grad:
-            raise RuntimeError("a quantised ExpertFFN has no backward pass")
-        prep = mx4.quantize if x.shape[0] > self.prompt_tokens else (lambda t: t)
-        gate, up = mx4.expert_fwd(plan, prep(x), self.up4, self.up_bias).chunk(2, dim=1)
-        y = mx4.expert_fwd(plan, prep((F.silu(gate) * up).contiguous()), self.down4, self.down_bias, gather=False)
+        form = mx4.quantize if x.shape[0] > self.prompt_tokens else (lambda t: t)
+        h = mx4.expert_fwd(plan, form(x), mx4.Mx4(self.up_codes, self.up_scales), self.up_bias)
+        gate, up = h.chunk(2, dim=1)
+        h = form((F.silu(gate) * up).contiguous())
+        y = mx4.expert_fwd(plan, h, mx4.Mx4(self.down_codes, self.down_scales), self.down_bias, gather=False)
         return experts.combine_fwd(plan, y, weight.detach()).reshape(*lead, self.dim)
+
+    def extra_repr(self) -> str:
+        return (f"dim={self.dim}, hidden={self.hidden}, num_experts={self.num_experts}, k={self.k}, "
+                f"bias={self.up_bias is not None}, quantized={self.quantized}")

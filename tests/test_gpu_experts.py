@@ -139,6 +139,9 @@ PRODUCTS = [("ragged", 1, 1, 1, 8, 8), ("ragged", 1, 2, 4, 136, 72), ("ragged", 
             ("dropped", 2050, 2, 3, 512, 512)]
 
 
+# more than 64 experts, rows and columns for 256 x 256 tiles in every direction
+LARGE = [("ragged", 11000, 3, 130, 520, 1032), ("dropped", 10000, 2, 70, 1032, 520), ("dropped", 9000, 1, 2, 712, 2056)]
+
 # enough rows and columns for 256 x 256 tiles: (T, k, E, N, K) of the forward; the input gradient swaps N and K
 WIDE = [("one", 530, 1, 1, 16392, 72), ("ragged", 400, 2, 2, 12296, 200), ("dropped", 700, 2, 3, 16400, 264)]
 
@@ -162,7 +165,7 @@ def product_inputs(kind, T, k, E, N, K, gather, seed=0):
     return p, off, live, X, W, dY, x
 
 
-@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + WIDE)
+@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + LARGE + WIDE)
 @pytest.mark.parametrize("gather", [False, True])
 def test_expert_fwd(kind, T, k, E, N, K, gather):
     say(f"case expert_fwd {kind} T={T} k={k} E={E} N={N} K={K} gather={gather}")
@@ -176,7 +179,7 @@ def test_expert_fwd(kind, T, k, E, N, K, gather):
         assert (f64(y)[live:] == 0).all()
 
 
-@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + [(kind, T, k, E, K, N) for kind, T, k, E, N, K in WIDE])
+@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + LARGE + [(kind, T, k, E, K, N) for kind, T, k, E, N, K in WIDE])
 def test_expert_bwd_input(kind, T, k, E, N, K):
     say(f"case expert_bwd_input {kind} T={T} k={k} E={E} N={N} K={K}")
     p, off, live, _, W, dY, _ = product_inputs(kind, T, k, E, N, K, False)
@@ -188,7 +191,7 @@ def test_expert_bwd_input(kind, T, k, E, N, K):
     near_bf16(dX, Y, S, N)
 
 
-@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + [("ragged", 130, 2, 3, 2056, 2056), ("dropped", 300, 1, 25, 776, 520),
+@pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + LARGE + [("ragged", 130, 2, 3, 2056, 2056), ("dropped", 300, 1, 25, 776, 520),
                                                          ("ragged", 500, 2, 7, 1032, 1544)])
 @pytest.mark.parametrize("gather", [False, True])
 def test_expert_bwd_weight(kind, T, k, E, N, K, gather):

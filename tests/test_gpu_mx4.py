@@ -86,6 +86,7 @@ def test_experts_weights_quantize_like_matrices():
 
 MX_PRODUCTS = [(kind, T, k, E, N, max(32, K // 32 * 32)) for kind, T, k, E, N, K in PRODUCTS] + [
     ("ragged", 3, 2, 4, 1024, 2048), ("one", 20, 1, 2, 72, 1056), ("one", 270, 1, 1, 304, 800), ("ragged", 70, 4, 8, 256, 768),
+    ("ragged", 10000, 2, 70, 1032, 544), ("ragged", 150, 4, 4, 200, 352),
     ("one", 530, 1, 1, 16392, 96), ("ragged", 400, 2, 2, 12296, 288), ("dropped", 700, 2, 3, 16400, 544)]
 
 
