@@ -54,7 +54,10 @@ int32_t bsr_router_fwd(const void *logits, int32_t type, int64_t T, int32_t E, i
 int32_t bsr_router_bwd(const void *logits, int32_t type, int64_t T, int32_t E, int32_t k, int32_t renormalize,
                        const int32_t *index, const float *weight, const float *dweight, void *dlogits, void *stream);
 
-/* Bytes of device workspace that bsr_expert_plan needs (0 for few slots). */
+/* Up to so many slots (T * k) bsr_expert_plan needs no workspace. */
+#define BSR_EXPERT_PLAN_SLOTS 1024
+
+/* Bytes of device workspace that bsr_expert_plan needs (0 up to BSR_EXPERT_PLAN_SLOTS slots). */
 size_t bsr_expert_plan_workspace(int64_t T, int32_t k, int32_t E);
 
 /* The plan of an index: offsets, row_token and slot_row as above, by a stable counting sort on the

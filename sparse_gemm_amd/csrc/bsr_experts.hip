@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256) void k_router_bwd(const L *__restrict__ logits
 // a second one every chunk adds up the counts that it needs by itself; chunks have as many rounds as keep
 // their number within 256, so that this stays a few loads a thread.
 // ------------------------------------------------------------------------------------------
-constexpr int kPlanRound = 1024, kPlanChunks = 256;
+constexpr int kPlanRound = BSR_EXPERT_PLAN_SLOTS, kPlanChunks = 256;
 
 // Counts of this round's waves in cnt[16][E] (16-bit) and this slot's rank among its wave's.
 __device__ __forceinline__ int plan_rank(int e, int E, int bits, uint16_t *cnt) {

@@ -29,12 +29,13 @@ C = _Calls()
 
 # What a call of a few microseconds spends on the host is most of its time. The current stream's handle and the
 # current device come without building objects for them, and outputs from the allocation call that torch's
-# compiled graphs use, where this torch has it.
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# compiled graphs use, where this torch has it (on the current device, shape and strides as tuples).
+raw_stream, current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 try:
-    from torch._C._dynamo.guards import _empty_strided_cuda
+    from torch._C._dynamo.guards import _empty_strided_cuda as empty_strided
 except ImportError:
-    _empty_strided_cuda = None
+    def empty_strided(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
 
 def pointer(t: torch.Tensor, name: str, shape, dtype, device: int) -> int:
@@ -50,38 +51,23 @@ def pointer(t: torch.Tensor, name: str, shape, dtype, device: int) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
-def device_of(t: torch.Tensor, name: str) -> int:
-    """Index of the GPU that t is on; raises if it is on none."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU, got {t.device}")
-    return t.get_device()
+def new2(rows: int, cols: int, dtype) -> torch.Tensor:
+    return empty_strided((rows, cols), (cols, 1), dtype)
 
 
-def output(out: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> torch.Tensor:
-    """`out`, checked, or a new tensor of that shape (1 to 4 dimensions) and type."""
-    if out is not None:
-        pointer(out, name, shape, dtype, device)
-        return out
-    if _empty_strided_cuda is None or device != _current_device():
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
-    strides = (1,)
-    for n in shape[:0:-1]:
-        strides = (n * strides[0], *strides)
-    return _empty_strided_cuda(shape, strides, dtype)
+def new3(n: int, rows: int, cols: int, dtype) -> torch.Tensor:
+    return empty_strided((n, rows, cols), (rows * cols, cols, 1), dtype)
 
 
-def call(f, what: str, device: int, *args) -> None:
-    """f(*args, current stream of GPU `device`), with that device current; raises BsrError on a status."""
-    if device == _current_device():
-        status = f(*args, _raw_stream(device))
-    else:
-        with torch.cuda.device(device):
-            status = f(*args, _raw_stream(device))
-    if status:
-        _lib.check(status, what)
+def elsewhere(f, device: int, *args):
+    """f(*args) with GPU `device` current (every call here starts by asking for that); raises if there is none."""
+    if device < 0:
+        raise ValueError("tensors must be on a GPU")
+    with torch.cuda.device(device):
+        return f(*args)
 
 
-def _sizes(t: torch.Tensor, name: str, dims: int) -> torch.Size:
+def sizes(t: torch.Tensor, name: str, dims: int) -> torch.Size:
     shape = t.shape
     if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
@@ -92,35 +78,53 @@ def router_fwd(logits: torch.Tensor, k: int, renormalize: bool = True, out=None)
     """(index int32 [T, k], weight f32 [T, k]): the k largest of logits [T, E] (f32 or bf16), ties to the
     lowest expert, and their softmax weights, over all experts or over the chosen ones, via bsr_router_fwd.
     Experts at -infinity are never chosen: index -1, weight 0."""
-    T, E = _sizes(logits, "logits", 2)
+    d = logits.get_device()
+    if d < 0 or d != current_device():
+        return elsewhere(router_fwd, d, logits, k, renormalize, out)
+    T, E = sizes(logits, "logits", 2)
     kind = _LOGITS.get(logits.dtype)
     if kind is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    d = device_of(logits, "logits")
     lp = pointer(logits, "logits", (T, E), logits.dtype, d)
-    index, weight = out if out else (None, None)
-    index = output(index, "index", (T, k), _I32, d)
-    weight = output(weight, "weight", (T, k), _F32, d)
-    call(C.bsr_router_fwd, "bsr_router_fwd", d, lp, kind, T, E, k, int(renormalize), index.data_ptr(), weight.data_ptr())
+    if out is None:
+        index, weight = new2(T, k, _I32), new2(T, k, _F32)
+        ip, wp = index.data_ptr(), weight.data_ptr()
+    else:
+        index, weight = out
+        ip, wp = pointer(index, "index", (T, k), _I32, d), pointer(weight, "weight", (T, k), _F32, d)
+    status = C.bsr_router_fwd(lp, kind, T, E, k, renormalize, ip, wp, raw_stream(d))
+    if status:
+        _lib.check(status, "bsr_router_fwd")
     return index, weight
 
 
 def router_bwd(logits: torch.Tensor, index: torch.Tensor, weight: torch.Tensor, dweight: torch.Tensor,
                renormalize: bool = True, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dlogits [T, E] (the logits' type) of router_fwd's weights, via bsr_router_bwd."""
-    T, E = _sizes(logits, "logits", 2)
-    k = _sizes(index, "index", 2)[1]
+    d = logits.get_device()
+    if d < 0 or d != current_device():
+        return elsewhere(router_bwd, d, logits, index, weight, dweight, renormalize, out)
+    T, E = sizes(logits, "logits", 2)
+    k = sizes(index, "index", 2)[1]
     kind = _LOGITS.get(logits.dtype)
     if kind is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    d = device_of(logits, "logits")
     lp = pointer(logits, "logits", (T, E), logits.dtype, d)
     ip = pointer(index, "index", (T, k), _I32, d)
     wp = pointer(weight, "weight", (T, k), _F32, d)
     gp = pointer(dweight, "dweight", (T, k), _F32, d)
-    out = output(out, "out", (T, E), logits.dtype, d)
-    call(C.bsr_router_bwd, "bsr_router_bwd", d, lp, kind, T, E, k, int(renormalize), ip, wp, gp, out.data_ptr())
+    if out is None:
+        out = new2(T, E, logits.dtype)
+        op = out.data_ptr()
+    else:
+        op = pointer(out, "out", (T, E), logits.dtype, d)
+    status = C.bsr_router_bwd(lp, kind, T, E, k, renormalize, ip, wp, gp, op, raw_stream(d))
+    if status:
+        _lib.check(status, "bsr_router_bwd")
     return out
+
+
+PLAN_SLOTS = 1024   # BSR_EXPERT_PLAN_SLOTS: up to here a plan needs no workspace
 
 
 class ExpertPlan:
@@ -130,9 +134,11 @@ class ExpertPlan:
     __slots__ = ("offsets", "row_token", "slot_row", "T", "k", "E", "R", "device", "_offsets", "_token", "_row")
 
     def __init__(self, offsets: torch.Tensor, row_token: torch.Tensor, slot_row: torch.Tensor):
-        T, k = _sizes(slot_row, "slot_row", 2)
-        E = _sizes(offsets, "offsets", 1)[0] - 1
-        d = device_of(offsets, "offsets")
+        d = offsets.get_device()
+        if d < 0:
+            raise ValueError(f"offsets must be on a GPU, got {offsets.device}")
+        T, k = sizes(slot_row, "slot_row", 2)
+        E = sizes(offsets, "offsets", 1)[0] - 1
         self.T, self.k, self.R, self.E, self.device = T, k, T * k, E, d
         self._offsets = pointer(offsets, "offsets", (E + 1,), _I32, d)
         self._token = pointer(row_token, "row_token", (T * k,), _I32, d)
@@ -142,19 +148,25 @@ class ExpertPlan:
     @classmethod
     def from_index(cls, index: torch.Tensor, E: int) -> "ExpertPlan":
         """The plan of index [T, k] int32 (entries outside [0, E) are dropped), via bsr_expert_plan."""
-        T, k = _sizes(index, "index", 2)
-        d = device_of(index, "index")
+        d = index.get_device()
+        if d < 0 or d != current_device():
+            return elsewhere(cls.from_index, d, index, E)
+        T, k = sizes(index, "index", 2)
+        R = T * k
         ip = pointer(index, "index", (T, k), _I32, d)
         self = cls.__new__(cls)
-        self.T, self.k, self.R, self.E, self.device = T, k, T * k, E, d
-        self.offsets = output(None, "offsets", (max(E, 0) + 1,), _I32, d)
-        self.row_token = output(None, "row_token", (T * k,), _I32, d)
-        self.slot_row = output(None, "slot_row", (T, k), _I32, d)
-        self._offsets, self._token, self._row = self.offsets.data_ptr(), self.row_token.data_ptr(), self.slot_row.data_ptr()
-        need = C.bsr_expert_plan_workspace(T, k, E)
-        ws = output(None, "workspace", (need,), torch.uint8, d) if need else None
-        call(C.bsr_expert_plan, "bsr_expert_plan", d, ip, T, k, E, self._offsets, self._token, self._row,
-             ws.data_ptr() if need else None, need)
+        self.T, self.k, self.R, self.E, self.device = T, k, R, E, d
+        self.offsets = o = empty_strided((max(E, 0) + 1,), (1,), _I32)
+        self.row_token = t = empty_strided((R,), (1,), _I32)
+        self.slot_row = s = new2(T, k, _I32)
+        self._offsets, self._token, self._row = op, tp, sp = o.data_ptr(), t.data_ptr(), s.data_ptr()
+        need, ws = 0, None
+        if R > PLAN_SLOTS:
+            need = C.bsr_expert_plan_workspace(T, k, E)
+            ws = empty_strided((need,), (1,), torch.uint8)
+        status = C.bsr_expert_plan(ip, T, k, E, op, tp, sp, None if ws is None else ws.data_ptr(), need, raw_stream(d))
+        if status:
+            _lib.check(status, "bsr_expert_plan")
         return self
 
 
@@ -162,40 +174,60 @@ def expert_fwd(plan: ExpertPlan, X: torch.Tensor, W: torch.Tensor, bias: Optiona
                gather: bool = True, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y [R, N] bf16: row r of expert e is x(r) . W[e]^T + bias[e]; W [E, N, K], bias [E, N] or None, via
     bsr_expert_fwd. gather: X is [T, K] by token; otherwise [R, K], sorted like Y."""
-    _, N, K = _sizes(W, "W", 3)
     T, R, E, d = plan.T, plan.R, plan.E, plan.device
+    if d != current_device():
+        return elsewhere(expert_fwd, d, plan, X, W, bias, gather, out)
+    _, N, K = sizes(W, "W", 3)
     xp = pointer(X, "X", (T if gather else R, K), _BF16, d)
     wp = pointer(W, "W", (E, N, K), _BF16, d)
     bp = None if bias is None else pointer(bias, "bias", (E, N), _BF16, d)
-    out = output(out, "out", (R, N), _BF16, d)
-    call(C.bsr_expert_fwd, "bsr_expert_fwd", d, xp, T, R, E, N, K, plan._offsets, plan._token if gather else None, wp, bp,
-         out.data_ptr())
+    if out is None:
+        out = new2(R, N, _BF16)
+        op = out.data_ptr()
+    else:
+        op = pointer(out, "out", (R, N), _BF16, d)
+    status = C.bsr_expert_fwd(xp, T, R, E, N, K, plan._offsets, plan._token if gather else None, wp, bp, op, raw_stream(d))
+    if status:
+        _lib.check(status, "bsr_expert_fwd")
     return out
 
 
 def expert_bwd_input(plan: ExpertPlan, dY: torch.Tensor, W: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX [R, K] = dY . W[e] by rows sorted like dY [R, N], via bsr_expert_bwd_input. For a gathered X sum a
     token's rows: combine_fwd(plan, dX, None)."""
-    _, N, K = _sizes(W, "W", 3)
     R, E, d = plan.R, plan.E, plan.device
+    if d != current_device():
+        return elsewhere(expert_bwd_input, d, plan, dY, W, out)
+    _, N, K = sizes(W, "W", 3)
     gp = pointer(dY, "dY", (R, N), _BF16, d)
     wp = pointer(W, "W", (E, N, K), _BF16, d)
-    out = output(out, "out", (R, K), _BF16, d)
-    call(C.bsr_expert_bwd_input, "bsr_expert_bwd_input", d, gp, R, E, N, K, plan._offsets, wp, out.data_ptr())
+    if out is None:
+        out = new2(R, K, _BF16)
+        op = out.data_ptr()
+    else:
+        op = pointer(out, "out", (R, K), _BF16, d)
+    status = C.bsr_expert_bwd_input(gp, R, E, N, K, plan._offsets, wp, op, raw_stream(d))
+    if status:
+        _lib.check(status, "bsr_expert_bwd_input")
     return out
 
 
 def expert_bwd_weight(plan: ExpertPlan, dY: torch.Tensor, X: torch.Tensor, gather: bool = True, want_dbias: bool = False,
                       out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """(dW [E, N, K], dbias [E, N] or None) via bsr_expert_bwd_weight; X and gather as for expert_fwd."""
-    N, K = _sizes(dY, "dY", 2)[1], _sizes(X, "X", 2)[1]
     T, R, E, d = plan.T, plan.R, plan.E, plan.device
+    if d != current_device():
+        return elsewhere(expert_bwd_weight, d, plan, dY, X, gather, want_dbias, out)
+    N, K = sizes(dY, "dY", 2)[1], sizes(X, "X", 2)[1]
     gp = pointer(dY, "dY", (R, N), _BF16, d)
     xp = pointer(X, "X", (T if gather else R, K), _BF16, d)
-    dW = output(out, "out", (E, N, K), _BF16, d)
-    db = output(None, "dbias", (E, N), _BF16, d) if want_dbias else None
-    call(C.bsr_expert_bwd_weight, "bsr_expert_bwd_weight", d, gp, xp, T, R, E, N, K, plan._offsets,
-         plan._token if gather else None, dW.data_ptr(), db.data_ptr() if want_dbias else None)
+    dW = new3(E, N, K, _BF16) if out is None else out
+    op = pointer(dW, "out", (E, N, K), _BF16, d)
+    db = new2(E, N, _BF16) if want_dbias else None
+    status = C.bsr_expert_bwd_weight(gp, xp, T, R, E, N, K, plan._offsets, plan._token if gather else None, op,
+                                     db.data_ptr() if want_dbias else None, raw_stream(d))
+    if status:
+        _lib.check(status, "bsr_expert_bwd_weight")
     return dW, db
 
 
@@ -203,25 +235,36 @@ def combine_fwd(plan: ExpertPlan, Y: torch.Tensor, weight: Optional[torch.Tensor
                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [T, N] = sum over a token's slots of weight [T, k] (f32; None: 1) times its rows of Y [R, N], via
     bsr_expert_combine_fwd."""
-    N = _sizes(Y, "Y", 2)[1]
     T, k, d = plan.T, plan.k, plan.device
+    if d != current_device():
+        return elsewhere(combine_fwd, d, plan, Y, weight, out)
+    N = sizes(Y, "Y", 2)[1]
     yp = pointer(Y, "Y", (plan.R, N), _BF16, d)
     wp = None if weight is None else pointer(weight, "weight", (T, k), _F32, d)
-    out = output(out, "out", (T, N), _BF16, d)
-    call(C.bsr_expert_combine_fwd, "bsr_expert_combine_fwd", d, yp, T, k, N, plan._row, wp, out.data_ptr())
+    if out is None:
+        out = new2(T, N, _BF16)
+        op = out.data_ptr()
+    else:
+        op = pointer(out, "out", (T, N), _BF16, d)
+    status = C.bsr_expert_combine_fwd(yp, T, k, N, plan._row, wp, op, raw_stream(d))
+    if status:
+        _lib.check(status, "bsr_expert_combine_fwd")
     return out
 
 
 def combine_bwd(plan: ExpertPlan, dout: torch.Tensor, Y: torch.Tensor,
                 weight: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(dY [R, N] bf16, dweight [T, k] f32) of combine_fwd, via bsr_expert_combine_bwd."""
-    N = _sizes(Y, "Y", 2)[1]
     T, k, R, d = plan.T, plan.k, plan.R, plan.device
+    if d != current_device():
+        return elsewhere(combine_bwd, d, plan, dout, Y, weight)
+    N = sizes(Y, "Y", 2)[1]
     gp = pointer(dout, "dout", (T, N), _BF16, d)
     yp = pointer(Y, "Y", (R, N), _BF16, d)
     wp = None if weight is None else pointer(weight, "weight", (T, k), _F32, d)
-    dY = output(None, "dY", (R, N), _BF16, d)
-    dw = output(None, "dweight", (T, k), _F32, d)
-    call(C.bsr_expert_combine_bwd, "bsr_expert_combine_bwd", d, gp, yp, T, k, plan.E, N, plan._offsets, plan._row, wp,
-         dY.data_ptr(), dw.data_ptr())
+    dY, dw = new2(R, N, _BF16), new2(T, k, _F32)
+    status = C.bsr_expert_combine_bwd(gp, yp, T, k, plan.E, N, plan._offsets, plan._row, wp, dY.data_ptr(), dw.data_ptr(),
+                                      raw_stream(d))
+    if status:
+        _lib.check(status, "bsr_expert_combine_bwd")
     return dY, dw

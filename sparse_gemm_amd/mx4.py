@@ -6,7 +6,8 @@ from typing import Optional, Union
 
 import torch
 
-from .experts import C, ExpertPlan, _sizes, call, device_of, output, pointer
+from . import _lib
+from .experts import C, ExpertPlan, current_device, elsewhere, empty_strided, new2, new3, pointer, raw_stream, sizes
 
 _BF16, _U8 = torch.bfloat16, torch.uint8
 GROUP = 32      # elements that share a scale
@@ -47,45 +48,56 @@ class Mx4:
         return s.reshape(*s.shape[:-2], -1)[..., :self.shape[-1] // GROUP].contiguous()
 
 
+def _quantize(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, values: Optional[torch.Tensor], d: int) -> None:
+    rows, K = X.shape
+    status = C.bsr_mx4_quantize(X.data_ptr(), rows, K, codes.data_ptr(), scales.data_ptr(),
+                                None if values is None else values.data_ptr(), raw_stream(d))
+    if status:
+        _lib.check(status, "bsr_mx4_quantize")
+
+
 def quantize(X: torch.Tensor, want_values: bool = False):
     """Mx4 of X [rows, K] or [E, rows, K] (bf16, K a multiple of 32) via bsr_mx4_quantize. want_values: also the
     bf16 values that the codes stand for (X [rows, K] only), as (Mx4, values)."""
-    d = device_of(X, "X")
+    d = X.get_device()
+    if d < 0 or d != current_device():
+        return elsewhere(quantize, d, X, want_values)
     if X.dim() == 3:
         if want_values:
             raise ValueError("want_values needs X of 2 dimensions")
         E, rows, K = X.shape
-        xp = pointer(X, "X", (E, rows, K), _BF16, d)
-        codes = output(None, "codes", (E, rows, K // 2), _U8, d)
-        scales = output(None, "scales", (E, chunks(K), rows, 8), _U8, d)
-        cp, sp = codes.data_ptr(), scales.data_ptr()
+        pointer(X, "X", (E, rows, K), _BF16, d)
+        c = chunks(K)
+        codes = new3(E, rows, K // 2, _U8)
+        scales = empty_strided((E, c, rows, 8), (c * rows * 8, rows * 8, 8, 1), _U8)
         for e in range(E):
-            call(C.bsr_mx4_quantize, "bsr_mx4_quantize", d, xp + e * rows * K * 2, rows, K, cp + e * rows * (K // 2),
-                 sp + e * chunks(K) * rows * 8, None)
+            _quantize(X[e], codes[e], scales[e], None, d)
         return Mx4(codes, scales)
-    rows, K = _sizes(X, "X", 2)
-    xp = pointer(X, "X", (rows, K), _BF16, d)
-    codes = output(None, "codes", (rows, K // 2), _U8, d)
-    scales = output(None, "scales", (chunks(K), rows, 8), _U8, d)
-    values = output(None, "values", (rows, K), _BF16, d) if want_values else None
-    call(C.bsr_mx4_quantize, "bsr_mx4_quantize", d, xp, rows, K, codes.data_ptr(), scales.data_ptr(),
-         values.data_ptr() if want_values else None)
+    rows, K = sizes(X, "X", 2)
+    pointer(X, "X", (rows, K), _BF16, d)
+    codes, scales = new2(rows, K // 2, _U8), new3(chunks(K), rows, 8, _U8)
+    values = new2(rows, K, _BF16) if want_values else None
+    _quantize(X, codes, scales, values, d)
     return (Mx4(codes, scales), values) if want_values else Mx4(codes, scales)
 
 
 def dequantize(q: Mx4) -> torch.Tensor:
     """The bf16 values of q [rows, K] or [E, rows, K] via bsr_mx4_dequantize."""
-    d = device_of(q.codes, "codes")
+    d = q.codes.get_device()
+    if d < 0 or d != current_device():
+        return elsewhere(dequantize, d, q)
     *lead, rows, half = q.codes.shape
     K = 2 * half
     if len(lead) > 1:
         raise ValueError("codes must have 2 or 3 dimensions")
     cp = pointer(q.codes, "codes", (*lead, rows, half), _U8, d)
     sp = pointer(q.scales, "scales", (*lead, chunks(K), rows, 8), _U8, d)
-    out = output(None, "values", (*lead, rows, K), _BF16, d)
+    out = torch.empty((*lead, rows, K), dtype=_BF16, device=q.codes.device)
     for e in range(lead[0] if lead else 1):
-        call(C.bsr_mx4_dequantize, "bsr_mx4_dequantize", d, cp + e * rows * half, sp + e * chunks(K) * rows * 8, rows, K,
-             out.data_ptr() + e * rows * K * 2)
+        status = C.bsr_mx4_dequantize(cp + e * rows * half, sp + e * chunks(K) * rows * 8, rows, K,
+                                      out.data_ptr() + e * rows * K * 2, raw_stream(d))
+        if status:
+            _lib.check(status, "bsr_mx4_dequantize")
     return out
 
 
@@ -93,21 +105,29 @@ def expert_fwd(plan: ExpertPlan, X: Union[torch.Tensor, Mx4], W: Mx4, bias: Opti
                gather: bool = True, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """experts.expert_fwd with W [E, N, K] in 4 bits: activations in bf16 (bsr_expert_fwd_mx4) or in 4 bits
     (bsr_expert_fwd_mx4_mx4)."""
-    _, N, half = _sizes(W.codes, "W.codes", 3)
-    K, T, R, E, d = 2 * half, plan.T, plan.R, plan.E, plan.device
-    rows = T if gather else R
+    T, R, E, d = plan.T, plan.R, plan.E, plan.device
+    if d != current_device():
+        return elsewhere(expert_fwd, d, plan, X, W, bias, gather, out)
+    _, N, half = sizes(W.codes, "W.codes", 3)
+    K, rows = 2 * half, T if gather else R
     cp = pointer(W.codes, "W.codes", (E, N, half), _U8, d)
     sp = pointer(W.scales, "W.scales", (E, chunks(K), N, 8), _U8, d)
     bp = None if bias is None else pointer(bias, "bias", (E, N), _BF16, d)
-    out = output(out, "out", (R, N), _BF16, d)
+    if out is None:
+        out = new2(R, N, _BF16)
+        op = out.data_ptr()
+    else:
+        op = pointer(out, "out", (R, N), _BF16, d)
     token = plan._token if gather else None
     if isinstance(X, Mx4):
         xc = pointer(X.codes, "X.codes", (rows, half), _U8, d)
         xs = pointer(X.scales, "X.scales", (chunks(K), rows, 8), _U8, d)
-        call(C.bsr_expert_fwd_mx4_mx4, "bsr_expert_fwd_mx4_mx4", d, xc, xs, T, R, E, N, K, plan._offsets, token, cp, sp, bp,
-             out.data_ptr())
+        status = C.bsr_expert_fwd_mx4_mx4(xc, xs, T, R, E, N, K, plan._offsets, token, cp, sp, bp, op, raw_stream(d))
+        what = "bsr_expert_fwd_mx4_mx4"
     else:
         xp = pointer(X, "X", (rows, K), _BF16, d)
-        call(C.bsr_expert_fwd_mx4, "bsr_expert_fwd_mx4", d, xp, T, R, E, N, K, plan._offsets, token, cp, sp, bp,
-             out.data_ptr())
+        status = C.bsr_expert_fwd_mx4(xp, T, R, E, N, K, plan._offsets, token, cp, sp, bp, op, raw_stream(d))
+        what = "bsr_expert_fwd_mx4"
+    if status:
+        _lib.check(status, what)
     return out

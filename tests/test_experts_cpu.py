@@ -42,6 +42,8 @@ def test_other_arguments():
     assert L.bsr_router_fwd(P, 0, 4, 8, 2, 7, P, P, None) == INVALID
     assert L.bsr_router_fwd(P, 0, (1 << 24) + 1, 8, 1, 1, P, P, None) == INVALID
     assert L.bsr_router_bwd(P, 0, 4, 8, 2, 1, P, P, None, P, None) == INVALID
+    assert L.bsr_expert_plan_workspace(experts.PLAN_SLOTS // 2, 2, 16) == 0
+    assert L.bsr_expert_plan_workspace(experts.PLAN_SLOTS // 2 + 1, 2, 16) > 0
     need = L.bsr_expert_plan_workspace(5000, 2, 16)
     assert need > 0 and L.bsr_expert_plan_workspace(100, 2, 16) == 0
     assert L.bsr_expert_plan(P, 5000, 2, 16, P, P, P, P, need - 1, None) == SMALL
