@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <string>
 
 #include "bsr_experts.h"
 #include "bsr_internal.hpp"
@@ -37,6 +38,12 @@ struct ExpertShape {
 
 int32_t launch_expert_fwd(const ExpertShape &s, const uint16_t *X, const uint16_t *W, const uint16_t *bias, uint16_t *Y,
                           void *stream);
+// A grid's threads are counted in 32 bits.
+inline int32_t check_grid(int64_t blocks, int threads, const char *what) {
+    if (blocks * threads > (int64_t)UINT32_MAX) return fail(BSR_ERR_INVALID_ARG, std::string(what) + ": too large for one launch");
+    return BSR_OK;
+}
+
 // Which tile a grouped product takes. R rows of E experts are known on the host, the experts' shares are not: the rule
 // takes equal groups and compares the tiles' estimated times, rounds of work-groups * (steps * time of a
 // step + 2 us for a tile's start and end). The times are measured (a product of one expert whose tiles fill the card

@@ -333,6 +333,7 @@ struct RowTiles {
             total += __builtin_amdgcn_readlane(more.upto, 63);
         }
         total += tiles_of(R - live);
+        total = min(total, (R + min(E + 1, R) * (BM - 1)) / BM);   // what a plan can need, whatever offsets holds
     }
     static __device__ __forceinline__ int tiles_of(int rows) { return (rows + BM - 1) / BM; }
     __device__ __forceinline__ void load(int base) {

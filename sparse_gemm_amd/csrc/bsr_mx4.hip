@@ -1,6 +1,7 @@
 // bsr_mx4.hip -- quantisation to the microscaled 4-bit form and back (include/bsr_mx4.h).
 //
-// Bound by the bytes: 2 read a value, 17/32 written, 2 more for the values that the codes stand for.
+// Bound by the bytes: 2 read a value, 17/32 written, 2 more for the values that the codes stand for. 57344 x 4096 with
+// values: 176 us, 6.0 TB/s (a copy of 2 GiB: 4.9).
 #include <hip/hip_runtime.h>
 
 #include <string>
@@ -69,7 +70,7 @@ int32_t launch_mx4_quantize(const uint16_t *X, int64_t rows, int K, uint8_t *cod
                             void *stream) {
     const int chunks = (K + 255) / 256;
     const int64_t blocks = (rows * chunks + 7) / 8;
-    if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, "bsr_mx4_quantize: too many elements");
+    if (const int32_t bad = check_grid(blocks, 256, "bsr_mx4_quantize")) return bad;
     hipLaunchKernelGGL(k_quantize, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), X, rows, K,
                        chunks, codes, scales, values);
     return launched("bsr_mx4_quantize");
@@ -78,7 +79,7 @@ int32_t launch_mx4_quantize(const uint16_t *X, int64_t rows, int K, uint8_t *cod
 int32_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int K, uint16_t *values,
                               void *stream) {
     const int64_t blocks = (rows * (K / 32) + 255) / 256;
-    if (blocks > INT32_MAX) return fail(BSR_ERR_INVALID_ARG, "bsr_mx4_dequantize: too many elements");
+    if (const int32_t bad = check_grid(blocks, 256, "bsr_mx4_dequantize")) return bad;
     hipLaunchKernelGGL(k_dequantize, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), codes, scales,
                        rows, K, values);
     return launched("bsr_mx4_dequantize");

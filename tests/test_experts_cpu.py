@@ -51,6 +51,7 @@ def test_other_arguments():
     assert L.bsr_expert_combine_fwd(P, 4, 2, 12, P, P, P, None) == INVALID
     assert L.bsr_expert_combine_fwd(P, 4, 2, 64, P, P, P + 4, None) == MISALIGNED
     assert L.bsr_expert_combine_bwd(P, P, 4, 2, 8, 64, P, P, None, P, None, None) == INVALID
+    assert L.bsr_expert_combine_fwd(P, 1 << 24, 1, 1 << 19, P, P, P, None) == INVALID    # more than one launch holds
     assert L.bsr_mx4_quantize(P, 4, 48, P, P, None, None) == INVALID
     assert L.bsr_mx4_quantize(P, -1, 64, P, P, None, None) == INVALID
     assert L.bsr_mx4_quantize(P, 4, 64, P, P + 8, None, None) == MISALIGNED
