@@ -34,7 +34,7 @@ def main(steps: int) -> dict:
         opt.zero_grad()
         loss.backward()
         opt.step()
-        losses.append(float(loss))
+        losses.append(loss.item())
         if step % 5 == 0 or step == steps - 1:
             print(f"step {step}: loss {losses[-1]:.5f}", flush=True)
 

@@ -7,7 +7,7 @@
 // direct-to-LDS loads, NS - 1 steps ahead. Its four waves split each step's contraction, 64 each, for all BN
 // columns of the output (16 x 16 x 32 products, fp32 sums) and add their sums through LDS at the end, in a fixed
 // order: with the contraction split inside the work-group, BN can be small, and a narrow layer still fills the card.
-// 4 tokens, k = 2 of 8 experts, 4096 -> 14336 in 4 bits: 42 us, 5.9 TB/s. 8 tokens, k = 8 of 64, 4096 -> 1536 in bf16:
+// 4 tokens, k = 2 of 8 experts, 4096 -> 14336 in 4 bits: 40 us, 6.2 TB/s. 8 tokens, k = 8 of 64, 4096 -> 1536 in bf16:
 // 75 us, 6.7 TB/s (some weights still cached). One token, k = 2 of 8, 2048 -> 1024 in bf16: 6 us, eight dependent steps.
 //   bf16: lane (r = l % 16, g = l / 16) takes the columns 64 w + 32 i + 8 g + 0 .. 7 of wave w's product i
 //   4-bit: the columns 64 w + 16 g + 8 i + 0 .. 7, so that its 16 codes are 8 neighbouring bytes of one group
@@ -57,7 +57,7 @@ template <Weights W, int MT, int BN, int NS>
 __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_expert_few(FewArgs g, int ntiles) {
     using L = FewLayout<W, MT, BN, NS>;
     constexpr bool MX4 = W == kMx4W, COLS = W == kColsW;
-    static_assert(L::kB % 4096 == 0 && (W == kRowsW || BN == 64), "whole loads a wave; whole lines or two waves' scale words");
+    static_assert(L::kB % 4096 == 0 && (W == kRowsW || BN == 64 || (MX4 && BN == 32)), "whole loads a wave, whole lines");
     constexpr int NT = BN / 16;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[L::kLds];
     const RowTiles<L::kM> tiles(g.offsets, g.E, g.R);
@@ -110,8 +110,8 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
             }
         }
         const uint32_t bstep = MX4 ? 128u : COLS ? 256u * (uint32_t)wrow : 512u;
-        // 4-bit: word h of row 32 w + r (w = wave % 2: two waves load the same words)
-        const int kb = (g.C + 255) / 256, srow = n0 + (wave & 1) * 32 + (lane >> 1);
+        // 4-bit: word h of row 32 w + r (w = wave % (BN / 32): several waves load the same words)
+        const int sw = wave % (BN >= 32 ? BN / 32 : 1), kb = (g.C + 255) / 256, srow = n0 + sw * 32 + (lane >> 1);
         const __amdgpu_buffer_rsrc_t rs = MX4 ? make_rsrc(g.scales + (int64_t)e * kb * g.N * 8, (uint32_t)((int64_t)kb * g.N * 8)) : rw;
         const uint32_t soff = (uint32_t)srow * 8u + 4u * (lane & 1);
         const int slim = srow < g.N ? steps : 0;
@@ -124,16 +124,17 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
             for (int j = 0; j < L::kBLoads; ++j)
                 dma16(rw, to + L::kA + (uint32_t)(wave + 4 * j) * 1024u, s < blim[j] ? boff[j] + (uint32_t)s * bstep : kPast, 0);
             if constexpr (MX4)
-                dma4(rs, to + L::kA + L::kB + (uint32_t)(wave & 1) * 256u, s < slim ? soff + (uint32_t)s * (uint32_t)g.N * 8u : kPast);
+                dma4(rs, to + L::kA + L::kB + (uint32_t)sw * 256u, s < slim ? soff + (uint32_t)s * (uint32_t)g.N * 8u : kPast);
         };
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) issue(s);
         for (int s = 0; s < steps; ++s) {
             wait_vm<(NS - 2) * L::kLoads, (NS - 2) * L::kLoads>(0);   // step s has landed
             __syncthreads();
-            issue(s + NS - 1);   // into the stage of step s - 1, which every wave has read
             const unsigned char *ta = smem + (s % NS) * L::kStage, *tb = ta + L::kA;
-            bf16x8 fa[MT][2];
+            bf16x8 fa[MT][2], fb[NT][2];
+            uint2 codes[MX4 ? NT : 1];
+            uint32_t byte[MX4 ? NT : 1];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -143,15 +144,10 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
                 }
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
-                bf16x8 fb[2];
                 if constexpr (MX4) {
                     const int r = c * 16 + r16, q = 2 * wave + (gq >> 1);   // the group
-                    const uint2 codes = *reinterpret_cast<const uint2 *>(tb + r * 128 + ((q ^ swz8(r)) << 4) + 8 * (gq & 1));
-                    uint32_t byte = *(ta + L::kA + L::kB + r * 8 + q);
-                    byte = (s * 8 + q) * 32 < g.C ? byte : 0;   // bytes past the contraction may hold anything
-                    const float scale = mx4_scale_bits(byte);
-                    fb[0] = mx4_expand8(codes.x, scale);
-                    fb[1] = mx4_expand8(codes.y, scale);
+                    codes[c] = *reinterpret_cast<const uint2 *>(tb + r * 128 + ((q ^ swz8(r)) << 4) + 8 * (gq & 1));
+                    byte[c] = *(ta + L::kA + L::kB + r * 8 + q);
                 } else if constexpr (COLS) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -162,18 +158,27 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
                         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(r));
                         const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(r + 4));
                         const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                        fb[i] = __builtin_bit_cast(bf16x8, v);
+                        fb[c][i] = __builtin_bit_cast(bf16x8, v);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        fb[i] = *reinterpret_cast<const bf16x8 *>(tb + (16 * c + r16) * 512 + (((wave * 8 + 4 * i + gq) ^ r16) << 4));
+                        fb[c][i] = *reinterpret_cast<const bf16x8 *>(tb + (16 * c + r16) * 512 + (((wave * 8 + 4 * i + gq) ^ r16) << 4));
+                }
+            }
+            issue(s + NS - 1);   // while the reads arrive; into the stage of step s - 1, which every wave has read
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                if constexpr (MX4) {   // bytes past the contraction may hold anything
+                    const float scale = mx4_scale_bits((s * 8 + 2 * wave + (gq >> 1)) * 32 < g.C ? byte[c] : 0);
+                    fb[c][0] = mx4_expand8(codes[c].x, scale);
+                    fb[c][1] = mx4_expand8(codes[c].y, scale);
                 }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[i], fa[m][i], acc[m][c], 0, 0, 0);
+                        acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[c][i], fa[m][i], acc[m][c], 0, 0, 0);
             }
         }
         wait_vm<0, 0>(0);   // the last loads (of zeros) leave the stages
@@ -234,6 +239,10 @@ int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, int mt, const uint16_t *
                                   const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream) {
     const FewArgs g{X, codes, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
     const char *what = "bsr_expert_fwd_mx4";
+    // Up to 16 rows a tile: 32 columns while tiles of 64 leave CUs without one. One row, one expert: 4096 -> 4096 7.5 us
+    // against 9.6, 8192 -> 312 of 8 experts 11.4 against 15.6; where they do not, 4 rows of 32 experts, 2048 -> 1024: 11.0
+    // against 8.9.
+    if (mt == 1 && max_row_tiles(s.R, s.E, 16) * ((s.N + 63) / 64) <= kCUs) return launch<kMx4W, 1, 32, 4>(g, stream, what);
     return mt == 1 ? launch<kMx4W, 1, 64, 4>(g, stream, what)
                    : mt == 2 ? launch<kMx4W, 2, 64, 3>(g, stream, what) : launch<kMx4W, 4, 64, 3>(g, stream, what);
 }

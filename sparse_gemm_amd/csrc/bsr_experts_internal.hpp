@@ -83,7 +83,7 @@ constexpr TileKind kFwdTiles[] = {{1, 16, 32, 256, 512, 0.40, 0.62}, {2, 32, 32,
 constexpr TileKind kBwdInputTiles[] = {{1, 16, 64, 256, 256, 0.65, 0.65}, {2, 32, 64, 256, 256, 0.75, 0.75},
                                        {4, 64, 64, 256, 256, 1.05, 1.05}, {128, 128, 128, 64, 512, 0.50, 1.00},
                                        {256, 256, 256, 64, 256, 1.60, 1.60}};
-constexpr TileKind kFwdMx4Tiles[] = {{1, 16, 64, 256, 512, 0.50, 0.75}, {2, 32, 64, 256, 512, 0.60, 0.90},
+constexpr TileKind kFwdMx4Tiles[] = {{1, 16, 64, 256, 512, 0.45, 0.75}, {2, 32, 64, 256, 512, 0.60, 0.90},
                                      {4, 64, 64, 256, 256, 0.90, 0.90}, {128, 128, 128, 64, 512, 0.56, 1.00}};
 
 int32_t launch_expert_fwd_few(const ExpertShape &s, int mt, const uint16_t *X, const uint16_t *W, const uint16_t *bias,

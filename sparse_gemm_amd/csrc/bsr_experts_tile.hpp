@@ -52,7 +52,6 @@ struct Side {
 
 template <Operand O, int BM, int NW>
 struct Stager {
-    static constexpr int kBytes = BM * 128;
     static constexpr int kRowChunks = BM / 8, kRowsPerLoad = 64 / kRowChunks;   // kCols: a row's chunks, rows of one 1 KB load
     __amdgpu_buffer_rsrc_t rsrc;
     uint32_t off[4];       // byte offset of this lane's 16 bytes of load j at step 0

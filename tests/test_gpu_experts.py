@@ -296,6 +296,44 @@ def ffn_reference(m, x, dout):
     return y.detach(), x.grad, {n: q.grad for n, q in P.items()}
 
 
+@pytest.mark.parametrize("T,k,E,N,K", [(30, 2, 4, 72, 40), (700, 2, 3, 264, 136)])
+def test_product_and_sum_gradients_against_differences(T, k, E, N, K):
+    """L = <dout, combine(x W^T + b, w)> in 64 bits, moved by +-h along a random direction of each input, against the
+    gradients' product with that direction. A gradient's elements are off by a few roundings to bf16 (the sum's
+    gradient, the product's, the sum over a token's rows), each at most 2^-8 of what it rounds."""
+    index, p, (off, tok, row) = a_plan("dropped", T, k, E, T)
+    live = int(off[-1])
+    g = gen(5)
+    X, W = torch.randn(T, K, generator=g).bfloat16(), (torch.randn(E, N, K, generator=g) * K ** -0.5).bfloat16()
+    b, w = torch.randn(E, N, generator=g).bfloat16(), torch.rand(T, k, generator=g)
+    dout = torch.randn(T, N, generator=g).bfloat16()
+
+    def loss(X, W, b, w):
+        y, total = np.zeros((T * k, N)), 0.0
+        for e in range(E):
+            r = slice(off[e], off[e + 1])
+            y[r] = X[tok[r]] @ W[e].T + b[e]
+        for j in range(k):
+            t = np.nonzero(row[:, j] >= 0)[0]
+            total += (f64(dout)[t] * w[t, j, None] * y[row[t, j]]).sum()
+        return total
+
+    leaves = [q.to(dev()).requires_grad_() for q in (X, W, b, w)]
+    y = expert_layer.expert_linear(p, leaves[0], leaves[1], leaves[2])
+    expert_layer.combine(p, y, leaves[3]).backward(dout.to(dev()))
+    at = [f64(q) for q in (X, W, b, w)]
+    rng = np.random.default_rng(2)
+    for i, name in enumerate("XWbw"):
+        v, h = rng.standard_normal(at[i].shape), 1e-4
+        up, dn = list(at), list(at)
+        up[i], dn[i] = at[i] + h * v, at[i] - h * v
+        diff = (loss(*up) - loss(*dn)) / (2 * h)
+        grad = f64(leaves[i].grad)
+        say(f"    {name}: difference {diff:.6f}, gradient {(grad * v).sum():.6f}")
+        # 4 roundings of every term of the gradient's product with the direction
+        assert abs((grad * v).sum() - diff) <= 4 * 2.0 ** -8 * np.abs(grad * v).sum() + 1e-6 * abs(diff) + 1e-6
+
+
 @pytest.mark.parametrize("renorm,bias", [(True, False), (False, True)])
 def test_layer_forward_and_gradients(renorm, bias):
     """Each step rounds to bf16 (2^-8): up, silu * up, down, sum, and as many on the way back. The 2-norm of the
@@ -382,3 +420,14 @@ def test_refusals():
         experts.combine_fwd(p, bf(7, 64))
     with pytest.raises(ValueError):
         experts.expert_fwd(p, bf(4, 64), bf(3, 64, 64), out=bf(8, 32))
+
+
+def test_layer_without_tokens():
+    m = expert_layer.ExpertFFN(64, 64, 4, 2, device=dev())
+    x = torch.zeros(0, 64, device=dev(), dtype=torch.bfloat16, requires_grad=True)
+    y = m(x)
+    assert y.shape == (0, 64)
+    y.sum().backward()
+    assert x.grad.shape == (0, 64)
+    for name in ("router", "up", "down"):
+        assert not getattr(m, name).grad.any(), name

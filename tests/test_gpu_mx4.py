@@ -187,3 +187,17 @@ def test_refusals():
         mx4.expert_fwd(p, bf(4, 64), mx4.quantize(bf(2, 12, 64)))
     with pytest.raises(ValueError):
         Mx4.from_rows(W.codes[0], torch.zeros((64, 3), dtype=torch.uint8, device=d))
+
+
+def test_layer_in_4_bits_keeps_its_weights_in_the_state():
+    """A quantised layer's state loads into another quantised layer, and moves with it."""
+    torch.manual_seed(3)
+    a = expert_layer.ExpertFFN(64, 64, 4, 2, device=dev()).quantize_()
+    b = expert_layer.ExpertFFN(64, 64, 4, 2, device=dev()).quantize_()
+    assert a.quantize_() is a
+    x = torch.randn(9, 64, device=dev()).bfloat16()
+    with torch.no_grad():
+        assert not torch.equal(a(x), b(x))
+        b.load_state_dict(a.state_dict())
+        assert torch.equal(a(x), b(x))
+        assert a(x[:0]).shape == (0, 64)
