@@ -3,7 +3,7 @@
 //
 // Bound by the weights' bytes. A work-group owns up to 16 MT rows of one expert and BN output columns, and
 // streams the BN weight rows in steps of 256 columns (512 bytes of bf16 or 128 bytes of codes a row; for the input
-// gradient 128 bytes of 256 weight rows: whole cache lines in each case) through a ring of NS LDS stages by
+// gradient 2 BN bytes of 256 weight rows: whole cache lines in most cases) through a ring of NS LDS stages by
 // direct-to-LDS loads, NS - 1 steps ahead. Its four waves split each step's contraction, 64 each, for all BN
 // columns of the output (16 x 16 x 32 products, fp32 sums) and add their sums through LDS at the end, in a fixed
 // order: with the contraction split inside the work-group, BN can be small, and a narrow layer still fills the card.
@@ -49,15 +49,18 @@ struct FewLayout {
     static constexpr int kGroups = kLds <= 80 * 1024 ? 2 : 1;   // work-groups a CU
 };
 
-// kColsW tile: [256 rows][8 chunks of 16 bytes], chunk q of row r at q ^ cswz(r): the 4 rows of a transposing read,
-// and the 8 rows of two of them, fall on different banks.
-__device__ __forceinline__ int cswz(int r) { return (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2); }
+// kColsW tile: [256 rows][BN / 8 chunks of 16 bytes], chunk q of row r at q ^ cswz(r): the 4 rows of a transposing
+// read, and the 8 rows of two of them, fall on different banks.
+template <int BN>
+__device__ __forceinline__ int cswz(int r) {
+    return BN == 64 ? (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2) : ((r >> 3) & 1) << 1;
+}
 
 template <Weights W, int MT, int BN, int NS>
 __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_expert_few(FewArgs g, int ntiles) {
     using L = FewLayout<W, MT, BN, NS>;
     constexpr bool MX4 = W == kMx4W, COLS = W == kColsW;
-    static_assert(L::kB % 4096 == 0 && (W == kRowsW || BN == 64 || (MX4 && BN == 32)), "whole loads a wave, whole lines");
+    static_assert(L::kB % 4096 == 0 && (W == kRowsW || BN == 64 || BN == 32), "whole loads a wave");
     constexpr int NT = BN / 16;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[L::kLds];
     const RowTiles<L::kM> tiles(g.offsets, g.E, g.R);
@@ -98,8 +101,8 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
 #pragma unroll
         for (int j = 0; j < L::kBLoads; ++j) {
             const int i = wave + 4 * j;
-            if constexpr (COLS) {   // 8 contraction rows of 128 bytes a load
-                const int r = 8 * i + (lane >> 3), q = (lane & 7) ^ cswz(r);
+            if constexpr (COLS) {   // 512 / BN contraction rows a load
+                const int r = (512 / BN) * i + lane / (BN / 8), q = (lane % (BN / 8)) ^ cswz<BN>(r);
                 boff[j] = (uint32_t)r * (uint32_t)wrow + (uint32_t)(n0 + 8 * q) * 2u;
                 blim[j] = n0 + 8 * q < g.N ? (g.C - r + 255) / 256 : 0;
             } else {
@@ -153,7 +156,7 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
                     for (int i = 0; i < 2; ++i) {
                         const int r = 64 * wave + 32 * i + 8 * gq + (r16 >> 2), col = 16 * c + 4 * (r16 & 3);
                         auto at = [&](int row) {
-                            return (lds_i16x4 *)(tb + row * 128 + ((((col >> 3) ^ cswz(row)) << 4) | ((col & 7) << 1)));
+                            return (lds_i16x4 *)(tb + row * (2 * BN) + ((((col >> 3) ^ cswz<BN>(row)) << 4) | ((col & 7) << 1)));
                         };
                         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(r));
                         const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(r + 4));
@@ -231,6 +234,12 @@ int32_t launch_expert_bwd_input_few(const ExpertShape &s, int mt, const uint16_t
                                     void *stream) {
     const FewArgs g{dY, W, nullptr, nullptr, dX, s.offsets, nullptr, s.T, s.R, s.E, s.K, s.N};
     const char *what = "bsr_expert_bwd_input";
+    // 32 columns a tile (half lines, two work-groups a CU) while tiles of 64 leave half of the CUs without one: one row of
+    // 8 experts, 10744 -> 312: 23 us against 31, one expert, 4096 -> 4096: 10 against 12; where they do not, 4 rows of 64
+    // experts, 1536 -> 2048: 92 against 80.
+    const bool narrow = max_row_tiles(s.R, s.E, 16 * mt) * ((s.K + 63) / 64) <= kCUs / 2;
+    if (narrow && mt == 1) return launch<kColsW, 1, 32, 3>(g, stream, what);
+    if (narrow && mt == 2) return launch<kColsW, 2, 32, 3>(g, stream, what);
     return mt == 1 ? launch<kColsW, 1, 64, 3>(g, stream, what)
                    : mt == 2 ? launch<kColsW, 2, 64, 3>(g, stream, what) : launch<kColsW, 4, 64, 2>(g, stream, what);
 }
