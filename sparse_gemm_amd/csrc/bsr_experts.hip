@@ -380,8 +380,8 @@ __global__ __launch_bounds__(kPlanRound) void k_plan_write(const int32_t *__rest
 
 // ------------------------------------------------------------------------------------------
 // The sum over a token's rows and its gradient: 8 columns a thread, so that a wave takes 1 KB of a row. 8191 tokens, k = 8,
-// N = 2048: forward 80 us (302 MB, 3.8 TB/s: rows from all over Y), backward, one wave a slot, 99 us (570 MB, 5.8 TB/s;
-// much of Y is still in the last-level cache when it follows the forward).
+// N = 2048: forward 55 us (302 MB, 5.5 TB/s; 75 us behind other work, with nothing of Y in the last-level cache), backward, one
+// wave a slot, 113 us (570 MB, 5.0 TB/s; 99 behind the forward, which leaves Y there).
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void unpack8(u32x4 v, float *f) {
 #pragma unroll
@@ -397,33 +397,48 @@ __device__ __forceinline__ u32x4 pack8(const float *f) {
     return v;
 }
 
+// One wave takes 512 columns of a token, so that its rows and weights are scalars; a row behind a descriptor of its own,
+// of no bytes where the slot has no row: that load reads zeros without a branch, and Rows rows are in flight. The waves of a
+// row follow one another (with all first pieces first: 70 us instead of 55). Rows covers k up to 8; 8 of them
+// for k = 2 (16384 tokens, N = 4096): 78 us instead of 74.
+constexpr int kCombineTokens = 1 << 14;   // tokens of one slice of the grid (blockIdx.y): its threads fit 32 bits for every N
+
+template <int Rows>
 __global__ __launch_bounds__(256) void k_combine_fwd(const uint16_t *__restrict__ Y, int T, int k, int N, int R,
                                                      const int32_t *__restrict__ slot_row,
-                                                     const float *__restrict__ weight, uint16_t *__restrict__ out) {
-    const int n8 = N >> 3;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)T * n8) return;
-    const int t = (int)(i / n8), c = (int)(i % n8);
+                                                     const float *__restrict__ weight, uint16_t *__restrict__ out,
+                                                     uint32_t pieces) {
+    const uint32_t id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = (int)blockIdx.y * kCombineTokens + (int)(id / pieces);
+    const int c = (int)(id % pieces) * 512 + (int)(threadIdx.x & 63) * 8;
+    if (t >= T) return;
+    const int64_t s0 = (int64_t)t * k;
     float acc[8] = {};
-    for (int j0 = 0; j0 < k; j0 += 8) {   // up to 8 rows in flight
-        int row[8];
-        u32x4 y[8];
+    for (int j0 = 0; j0 < k; j0 += Rows) {
+        // lane j % Rows looks at slot j0 + j
+        const int64_t s = s0 + min(j0 + (int)(threadIdx.x & (Rows - 1)), k - 1);
+        const int r = slot_row[s];
+        const float wr = weight ? weight[s] : 1.f;
+        const bool there = j0 + (int)(threadIdx.x & (Rows - 1)) < k && (unsigned)r < (unsigned)R;
+        const int rows = there ? r : -1;
+        const float ws = there ? wr : 0.f;
+        u32x4 y[Rows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) row[j] = j0 + j < k ? slot_row[(int64_t)t * k + j0 + j] : -1;
+        for (int j = 0; j < Rows; ++j) {
+            const int row = __builtin_amdgcn_readlane(rows, j);
+            y[j] = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(Y + (int64_t)max(row, 0) * N, row < 0 ? 0u : (uint32_t)N * 2u),
+                                                         (uint32_t)c * 2u, 0, 0);
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if ((unsigned)row[j] < (unsigned)R) y[j] = *reinterpret_cast<const u32x4 *>(Y + (int64_t)row[j] * N + c * 8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if ((unsigned)row[j] >= (unsigned)R) continue;
-            const float w = weight ? weight[(int64_t)t * k + j0 + j] : 1.f;
+        for (int j = 0; j < Rows; ++j) {
+            const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(ws), j));
             float f[8];
             unpack8(y[j], f);
 #pragma unroll
             for (int v = 0; v < 8; ++v) acc[v] += w * f[v];
         }
     }
-    *reinterpret_cast<u32x4 *>(out + (int64_t)t * N + c * 8) = pack8(acc);
+    if (c < N) *reinterpret_cast<u32x4 *>(out + (int64_t)t * N + c) = pack8(acc);
 }
 
 __global__ __launch_bounds__(256) void k_combine_bwd(const uint16_t *__restrict__ dout, const uint16_t *__restrict__ Y,
@@ -536,10 +551,12 @@ int32_t launch_expert_plan(const int32_t *index, int T, int k, int E, int32_t *o
 
 int32_t launch_combine_fwd(const uint16_t *Y, int T, int k, int N, const int32_t *slot_row, const float *weight,
                            uint16_t *out, void *stream) {
-    const int64_t blocks = ((int64_t)T * (N / 8) + 255) / 256;
-    if (const int32_t bad = check_grid(blocks, 256, "bsr_expert_combine_fwd")) return bad;
-    hipLaunchKernelGGL(k_combine_fwd, dim3((unsigned)blocks), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), Y, T, k, N, T * k, slot_row, weight, out);
+    const int pieces = (N + 511) / 512;
+    const dim3 grid((unsigned)((std::min(T, kCombineTokens) * pieces + 3) / 4),
+                    (unsigned)((T + kCombineTokens - 1) / kCombineTokens));
+    hipLaunchKernelGGL(k <= 2 ? k_combine_fwd<2> : k <= 4 ? k_combine_fwd<4> : k_combine_fwd<8>, grid, dim3(256), 0,
+                       static_cast<hipStream_t>(stream), Y, T, k, N, T * k, slot_row, weight, out,
+                       (uint32_t)pieces);
     return launched("bsr_expert_combine_fwd");
 }
 

@@ -226,7 +226,7 @@ def test_products_without_tokens():
 
 @pytest.mark.parametrize("kind,T,k,E,N", [("ragged", 1, 1, 2, 8), ("ragged", 7, 2, 4, 72), ("dropped", 50, 3, 6, 520),
                                           ("none", 4, 2, 3, 16), ("ragged", 33, 8, 64, 4104), ("dropped", 130, 32, 40, 264),
-                                          ("one", 300, 1, 2, 2048)])
+                                          ("one", 300, 1, 2, 2048), ("dropped", 40000, 2, 8, 16)])
 def test_combine(kind, T, k, E, N):
     say(f"case combine {kind} T={T} k={k} E={E} N={N}")
     index, p, (off, tok, row) = a_plan(kind, T, k, E, T)
