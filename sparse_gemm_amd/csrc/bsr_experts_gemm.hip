@@ -10,7 +10,7 @@
 // experts, 4096 -> 11008: 2.49 ms, 1.19 PFLOP/s; one dense 16384 x 4096 -> 4096: 423 us, 1.30 PFLOP/s (the matrix
 // instructions alone, on random data: 1.88). Measured there: matrix cores busy 67% of the time at 1.8 GHz; without the loads in
 // the loop 76% at 2.2 GHz, so the 64 KB a step through L2 cost both stalls and clock. Gradients of 8192 tokens, k = 2 of 8, 4096 -> 4096:
-// input 525 us (1.05 PFLOP/s), weight 517 us (1.06). Ragged groups cost partly empty tiles and the last round of tiles.
+// input 525 us (1.05 PFLOP/s), weight 475 us (1.16). Ragged groups cost partly empty tiles and the last round of tiles.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -55,9 +55,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_rows(GemmArgs g, int 
 
 // Weight gradient: one BM x BN tile of one expert's dW a work-group, over all rows of the expert. Every XCD takes an eighth
 // of every expert's tiles: the experts' row counts differ, and whole experts a XCD would leave some of them idle (64
-// narrow experts, 16396 rows, dW 1000 x 2048: 272 -> 155 us together with token loads a step ahead; now 145 us, at least 54 of
+// narrow experts, 16396 rows, dW 1000 x 2048: 272 -> 155 us together with token loads a step ahead; now 127 us, at least 54 of
 // them for the 262 MB of dW).
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, bool Gathered>
 __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_weight(const uint16_t *__restrict__ dY, const uint16_t *__restrict__ X,
                                                                const int32_t *__restrict__ offsets,
                                                                const int32_t *__restrict__ gather, int T, int R, int N,
@@ -69,10 +69,10 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_weight(const uint16_t
     const TileOrder o = tile_order(tile, mtiles, ntiles, kRowsTogether);
     const int lo = clamp_row(scalar_load(offsets, e), R), n = max(clamp_row(scalar_load(offsets, e + 1), R) - lo, 0);
     const Side a{dY + (int64_t)lo * N, (uint32_t)((int64_t)n * N * 2), N, o.row * BM, N, nullptr, 0, 0};
-    const Side b = gather ? Side{X, (uint32_t)((int64_t)T * K * 2), K, o.col * BN, K, gather + lo, R - lo, T}
-                          : Side{X + (int64_t)lo * K, (uint32_t)((int64_t)n * K * 2), K, o.col * BN, K, nullptr, 0, 0};
-    tile_product<kCols, kCols, BM, BN, WM, WN>(a, b, n, nullptr, dW + ((int64_t)e * N + o.row * BM) * K + o.col * BN, K,
-                                               N - o.row * BM, K - o.col * BN, smem);
+    const Side b = Gathered ? Side{X, (uint32_t)((int64_t)T * K * 2), K, o.col * BN, K, gather + lo, R - lo, T}
+                            : Side{X + (int64_t)lo * K, (uint32_t)((int64_t)n * K * 2), K, o.col * BN, K, nullptr, 0, 0};
+    tile_product<kCols, kCols, BM, BN, WM, WN, Gathered>(a, b, n, nullptr, dW + ((int64_t)e * N + o.row * BM) * K + o.col * BN,
+                                                         K, N - o.row * BM, K - o.col * BN, smem);
 }
 
 // Bias gradient: 64 columns (whole cache lines) of one expert a work-group, 8 columns a thread and 128 threads over
@@ -159,8 +159,10 @@ int32_t launch_expert_bwd_weight(const ExpertShape &s, const uint16_t *dY, const
         hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(w ? 512 : 256), 0, st, dY, X, s.offsets, s.row_token, s.T,
                            s.R, s.N, s.K, dW, (int)mt, (int)nt);
     };
-    if (w) run(k_expert_weight<256, 256, 2, 4>);
-    else run(k_expert_weight<128, 128, 2, 2>);
+    if (w && s.row_token) run(k_expert_weight<256, 256, 2, 4, true>);
+    else if (w) run(k_expert_weight<256, 256, 2, 4, false>);
+    else if (s.row_token) run(k_expert_weight<128, 128, 2, 2, true>);
+    else run(k_expert_weight<128, 128, 2, 2, false>);
     if (dbias)
         hipLaunchKernelGGL(k_expert_bias, dim3((unsigned)((s.N + 63) / 64), (unsigned)s.E), dim3(8 * kBiasRows), 0, st, dY,
                            s.offsets, s.R, s.N, dbias);

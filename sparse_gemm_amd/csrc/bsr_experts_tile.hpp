@@ -50,7 +50,8 @@ struct Side {
     int gcount, gmax;        // entries of gather, rows of the matrix
 };
 
-template <Operand O, int BM, int NW>
+// Gathered: the rows of a kCols operand (c) are taken through Side::gather; kRows operands look at gather itself.
+template <Operand O, int BM, int NW, bool Gathered = false>
 struct Stager {
     static constexpr int kRowChunks = BM / 8, kRowsPerLoad = 64 / kRowChunks;   // kCols: a row's chunks, rows of one 1 KB load
     __amdgpu_buffer_rsrc_t rsrc;
@@ -61,7 +62,7 @@ struct Stager {
     const int32_t *gather;
     int gcount, gmax, C;
     uint32_t ld2;
-    int tok[4 * kRowsPerLoad];   // tokens of this wave's rows
+    uint32_t held[2];      // row offsets of this wave's tokens in kHeld steps, one a lane
     uint32_t rowoff[4];    // this lane's row offset of load j of the step being issued
 
     __device__ __forceinline__ void init(const Side &s, int C_) {
@@ -90,7 +91,7 @@ struct Stager {
                 const int lr = kRowsPerLoad * i + lane / kRowChunks, q = (lane % kRowChunks) ^ ((lr & 3) << 2);
                 // a column past the matrix reads the next row's values, or zeros: they only reach
                 // outputs that do not exist. Rows past C read zeros by themselves.
-                off[j] = (s.gather ? 0u : (uint32_t)lr * ld2) + (uint32_t)(s.at + 8 * q) * 2u;
+                off[j] = (Gathered ? 0u : (uint32_t)lr * ld2) + (uint32_t)(s.at + 8 * q) * 2u;
                 lim[j] = (C_ + 63) / 64;
             }
         }
@@ -98,52 +99,39 @@ struct Stager {
     }
     // Which 1 KB of the tile load j of a wave fills. kCols: a wave's four loads take neighbouring rows, so that a gathered
     // operand's tokens are kWaveRows neighbouring entries of the plan.
-    static constexpr int kWaveRows = 4 * kRowsPerLoad;
+    static constexpr int kWaveRows = 4 * kRowsPerLoad, kHeld = 2 * 64 / kWaveRows;
     static __device__ __forceinline__ int place(int wave, int j) { return O == kRows ? wave + NW * j : 4 * wave + j; }
 
-    // Rows of a gathered kCols operand: tokens(s) issues scalar loads of step s's entries, which are not waited
-    // for; rows(s) turns them into this lane's offsets (rows past C and tokens out of range read zeros).
-    __device__ __forceinline__ void tokens(int s) {
-        if constexpr (O == kCols) {
-            if (!gather) return;   // uniform
-            const int c0 = s * 64 + kWaveRows * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-            if (c0 + kWaveRows <= gcount) {   // uniform
+    // Rows of a gathered kCols operand. hold(s), s a multiple of kHeld, takes this wave's tokens of the steps s .. s + kHeld - 1
+    // by vector loads, one or two a lane, and keeps their row offsets (rows past C and tokens out of range read zeros);
+    // rows(s) hands each lane those of its four loads. Scalar loads of a step's tokens would return out of order
+    // with the LDS reads, whose waits would then all be for everything: 8192 tokens, k = 2 of 8, 4096 -> 4096: 523 us instead of 475.
+    __device__ __forceinline__ void hold(int s) {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        int t[2];
 #pragma unroll
-                for (int q = 0; q < kWaveRows / 8; ++q) {
-                    const i32x8 v = ((const __attribute__((address_space(4))) i32x8 *)(uintptr_t)(gather + c0))[q];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) tok[8 * q + r] = v[r];
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < kWaveRows; ++r) tok[r] = scalar_load(gather, min(c0 + r, gcount - 1));
-            }
+        for (int i = 0; i < 2; ++i) {
+            const int c = (s + i * (kHeld / 2) + lane / kWaveRows) * 64 + kWaveRows * wave + lane % kWaveRows;
+            t[i] = gather[min(c, gcount - 1)];
+            t[i] = c < C ? t[i] : -1;
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) held[i] = (unsigned)t[i] < (unsigned)gmax ? (uint32_t)t[i] * ld2 : kPast;
     }
     __device__ __forceinline__ void rows(int s) {
-        if constexpr (O == kCols) {
-            if (!gather) return;
-            const int lane = threadIdx.x & 63;
-            const int c0 = s * 64 + kWaveRows * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int lane = threadIdx.x & 63;
+        const uint32_t from = s & (kHeld / 2) ? held[1] : held[0];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t v = 0;
-#pragma unroll
-                for (int r = 0; r < kRowsPerLoad; ++r) {
-                    const int i = kRowsPerLoad * j + r;
-                    const uint32_t o = c0 + i < C && (unsigned)tok[i] < (unsigned)gmax ? (uint32_t)tok[i] * ld2 : kPast;
-                    v = r == 0 || lane / kRowChunks == r ? o : v;
-                }
-                rowoff[j] = v;
-            }
-        }
+        for (int j = 0; j < 4; ++j)
+            rowoff[j] = (uint32_t)__builtin_amdgcn_ds_bpermute(
+                4 * ((s & (kHeld / 2 - 1)) * kWaveRows + kRowsPerLoad * j + lane / kRowChunks), (int)from);
     }
     // Load j of step s into the stage at LDS byte address m0. Steps past the last one read zeros: the
     // loops issue them too, so that their bodies have no branch that products could be moved across.
     __device__ __forceinline__ void issue(uint32_t m0, int s, int j) const {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         uint32_t o;
-        if (O == kCols && gather) o = rowoff[j] + off[j];
+        if (Gathered) o = rowoff[j] + off[j];
         else o = s < lim[j] ? off[j] + (uint32_t)s * step : kPast;
         dma16(rsrc, m0 + (uint32_t)place(wave, j) * 1024u, o, 0);
     }
@@ -213,7 +201,7 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[BM / WM / 32][BN 
 }
 
 // The tile's product and its store. WM x WN waves, each RT x 2 accumulators of 32 x 32.
-template <Operand OA, Operand OB, int BM, int BN, int WM, int WN>
+template <Operand OA, Operand OB, int BM, int BN, int WM, int WN, bool Gathered = false>
 __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int C, const uint16_t *bias, uint16_t *out,
                                              int ldo, int om, int on, unsigned char *smem) {
     constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32;
@@ -252,8 +240,9 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
 
     const int steps = (C + 63) / 64;
     if (steps > 0) {
+        using StagerB = Stager<OB, BN, NW, Gathered>;
         Stager<OA, BM, NW> ga;
-        Stager<OB, BN, NW> gb;
+        StagerB gb;
         ga.init(sa, C);
         gb.init(sb, C);
         auto issue_a = [&](int xs, int s, int j) __attribute__((always_inline)) {
@@ -262,16 +251,15 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
         auto issue_b = [&](int vs, int s, int j) __attribute__((always_inline)) {
             gb.issue(base + 3 * AB + (uint32_t)vs * BB, s, j);
         };
+        if constexpr (Gathered) gb.hold(0);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            gb.tokens(s);
+            if constexpr (Gathered) gb.rows(s);
 #pragma unroll
             for (int j = 0; j < 4; ++j) issue_a(s, s, j);
-            gb.rows(s);
 #pragma unroll
             for (int j = 0; j < 4; ++j) issue_b(s, s, j);
         }
-        gb.tokens(2);
         wait_vm<8, 8>(8);
         __syncthreads();
         read_frags(0, 0, 0, 0);
@@ -281,14 +269,14 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
 #pragma unroll
             for (int kc = 0; kc < 3; ++kc) {
                 read_frags((kc + 1) & 1, xs, vs, kc + 1);
+                if (Gathered && kc == 1) gb.rows(s + 2);
                 products(kc, [&](int t) __attribute__((always_inline)) {
                     if (kc < 2) issue_a(x2, s + 2, 2 * kc + t);
                 });
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
-            gb.rows(s + 2);
-            gb.tokens(s + 3);   // with no LDS read outstanding: scalar loads share their counter and return out of order
             wait_vm<4, 4>(4);                                     // all but the A loads of s + 2 have landed
+            if (Gathered && (s + 3) % StagerB::kHeld == 0 && s + 3 < steps) gb.hold(s + 3);
             __syncthreads();
             const int xn = xs == 2 ? 0 : xs + 1, vn = vs ^ 1;
             read_frags(0, xn, vn, 0);

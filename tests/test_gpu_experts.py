@@ -192,7 +192,8 @@ def test_expert_bwd_input(kind, T, k, E, N, K):
 
 
 @pytest.mark.parametrize("kind,T,k,E,N,K", PRODUCTS + LARGE + [("ragged", 130, 2, 3, 2056, 2056), ("dropped", 300, 1, 25, 776, 520),
-                                                         ("ragged", 500, 2, 7, 1032, 1544)])
+                                                         ("ragged", 500, 2, 7, 1032, 1544), ("one", 2200, 1, 25, 776, 520),
+                                                         ("one", 1600, 1, 2, 136, 200), ("dropped", 2300, 2, 2, 264, 72)])
 @pytest.mark.parametrize("gather", [False, True])
 def test_expert_bwd_weight(kind, T, k, E, N, K, gather):
     say(f"case expert_bwd_weight {kind} T={T} k={k} E={E} N={N} K={K} gather={gather}")
