@@ -7,10 +7,10 @@
 // Work-groups find their expert and rows from offsets on the device.
 //
 // Large products are bound by the matrix cores' rate at the clock that the power allows. 16384 tokens, k = 2 of 8
-// experts, 4096 -> 11008: 2.49 ms, 1.19 PFLOP/s; one dense 16384 x 4096 -> 4096: 423 us, 1.30 PFLOP/s (the matrix
+// experts, 4096 -> 11008: 2.46 ms, 1.20 PFLOP/s; one dense 16384 x 4096 -> 4096: 423 us, 1.30 PFLOP/s (the matrix
 // instructions alone, on random data: 1.88). Measured there: matrix cores busy 67% of the time at 1.8 GHz; without the loads in
 // the loop 76% at 2.2 GHz, so the 64 KB a step through L2 cost both stalls and clock. Gradients of 8192 tokens, k = 2 of 8, 4096 -> 4096:
-// input 525 us (1.05 PFLOP/s), weight 475 us (1.16). Ragged groups cost partly empty tiles and the last round of tiles.
+// input 499 us (1.10 PFLOP/s), weight 475 us (1.16). Ragged groups cost partly empty tiles and the last round of tiles.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -31,26 +31,31 @@ struct GemmArgs {
     int T, R, E, Nout, C;   // output columns, contraction length
 };
 
-// Forward (OB = kRows) and input gradient (OB = kCols): one BM x BN tile a work-group.
+// Forward (OB = kRows) and input gradient (OB = kCols): one BM x BN tile a work-group, or half of one (piece_of).
 template <Operand OB, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_rows(GemmArgs g, int ntiles) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[tile_lds<BM, BN>()];
     const RowTiles<BM> tiles(g.offsets, g.E, g.R);
     const int total = tiles.total;
-    if ((int64_t)blockIdx.x >= (int64_t)total * ntiles) return;
-    const TileOrder o = tile_order(xcd_remap(blockIdx.x, total * ntiles), total, ntiles, kRowsTogether);
+    const Piece piece = piece_of<BN == 256>(blockIdx.x, total * ntiles);
+    if (piece.tile < 0) return;
+    const TileOrder o = tile_order(piece.tile, total, ntiles, kRowsTogether);
     const Rows t = tiles.find(o.row);
-    if (t.n <= 0) return;
+    const int col = o.col * BN + (piece.half > 0 ? BN / 2 : 0);
+    if (t.n <= 0 || col >= g.Nout) return;
     const bool live = t.e < g.E;
     const int e = live ? t.e : 0;
     const int64_t wsize = (int64_t)g.Nout * g.C;
     const Side a = g.gather ? Side{g.act, (uint32_t)((int64_t)g.T * g.C * 2), g.C, t.at, t.at + t.n, g.gather, g.R, g.T}
                             : Side{g.act + (int64_t)t.at * g.C, (uint32_t)((int64_t)t.n * g.C * 2), g.C, 0, t.n, nullptr, 0, 0};
-    const Side b{g.w + e * wsize, (uint32_t)(wsize * 2), OB == kRows ? g.C : g.Nout, o.col * BN, g.Nout, nullptr, 0, 0};
-    tile_product<kRows, OB, BM, BN, WM, WN>(a, b, live ? g.C : 0,
-                                            live && g.bias ? g.bias + (int64_t)e * g.Nout + o.col * BN : nullptr,
-                                            g.out + (int64_t)t.at * g.Nout + o.col * BN, g.Nout, t.n, g.Nout - o.col * BN,
-                                            smem);
+    const Side b{g.w + e * wsize, (uint32_t)(wsize * 2), OB == kRows ? g.C : g.Nout, col, g.Nout, nullptr, 0, 0};
+    const uint16_t *bias = live && g.bias ? g.bias + (int64_t)e * g.Nout + col : nullptr;
+    uint16_t *out = g.out + (int64_t)t.at * g.Nout + col;
+    if constexpr (BN == 256) {
+        if (piece.half >= 0)
+            return tile_product<kRows, OB, BM, BN / 2, 4, 2>(a, b, live ? g.C : 0, bias, out, g.Nout, t.n, g.Nout - col, smem);
+    }
+    tile_product<kRows, OB, BM, BN, WM, WN>(a, b, live ? g.C : 0, bias, out, g.Nout, t.n, g.Nout - col, smem);
 }
 
 // Weight gradient: one BM x BN tile of one expert's dW a work-group, over all rows of the expert. Every XCD takes an eighth
@@ -122,7 +127,7 @@ int32_t launched(const char *what) {
 template <Operand OB>
 int32_t launch_rows(const GemmArgs &g, int64_t bm, void *stream, const char *what) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const int64_t ntiles = (g.Nout + bm - 1) / bm, blocks = max_row_tiles(g.R, g.E, bm) * ntiles;
+    const int64_t ntiles = (g.Nout + bm - 1) / bm, blocks = max_row_tiles(g.R, g.E, bm) * ntiles + (bm == 256 ? kPieces : 0);
     if (const int32_t bad = check_grid(blocks, 512, what)) return bad;
     if (bm == 256)
         hipLaunchKernelGGL((k_expert_rows<OB, 256, 256, 2, 4>), dim3((unsigned)blocks), dim3(512), 0, st, g, (int)ntiles);

@@ -53,17 +53,18 @@ struct Side {
 // Gathered: the rows of a kCols operand (c) are taken through Side::gather; kRows operands look at gather itself.
 template <Operand O, int BM, int NW, bool Gathered = false>
 struct Stager {
-    static constexpr int kRowChunks = BM / 8, kRowsPerLoad = 64 / kRowChunks;   // kCols: a row's chunks, rows of one 1 KB load
+    static constexpr int kLoads = BM / 8 / NW;   // 1 KB loads a wave and step
+    static constexpr int kRowChunks = BM / 8, kRowsPerLoad = 64 / kRowChunks;   // kCols: a row's chunks, rows of one load
     __amdgpu_buffer_rsrc_t rsrc;
-    uint32_t off[4];       // byte offset of this lane's 16 bytes of load j at step 0
+    uint32_t off[kLoads];  // byte offset of this lane's 16 bytes of load j at step 0
     uint32_t step;         // bytes between steps
-    int lim[4];            // steps in which load j's 16 bytes exist: from step lim[j] on it reads zeros
+    int lim[kLoads];       // steps in which load j's 16 bytes exist: from step lim[j] on it reads zeros
     // gathered kCols: rows come from the plan, 64 of them a step
     const int32_t *gather;
     int gcount, gmax, C;
     uint32_t ld2;
     uint32_t held[2];      // row offsets of this wave's tokens in kHeld steps, one a lane
-    uint32_t rowoff[4];    // this lane's row offset of load j of the step being issued
+    uint32_t rowoff[kLoads];   // this lane's row offset of load j of the step being issued
 
     __device__ __forceinline__ void init(const Side &s, int C_) {
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -74,7 +75,7 @@ struct Stager {
         C = C_;
         ld2 = (uint32_t)s.ld * 2u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kLoads; ++j) {
             const int i = place(wave, j);
             if constexpr (O == kRows) {
                 const int lr = 8 * i + (lane >> 3), q = (lane & 7) ^ swz8(lr), row = s.at + lr;
@@ -97,14 +98,14 @@ struct Stager {
         }
         step = O == kRows ? 128u : 64u * ld2;
     }
-    // Which 1 KB of the tile load j of a wave fills. kCols: a wave's four loads take neighbouring rows, so that a gathered
+    // Which 1 KB of the tile load j of a wave fills. kCols: a wave's loads take neighbouring rows, so that a gathered
     // operand's tokens are kWaveRows neighbouring entries of the plan.
-    static constexpr int kWaveRows = 4 * kRowsPerLoad, kHeld = 2 * 64 / kWaveRows;
-    static __device__ __forceinline__ int place(int wave, int j) { return O == kRows ? wave + NW * j : 4 * wave + j; }
+    static constexpr int kWaveRows = kLoads * kRowsPerLoad, kHeld = 2 * 64 / kWaveRows;
+    static __device__ __forceinline__ int place(int wave, int j) { return O == kRows ? wave + NW * j : kLoads * wave + j; }
 
     // Rows of a gathered kCols operand. hold(s), s a multiple of kHeld, takes this wave's tokens of the steps s .. s + kHeld - 1
     // by vector loads, one or two a lane, and keeps their row offsets (rows past C and tokens out of range read zeros);
-    // rows(s) hands each lane those of its four loads. Scalar loads of a step's tokens would return out of order
+    // rows(s) hands each lane those of its loads. Scalar loads of a step's tokens would return out of order
     // with the LDS reads, whose waits would then all be for everything: 8192 tokens, k = 2 of 8, 4096 -> 4096: 523 us instead of 475.
     __device__ __forceinline__ void hold(int s) {
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -122,7 +123,7 @@ struct Stager {
         const int lane = threadIdx.x & 63;
         const uint32_t from = s & (kHeld / 2) ? held[1] : held[0];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kLoads; ++j)
             rowoff[j] = (uint32_t)__builtin_amdgcn_ds_bpermute(
                 4 * ((s & (kHeld / 2 - 1)) * kWaveRows + kRowsPerLoad * j + lane / kRowChunks), (int)from);
     }
@@ -207,7 +208,7 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
     constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32;
     static_assert(CT == 2, "the schedule issues two loads after each of two column tiles");
     constexpr int AB = BM * 128, BB = BN * 128;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN);
     const uint32_t base = lds_addr(smem);
 
@@ -243,6 +244,8 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
         using StagerB = Stager<OB, BN, NW, Gathered>;
         Stager<OA, BM, NW> ga;
         StagerB gb;
+        constexpr int LA = Stager<OA, BM, NW>::kLoads, LB = StagerB::kLoads;
+        static_assert(LA == 4, "A loads go after each of two column tiles of two chunks");
         ga.init(sa, C);
         gb.init(sb, C);
         auto issue_a = [&](int xs, int s, int j) __attribute__((always_inline)) {
@@ -256,11 +259,11 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
         for (int s = 0; s < 2; ++s) {
             if constexpr (Gathered) gb.rows(s);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) issue_a(s, s, j);
+            for (int j = 0; j < LA; ++j) issue_a(s, s, j);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) issue_b(s, s, j);
+            for (int j = 0; j < LB; ++j) issue_b(s, s, j);
         }
-        wait_vm<8, 8>(8);
+        wait_vm<LA + LB, LA + LB>(LA + LB);
         __syncthreads();
         read_frags(0, 0, 0, 0);
         int xs = 0, vs = 0;
@@ -275,14 +278,14 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
                 });
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
-            wait_vm<4, 4>(4);                                     // all but the A loads of s + 2 have landed
+            wait_vm<LA, LA>(LA);                                    // all but the A loads of s + 2 have landed
             if (Gathered && (s + 3) % StagerB::kHeld == 0 && s + 3 < steps) gb.hold(s + 3);
             __syncthreads();
             const int xn = xs == 2 ? 0 : xs + 1, vn = vs ^ 1;
             read_frags(0, xn, vn, 0);
             products(3, [&](int t) __attribute__((always_inline)) {
-                issue_b(vs, s + 2, 2 * t);
-                issue_b(vs, s + 2, 2 * t + 1);
+#pragma unroll
+                for (int j = t * LB / 2; j < (t + 1) * LB / 2; ++j) issue_b(vs, s + 2, j);
             });
             xs = xn;
             vs = vn;
@@ -368,7 +371,25 @@ __device__ __forceinline__ TileOrder tile_order(int L, int rows, int cols, int p
 
 constexpr int kRowsTogether = 4;
 
+// Which of `tiles` tiles a block takes, one work-group a CU; -1 past the end. With Halves, where the last round would leave half of
+// the CUs idle or more, its tiles are taken by two work-groups each, half of the columns a work-group (half = 0 or 1, else -1).
+// Whole | halves: input gradient of 16384 rows, 8 experts, 4096 -> 4096 (4.3 rounds) 521 | 499 us; 64 experts, 2048 -> 1000
+// 117 | 109; forward 32768 rows, 4096 -> 11008 (22.3 rounds) 2500 | 2460; the same in 4 bits 854 | 841.
+struct Piece {
+    int tile, half;
+};
+template <bool Halves>
+__device__ __forceinline__ Piece piece_of(int64_t block, int tiles) {
+    const int rest = Halves && tiles % kCUs <= kCUs / 2 ? tiles % kCUs : 0, whole = tiles - rest;
+    if (block < whole) return {xcd_remap((int)block, whole), -1};
+    if (block >= whole + 2 * rest) return {-1, -1};
+    const int h = xcd_remap((int)block - whole, 2 * rest);
+    return {whole + h / 2, h & 1};
+}
+
 }  // namespace dev
+
+constexpr int kPieces = 128;   // work-groups that halves add to a grid: a half round
 
 // Row tiles that R rows in E groups and the rows past the plan can need.
 inline int64_t max_row_tiles(int64_t R, int64_t E, int64_t bm) { return (R + std::min(E + 1, R) * (bm - 1)) / bm; }

@@ -121,8 +121,8 @@ __global__ __launch_bounds__(256, 2) void k_mx4_rows(GemmArgs g, int ntiles) {
 // j = 0 .. 3 being the step's four products, so that its four scale bytes are one 32-bit word whose byte j the j-th
 // product selects. Two stages a side: the loads of step s + 2 are issued behind the barrier that ends the
 // reads of step s, among the products of its last chunk.
-// 16384 rows, 8 experts, 4096 -> 4096: 174 us, 3.2 PFLOP/s; 32768 rows, 4096 -> 11008: 836 us, 3.5 (the instructions alone, on
-// random data: 8.0). Copies that skip work, of the 836: no loads in the loop 700, no LDS reads 744, neither 632, a
+// 16384 rows, 8 experts, 4096 -> 4096: 171 us, 3.2 PFLOP/s; 32768 rows, 4096 -> 11008: 841 us, 3.5 (the instructions alone, on
+// random data: 8.0). Copies that skip work, of 836: no loads in the loop 700, no LDS reads 744, neither 632, a
 // single step 215: starts and ends of tiles and the matrix cores themselves hold most of it.
 // ------------------------------------------------------------------------------------------
 typedef int codes_x8 __attribute__((ext_vector_type(8)));
@@ -141,18 +141,12 @@ constexpr int mx4_lds() {
     return stages > out ? stages : out;
 }
 
+// The tile of t's rows and the columns from col.
 template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM *WN * 64, 1) void k_mx4_mx4(GemmArgs g, int ntiles) {
+__device__ __forceinline__ void mx4_tile(const GemmArgs &g, const Rows &t, int col, unsigned char *smem) {
     constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32;
-    static_assert(BM == NW * 32 && BN == NW * 32 && CT == 2, "one load of scales a wave and side");
+    static_assert(BM == NW * 32 && BN <= NW * 32 && CT == 2, "one load of scales a wave and side");
     constexpr int AB = BM * 128, BB = BN * 128, AS = 2 * (AB + BB), BS = AS + 2 * BM * 8;   // LDS: A, B, scales of A, of B
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[mx4_lds<BM, BN>()];
-    const RowTiles<BM> tiles(g.offsets, g.E, g.R);
-    const int total = tiles.total;
-    if ((int64_t)blockIdx.x >= (int64_t)total * ntiles) return;
-    const TileOrder o = tile_order(xcd_remap(blockIdx.x, total * ntiles), total, ntiles, kRowsTogether);
-    const Rows t = tiles.find(o.row);
-    if (t.n <= 0) return;
     const bool live = t.e < g.E;
     const int e = live ? t.e : 0, kb = (g.C + 255) / 256, steps = live ? kb : 0;
     const int64_t wbytes = (int64_t)g.Nout * (g.C / 2), abytes = (int64_t)(g.gather ? g.T : g.R) * (g.C / 2);
@@ -173,21 +167,23 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_mx4_mx4(GemmArgs g, int ntil
         // codes: 16-bit units, 128 bytes a row and step
         Stager<kRows, BM, NW> ga;
         Stager<kRows, BN, NW> gb;
+        constexpr int LB = Stager<kRows, BN, NW>::kLoads;
         ga.init({static_cast<const uint16_t *>(g.act), (uint32_t)abytes, g.C / 4, t.at, t.at + t.n, g.gather, g.R, g.T}, g.C / 4);
-        gb.init({static_cast<const uint16_t *>(g.w) + e * (wbytes / 2), (uint32_t)wbytes, g.C / 4, o.col * BN, g.Nout, nullptr, 0,
+        gb.init({static_cast<const uint16_t *>(g.w) + e * (wbytes / 2), (uint32_t)wbytes, g.C / 4, col, g.Nout, nullptr, 0,
                  0}, g.C / 4);
         // scale words: lane 2 r + h of wave w loads word h of row 32 w + r
         const int arows = g.gather ? g.T : g.R, half = lane & 1;
         const __amdgpu_buffer_rsrc_t rsa = make_rsrc(g.act_scales, (uint32_t)((int64_t)kb * arows * 8));
         const __amdgpu_buffer_rsrc_t rsb = make_rsrc(g.w_scales + (int64_t)e * kb * g.Nout * 8, (uint32_t)((int64_t)kb * g.Nout * 8));
-        const int ar = wave * 32 + (lane >> 1), br = o.col * BN + ar;
+        // (with fewer than 32 columns a wave, two waves load the same words)
+        const int ar = wave * 32 + (lane >> 1), bw = wave % (BN / 32), br = col + bw * 32 + (lane >> 1);
         const int arow = ar >= t.n ? -1 : g.gather ? g.gather[t.at + ar] : t.at + ar;
         const int sa_lim = (unsigned)arow < (unsigned)arows ? steps : 0, sb_lim = br < g.Nout ? steps : 0;
         const uint32_t sa_off = (uint32_t)arow * 8u + 4u * half, sb_off = (uint32_t)br * 8u + 4u * half;
         const uint32_t sa_step = (uint32_t)arows * 8u, sb_step = (uint32_t)g.Nout * 8u;
         auto issue_scales = [&](int st, int s) __attribute__((always_inline)) {
             dma4(rsa, base + AS + (uint32_t)st * (BM * 8) + (uint32_t)wave * 256u, s < sa_lim ? sa_off + (uint32_t)s * sa_step : kPast);
-            dma4(rsb, base + BS + (uint32_t)st * (BN * 8) + (uint32_t)wave * 256u, s < sb_lim ? sb_off + (uint32_t)s * sb_step : kPast);
+            dma4(rsb, base + BS + (uint32_t)st * (BN * 8) + (uint32_t)bw * 256u, s < sb_lim ? sb_off + (uint32_t)s * sb_step : kPast);
         };
         auto issue_a = [&](int st, int s, int j) __attribute__((always_inline)) {
             ga.issue(base + (uint32_t)st * AB, s, j);
@@ -242,12 +238,12 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_mx4_mx4(GemmArgs g, int ntil
 #pragma unroll
             for (int j = 0; j < 4; ++j) issue_a(st, s, j);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) issue_b(st, s, j);
+            for (int j = 0; j < LB; ++j) issue_b(st, s, j);
             issue_scales(st, s);
         };
         load(0, 0);
         load(1, 1);
-        wait_vm<10, 10>(10);
+        wait_vm<6 + LB, 6 + LB>(6 + LB);
         __syncthreads();
         read_frags(0, 0, 0);
         read_scales(0, 0);
@@ -267,7 +263,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_mx4_mx4(GemmArgs g, int ntil
             read_scales(st ^ 1, s + 1);
             products(std::integral_constant<int, 3>{}, [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < (c == 0 ? 4 : LB); ++j) {
                     if (c == 0) issue_a(st, s + 2, j);
                     else issue_b(st, s + 2, j);
                 }
@@ -277,9 +273,27 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_mx4_mx4(GemmArgs g, int ntil
         }
         wait_vm<0, 0>(0);
     }
-    store_tile<BM, BN, WM, WN>(acc, live && g.bias ? g.bias + (int64_t)e * g.Nout + o.col * BN : nullptr,
-                               g.out + (int64_t)t.at * g.Nout + o.col * BN, g.Nout, t.n, g.Nout - o.col * BN, smem);
+    store_tile<BM, BN, WM, WN>(acc, live && g.bias ? g.bias + (int64_t)e * g.Nout + col : nullptr,
+                               g.out + (int64_t)t.at * g.Nout + col, g.Nout, t.n, g.Nout - col, smem);
 }
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM *WN * 64, 1) void k_mx4_mx4(GemmArgs g, int ntiles) {
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[mx4_lds<BM, BN>()];
+    const RowTiles<BM> tiles(g.offsets, g.E, g.R);
+    const int total = tiles.total;
+    const Piece piece = piece_of<BN == 256>(blockIdx.x, total * ntiles);
+    if (piece.tile < 0) return;
+    const TileOrder o = tile_order(piece.tile, total, ntiles, kRowsTogether);
+    const Rows t = tiles.find(o.row);
+    const int col = o.col * BN + (piece.half > 0 ? BN / 2 : 0);
+    if (t.n <= 0 || col >= g.Nout) return;
+    if constexpr (BN == 256) {
+        if (piece.half >= 0) return mx4_tile<BM, BN / 2, 4, 2>(g, t, col, smem);
+    }
+    mx4_tile<BM, BN, WM, WN>(g, t, col, smem);
+}
+
 
 int32_t launched(const char *what) {
     const hipError_t err = hipGetLastError();
@@ -310,7 +324,8 @@ int32_t launch_expert_fwd_mx4_mx4(const ExpertShape &s, const uint8_t *xcodes, c
     const GemmArgs g{xcodes, codes, xscales, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const bool w = wide(s.R, s.E, s.N);
-    const int64_t bm = w ? 256 : 128, ntiles = (s.N + bm - 1) / bm, blocks = max_row_tiles(s.R, s.E, bm) * ntiles;
+    const int64_t bm = w ? 256 : 128, ntiles = (s.N + bm - 1) / bm;
+    const int64_t blocks = max_row_tiles(s.R, s.E, bm) * ntiles + (w ? kPieces : 0);
     if (const int32_t bad = check_grid(blocks, 512, "bsr_expert_fwd_mx4_mx4")) return bad;
     if (w)
         hipLaunchKernelGGL((k_mx4_mx4<256, 256, 2, 4>), dim3((unsigned)blocks), dim3(512), 0, st, g, (int)ntiles);
