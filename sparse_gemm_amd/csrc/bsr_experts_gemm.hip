@@ -7,10 +7,10 @@
 // Work-groups find their expert and rows from offsets on the device.
 //
 // Large products are bound by the matrix cores' rate at the clock that the power allows. 16384 tokens, k = 2 of 8
-// experts, 4096 -> 11008: 2.46 ms, 1.20 PFLOP/s; one dense 16384 x 4096 -> 4096: 423 us, 1.30 PFLOP/s (the matrix
-// instructions alone, on random data: 1.88). Measured there: matrix cores busy 67% of the time at 1.8 GHz; without the loads in
-// the loop 76% at 2.2 GHz, so the 64 KB a step through L2 cost both stalls and clock. Gradients of 8192 tokens, k = 2 of 8, 4096 -> 4096:
-// input 499 us (1.10 PFLOP/s), weight 475 us (1.16). Ragged groups cost partly empty tiles and the last round of tiles.
+// experts, 4096 -> 11008: 2.37 ms, 1.25 PFLOP/s; one dense 16384 x 4096 -> 4096: 393 us, 1.40 PFLOP/s (the matrix
+// instructions alone, on random data: 2.1). Copies that skip work, of a dense 16384 x 16384 -> 4096 in 1591 us: no loads in the loop 1079, no
+// waits for loads 1579, no barrier 1518, no LDS reads 1347: the 64 KB a step through L2, not their latency, cost most. Gradients of 8192 tokens, k = 2 of 8, 4096 -> 4096:
+// input 464 us (1.19 PFLOP/s), weight 459 us (1.20). Ragged groups cost partly empty tiles and the last round of tiles.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

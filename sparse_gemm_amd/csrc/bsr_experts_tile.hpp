@@ -5,14 +5,16 @@
 // operand lies in memory either with c contiguous (kRows: one row per m or n) or with m or n
 // contiguous (kCols: one row per c); both are staged as they are by direct-to-LDS loads, 4 a wave and
 // step, and read as matrix-core fragments, kCols ones by transposing reads.
-//   kRows tile: [BM rows][8 chunks of 16 bytes], chunk q of row r at q ^ swz8(r)
-//   kCols tile: [64 rows][BM / 8 chunks], chunk q of row r at q ^ (4 (r & 3)): the 4 rows that a
-//               transposing read takes lie in the 4 quarters of the 64 banks
-// Of A three stages are held, of B two (160 KB at 256 x 256): during step s the A loads of step s + 2 are issued
-// between the products of its first two 16-deep chunks; then every wave waits for its LDS reads of
-// s and for its loads of s + 1, a barrier publishes those, and the B loads of s + 2 go between the
-// products of the last chunk, after the first fragments of s + 1 have been read. So a load has about one
-// step to land, and the products never wait for an LDS read right behind a barrier.
+//   kRows tile: [BM rows][8 chunks of 16 bytes], chunk q of row r at q ^ swz_rows(r)
+//   kCols tile: [64 rows][BM / 8 chunks], chunk q of row r at q ^ swz_cols(r)
+// Of A three stages are held, of B two (160 KB at 256 x 256). A step is two 32-deep chunks of 16 x 16 x 32 products; while the rows of
+// one chunk are multiplied, the fragments of the next are read, each into registers that a finished row has left. Between a
+// step's chunks every wave waits for its LDS reads of s and for its loads of s + 1, and a barrier publishes those. The A loads of
+// s + 2 are issued in the first chunk of s, the B loads, into the stage that the barrier has freed, in the second; so a load has
+// one step to land, and no product waits for an LDS read right behind a barrier.
+// 16 x 16 x 32 products move half of the accumulators of 32 x 32 x 16 ones per operation: alone, on random data, 2100
+// TFLOP/s against 1750 at the clocks that the power allows; here, 16384 x 4096 -> 4096, 393 us against 420. Where in a chunk its reads
+// and loads go is left to the compiler: with every row's reads, products and loads pinned in order 399.
 #pragma once
 
 #include <algorithm>
@@ -50,9 +52,16 @@ struct Side {
     int gcount, gmax;        // entries of gather, rows of the matrix
 };
 
+// Chunk swizzle of a kCols tile: a transposing read of 32 lanes takes rows 8 g + (0 .. 3) for two g, 32 bytes of each: row % 4
+// picks a quarter of the 64 banks, g % 2 a half of that.
+__device__ __forceinline__ int swz_cols(int r) { return ((r & 3) << 2) ^ (((r >> 3) & 1) << 1); }
+
+// Frag: rows of the fragments that are read, 16 or 32; it decides how kRows chunks lie. (With 16 lanes a chunk, swz8 makes two rows of
+// each group of lanes that LDS serves at once share a bank: twice the LDS cycles.)
 // Gathered: the rows of a kCols operand (c) are taken through Side::gather; kRows operands look at gather itself.
-template <Operand O, int BM, int NW, bool Gathered = false>
+template <Operand O, int BM, int NW, int Frag, bool Gathered = false>
 struct Stager {
+    static __device__ __forceinline__ int swz_rows(int r) { return Frag == 16 ? r & 7 : swz8(r); }
     static constexpr int kLoads = BM / 8 / NW;   // 1 KB loads a wave and step
     static constexpr int kRowChunks = BM / 8, kRowsPerLoad = 64 / kRowChunks;   // kCols: a row's chunks, rows of one load
     __amdgpu_buffer_rsrc_t rsrc;
@@ -78,7 +87,7 @@ struct Stager {
         for (int j = 0; j < kLoads; ++j) {
             const int i = place(wave, j);
             if constexpr (O == kRows) {
-                const int lr = 8 * i + (lane >> 3), q = (lane & 7) ^ swz8(lr), row = s.at + lr;
+                const int lr = 8 * i + (lane >> 3), q = (lane & 7) ^ swz_rows(lr), row = s.at + lr;
                 uint32_t src = (uint32_t)row;
                 bool ok = row < s.rows;
                 if (s.gather) {
@@ -89,7 +98,7 @@ struct Stager {
                 off[j] = src * ld2 + (uint32_t)q * 16u;
                 lim[j] = ok ? (C_ - 8 * q + 63) / 64 : 0;
             } else {
-                const int lr = kRowsPerLoad * i + lane / kRowChunks, q = (lane % kRowChunks) ^ ((lr & 3) << 2);
+                const int lr = kRowsPerLoad * i + lane / kRowChunks, q = (lane % kRowChunks) ^ swz_cols(lr);
                 // a column past the matrix reads the next row's values, or zeros: they only reach
                 // outputs that do not exist. Rows past C read zeros by themselves.
                 off[j] = (Gathered ? 0u : (uint32_t)lr * ld2) + (uint32_t)(s.at + 8 * q) * 2u;
@@ -136,20 +145,25 @@ struct Stager {
         else o = s < lim[j] ? off[j] + (uint32_t)s * step : kPast;
         dma16(rsrc, m0 + (uint32_t)place(wave, j) * 1024u, o, 0);
     }
-    // Fragment of rows / columns t0 .. t0 + 31 of a staged tile for 16-deep chunk kc.
-    static __device__ __forceinline__ bf16x8 frag(const unsigned char *tile, int t0, int kc) {
-        const int lane = threadIdx.x & 63;
+    // Fragments of 16 rows / columns from t0 + 16 r and a 32-deep chunk kc of a staged tile. With t0 a multiple of 64, and of 128
+    // for r above 3, r and kc only flip bits of a lane's address and add to it: it is kept once, for r = kc = 0.
+    static __device__ __forceinline__ uint32_t lane_at(int t0) {
+        const int lane = threadIdx.x & 63, h = lane >> 4, l16 = lane & 15;
         if constexpr (O == kRows) {
-            const int r = t0 + (lane & 31);
-            return *reinterpret_cast<const bf16x8 *>(tile + r * 128 + (((2 * kc + (lane >> 5)) ^ swz8(r)) << 4));
+            return (uint32_t)((t0 + l16) * 128 + ((h ^ swz_rows(l16)) << 4));
         } else {
-            const int gq = lane >> 4, s16 = lane & 15;
-            const int R = kc * 16 + (gq >> 1) * 8 + (s16 >> 2), col = t0 + (gq & 1) * 16 + 4 * (s16 & 3);
-            auto at = [&](int row) {
-                return (lds_i16x4 *)(tile + row * (BM * 2) + ((((col >> 3) ^ ((row & 3) << 2)) << 4) | ((col & 7) << 1)));
-            };
-            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(R));
-            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at(R + 4));
+            const int R = h * 8 + (l16 >> 2), col = t0 + 4 * (l16 & 3);
+            return (uint32_t)(R * (BM * 2) + ((((col >> 3) ^ swz_cols(R)) << 4) | ((col & 7) << 1)));
+        }
+    }
+    static __device__ __forceinline__ bf16x8 frag(uint32_t at, int r, int kc) {
+        if constexpr (O == kRows) {
+            typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
+            return *(lds_bf16x8 *)((at ^ (uint32_t)(kc << 6)) + (uint32_t)r * 2048u);
+        } else {
+            const uint32_t p = (at ^ (uint32_t)(r << 5)) + (uint32_t)kc * (64u * BM);
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p);
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + 8u * BM));   // 4 rows on
             const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             return __builtin_bit_cast(bf16x8, v);
         }
@@ -162,9 +176,21 @@ constexpr int tile_lds() {
     return stages > out ? stages : out;
 }
 
+// A wave's 32 rows x 64 columns from its LDS to out: rows of 128 bytes in 16-byte pieces, piece q of row r at q ^ (r / 2 % 8), so
+// that 16 rows take different banks.
+__device__ __forceinline__ void store_piece(uint16_t *out, int ldo, int om, int on, const unsigned char *own) {
+    const int lane = threadIdx.x & 63;
+    const int q = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = 8 * i + (lane >> 3);
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(own + m * 128 + ((q ^ ((m >> 1) & 7)) << 4));
+        if (m < om && 8 * q < on) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(out + (int64_t)m * ldo + 8 * q));
+    }
+}
+
 // Stores 32 rows x 64 columns of a wave through its 4 KB of LDS: item v of lane l of acc[t] is column 32 t + 8 (v / 4) +
-// 4 (l / 32) + v % 4 of row l % 32. Bias in fp32, one rounding to bf16, then rows of 128 bytes in 16-byte
-// pieces; piece q of row r lies at q ^ (r / 2 % 8), so that 16 rows take different banks.
+// 4 (l / 32) + v % 4 of row l % 32. Bias in fp32, one rounding to bf16.
 __device__ __forceinline__ void store_rows(const f32x16 (&acc)[2], const uint16_t *bias, uint16_t *out, int ldo, int om,
                                            int on, unsigned char *own) {
     const int lane = threadIdx.x & 63, r = lane & 31, lh = lane >> 5;
@@ -178,13 +204,7 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[2], const uint16_
             store4_bf16(reinterpret_cast<uint16_t *>(own + r * 128 + (((4 * t + q) ^ ((r >> 1) & 7)) << 4) + 8 * lh), v[0], v[1],
                         v[2], v[3]);
         }
-    const int q = lane & 7;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = 8 * i + (lane >> 3);
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(own + m * 128 + ((q ^ ((m >> 1) & 7)) << 4));
-        if (m < om && 8 * q < on) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(out + (int64_t)m * ldo + 8 * q));
-    }
+    store_piece(out, ldo, om, on, own);
 }
 
 // Stores a tile from the waves' accumulators: row m of out at out + m * ldo; om rows and on (a multiple of 8) columns of
@@ -201,50 +221,71 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[BM / WM / 32][BN 
                    on - n0, smem + (wave * (BM / WM / 32) + r) * 4096);
 }
 
-// The tile's product and its store. WM x WN waves, each RT x 2 accumulators of 32 x 32.
+// The same from accumulators of 16 x 16: item v of lane l of acc[m][t] is column 16 t + 4 (l / 16) + v of row 16 m + l % 16.
+__device__ __forceinline__ void store_rows(const f32x4 (&lo)[4], const f32x4 (&hi)[4], const uint16_t *bias, uint16_t *out, int ldo,
+                                           int om, int on, unsigned char *own) {
+    const int lane = threadIdx.x & 63, l16 = lane & 15, h = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            f32x4 v = m ? hi[t] : lo[t];
+            const int n = 16 * t + 4 * h, r = 16 * m + l16;
+            if (bias && n < on) v = add_bias4(v, bias + n);
+            store4_bf16(reinterpret_cast<uint16_t *>(own + r * 128 + (((2 * t + (h >> 1)) ^ ((r >> 1) & 7)) << 4) + 8 * (h & 1)), v[0],
+                        v[1], v[2], v[3]);
+        }
+    store_piece(out, ldo, om, on, own);
+}
+
+template <int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[BM / WM / 16][BN / WN / 16], const uint16_t *bias, uint16_t *out,
+                                           int ldo, int om, int on, unsigned char *smem) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN);
+    __syncthreads();   // the stages are free
+#pragma unroll
+    for (int r = 0; r < BM / WM / 32; ++r)
+        store_rows(acc[2 * r], acc[2 * r + 1], bias ? bias + n0 : nullptr, out + (int64_t)(m0 + 32 * r) * ldo + n0, ldo,
+                   om - m0 - 32 * r, on - n0, smem + (wave * (BM / WM / 32) + r) * 4096);
+}
+
+// The tile's product and its store. WM x WN waves, each RT x 4 accumulators of 16 x 16.
 template <Operand OA, Operand OB, int BM, int BN, int WM, int WN, bool Gathered = false>
 __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int C, const uint16_t *bias, uint16_t *out,
                                              int ldo, int om, int on, unsigned char *smem) {
-    constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32;
-    static_assert(CT == 2, "the schedule issues two loads after each of two column tiles");
+    constexpr int NW = WM * WN, RT = BM / WM / 16, CT = BN / WN / 16;
+    static_assert(CT == 4 && RT % 4 == 0, "the schedule below");
     constexpr int AB = BM * 128, BB = BN * 128;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN);
     const uint32_t base = lds_addr(smem);
 
-    f32x16 acc[RT][CT];
+    f32x4 acc[RT][CT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[r][t][v] = 0.f;
+        for (int t = 0; t < CT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    bf16x8 fa[2][RT], fb[2][CT];
-    auto read_frags = [&](int set, int xs, int vs, int kc) __attribute__((always_inline)) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) fa[set][r] = Stager<OA, BM, NW>::frag(smem + xs * AB, m0 + 32 * r, kc);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) fb[set][t] = Stager<OB, BN, NW>::frag(smem + 3 * AB + vs * BB, n0 + 32 * t, kc);
+    bf16x8 fa[2][RT], fb[2][CT];   // [chunk]
+    const uint32_t lane_a = base + Stager<OA, BM, NW, 16>::lane_at(m0), lane_b = base + 3 * AB + Stager<OB, BN, NW, 16>::lane_at(n0);
+    auto read_a = [&](int xs, int kc, int r) __attribute__((always_inline)) {
+        fa[kc][r] = Stager<OA, BM, NW, 16>::frag(lane_a + (uint32_t)xs * AB, r, kc);
     };
-    auto products = [&](int kc, auto &&after) __attribute__((always_inline)) {
-        const int cur = kc & 1;
+    auto read_b = [&](int vs, int kc, int t) __attribute__((always_inline)) {
+        fb[kc][t] = Stager<OB, BN, NW, 16>::frag(lane_b + (uint32_t)vs * BB, t, kc);
+    };
+    auto products = [&](int kc, int r) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r) acc[r][t] = mfma32(fb[cur][t], fa[cur][r], acc[r][t]);
-            __builtin_amdgcn_sched_barrier(0);
-            after(t);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int t = 0; t < CT; ++t) acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kc][t], fa[kc][r], acc[r][t], 0, 0, 0);
     };
 
     const int steps = (C + 63) / 64;
     if (steps > 0) {
-        using StagerB = Stager<OB, BN, NW, Gathered>;
-        Stager<OA, BM, NW> ga;
+        using StagerB = Stager<OB, BN, NW, 16, Gathered>;
+        Stager<OA, BM, NW, 16> ga;
         StagerB gb;
-        constexpr int LA = Stager<OA, BM, NW>::kLoads, LB = StagerB::kLoads;
+        constexpr int LA = Stager<OA, BM, NW, 16>::kLoads, LB = StagerB::kLoads;
         static_assert(LA == 4, "A loads go after each of two column tiles of two chunks");
         ga.init(sa, C);
         gb.init(sb, C);
@@ -265,28 +306,44 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
         }
         wait_vm<LA + LB, LA + LB>(LA + LB);
         __syncthreads();
-        read_frags(0, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) read_b(0, 0, t);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) read_a(0, 0, r);
+        read_a(0, 1, 0);
+        read_a(0, 1, 1);
         int xs = 0, vs = 0;
         for (int s = 0; s < steps; ++s) {
             const int x2 = xs == 0 ? 2 : xs - 1;   // A stage of s + 2 (that of s - 1)
+            const int xn = xs == 2 ? 0 : xs + 1, vn = vs ^ 1;
 #pragma unroll
-            for (int kc = 0; kc < 3; ++kc) {
-                read_frags((kc + 1) & 1, xs, vs, kc + 1);
-                if (Gathered && kc == 1) gb.rows(s + 2);
-                products(kc, [&](int t) __attribute__((always_inline)) {
-                    if (kc < 2) issue_a(x2, s + 2, 2 * kc + t);
-                });
+            for (int r = 0; r < RT; ++r) {
+                if (r < 2) {
+                    read_b(vs, 1, 2 * r);
+                    read_b(vs, 1, 2 * r + 1);
+                }
+                if (r + 2 < RT) read_a(xs, 1, r + 2);
+                if (Gathered && r == 1) gb.rows(s + 2);
+#pragma unroll
+                for (int j = r * LA / RT; j < (r + 1) * LA / RT; ++j) issue_a(x2, s + 2, j);
+                products(0, r);
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
-            wait_vm<LA, LA>(LA);                                    // all but the A loads of s + 2 have landed
+            wait_vm<LA, LA>(LA);                                  // all but the A loads of s + 2 have landed
             if (Gathered && (s + 3) % StagerB::kHeld == 0 && s + 3 < steps) gb.hold(s + 3);
             __syncthreads();
-            const int xn = xs == 2 ? 0 : xs + 1, vn = vs ^ 1;
-            read_frags(0, xn, vn, 0);
-            products(3, [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-                for (int j = t * LB / 2; j < (t + 1) * LB / 2; ++j) issue_b(vs, s + 2, j);
-            });
+            for (int r = 0; r < RT; ++r) {
+                if (r < 2) {
+                    read_b(vn, 0, 2 * r);
+                    read_b(vn, 0, 2 * r + 1);
+                }
+                read_a(xn, 0, r);
+#pragma unroll
+                for (int j = r * LB / RT; j < (r + 1) * LB / RT; ++j) issue_b(vs, s + 2, j);
+                products(1, r);
+                if (r >= RT - 2) read_a(xn, 1, r - (RT - 2));
+            }
             xs = xn;
             vs = vn;
         }

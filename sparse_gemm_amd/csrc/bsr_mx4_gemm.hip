@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256, 2) void k_mx4_rows(GemmArgs g, int ntiles) {
             for (int v = 0; v < 16; ++v) acc[r][c][v] = 0.f;
 
     if (steps > 0) {
-        Stager<kRows, BM, 4> ga;
+        Stager<kRows, BM, 4, 32> ga;
         ga.init({static_cast<const uint16_t *>(g.act), (uint32_t)((int64_t)(g.gather ? g.T : g.R) * g.C * 2), g.C, t.at, t.at + t.n,
                  g.gather, g.R, g.T}, g.C);
         const int64_t wbytes = (int64_t)g.Nout * (g.C / 2);
@@ -165,9 +165,9 @@ __device__ __forceinline__ void mx4_tile(const GemmArgs &g, const Rows &t, int c
 
     if (steps > 0) {
         // codes: 16-bit units, 128 bytes a row and step
-        Stager<kRows, BM, NW> ga;
-        Stager<kRows, BN, NW> gb;
-        constexpr int LB = Stager<kRows, BN, NW>::kLoads;
+        Stager<kRows, BM, NW, 32> ga;
+        Stager<kRows, BN, NW, 32> gb;
+        constexpr int LB = Stager<kRows, BN, NW, 32>::kLoads;
         ga.init({static_cast<const uint16_t *>(g.act), (uint32_t)abytes, g.C / 4, t.at, t.at + t.n, g.gather, g.R, g.T}, g.C / 4);
         gb.init({static_cast<const uint16_t *>(g.w) + e * (wbytes / 2), (uint32_t)wbytes, g.C / 4, col, g.Nout, nullptr, 0,
                  0}, g.C / 4);
