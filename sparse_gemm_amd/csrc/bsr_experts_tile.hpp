@@ -56,12 +56,16 @@ struct Side {
 // picks a quarter of the 64 banks, g % 2 a half of that.
 __device__ __forceinline__ int swz_cols(int r) { return ((r & 3) << 2) ^ (((r >> 3) & 1) << 1); }
 
-// Frag: rows of the fragments that are read, 16 or 32; it decides how kRows chunks lie. (With 16 lanes a chunk, swz8 makes two rows of
-// each group of lanes that LDS serves at once share a bank: twice the LDS cycles.)
+// Frag: how the fragments of kRows tiles are read, which decides how their chunks lie: 32 rows, the half-waves a chunk each; 16 rows,
+// lane quarter h chunk 4 c + h; 16 rows, quarter h chunk 2 h + c. (LDS serves 16 lanes at once, not neighbours: lanes 0 .. 3,
+// 12 .. 15 and 20 .. 27, for one. With swz8 under the second kind two of them share a bank: twice the LDS cycles.)
+enum Frag { kFrag32, kFrag16, kFrag16Pairs };
 // Gathered: the rows of a kCols operand (c) are taken through Side::gather; kRows operands look at gather itself.
-template <Operand O, int BM, int NW, int Frag, bool Gathered = false>
+template <Operand O, int BM, int NW, Frag F, bool Gathered = false>
 struct Stager {
-    static __device__ __forceinline__ int swz_rows(int r) { return Frag == 16 ? r & 7 : swz8(r); }
+    static __device__ __forceinline__ int swz_rows(int r) { 
+        return F == kFrag32 ? swz8(r) : F == kFrag16 ? r & 7 : (r & 4) | (r & 1) << 1 | (r >> 1 & 1);
+    }
     static constexpr int kLoads = BM / 8 / NW;   // 1 KB loads a wave and step
     static constexpr int kRowChunks = BM / 8, kRowsPerLoad = 64 / kRowChunks;   // kCols: a row's chunks, rows of one load
     __amdgpu_buffer_rsrc_t rsrc;
@@ -268,12 +272,12 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
         for (int t = 0; t < CT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     bf16x8 fa[2][RT], fb[2][CT];   // [chunk]
-    const uint32_t lane_a = base + Stager<OA, BM, NW, 16>::lane_at(m0), lane_b = base + 3 * AB + Stager<OB, BN, NW, 16>::lane_at(n0);
+    const uint32_t lane_a = base + Stager<OA, BM, NW, kFrag16>::lane_at(m0), lane_b = base + 3 * AB + Stager<OB, BN, NW, kFrag16>::lane_at(n0);
     auto read_a = [&](int xs, int kc, int r) __attribute__((always_inline)) {
-        fa[kc][r] = Stager<OA, BM, NW, 16>::frag(lane_a + (uint32_t)xs * AB, r, kc);
+        fa[kc][r] = Stager<OA, BM, NW, kFrag16>::frag(lane_a + (uint32_t)xs * AB, r, kc);
     };
     auto read_b = [&](int vs, int kc, int t) __attribute__((always_inline)) {
-        fb[kc][t] = Stager<OB, BN, NW, 16>::frag(lane_b + (uint32_t)vs * BB, t, kc);
+        fb[kc][t] = Stager<OB, BN, NW, kFrag16>::frag(lane_b + (uint32_t)vs * BB, t, kc);
     };
     auto products = [&](int kc, int r) __attribute__((always_inline)) {
 #pragma unroll
@@ -282,11 +286,10 @@ __device__ __forceinline__ void tile_product(const Side &sa, const Side &sb, int
 
     const int steps = (C + 63) / 64;
     if (steps > 0) {
-        using StagerB = Stager<OB, BN, NW, 16, Gathered>;
-        Stager<OA, BM, NW, 16> ga;
+        using StagerB = Stager<OB, BN, NW, kFrag16, Gathered>;
+        Stager<OA, BM, NW, kFrag16> ga;
         StagerB gb;
-        constexpr int LA = Stager<OA, BM, NW, 16>::kLoads, LB = StagerB::kLoads;
-        static_assert(LA == 4, "A loads go after each of two column tiles of two chunks");
+        constexpr int LA = Stager<OA, BM, NW, kFrag16>::kLoads, LB = StagerB::kLoads;
         ga.init(sa, C);
         gb.init(sb, C);
         auto issue_a = [&](int xs, int s, int j) __attribute__((always_inline)) {
@@ -431,7 +434,7 @@ constexpr int kRowsTogether = 4;
 // Which of `tiles` tiles a block takes, one work-group a CU; -1 past the end. With Halves, where the last round would leave half of
 // the CUs idle or more, its tiles are taken by two work-groups each, half of the columns a work-group (half = 0 or 1, else -1).
 // Whole | halves: input gradient of 16384 rows, 8 experts, 4096 -> 4096 (4.3 rounds) 521 | 499 us; 64 experts, 2048 -> 1000
-// 117 | 109; forward 32768 rows, 4096 -> 11008 (22.3 rounds) 2500 | 2460; the same in 4 bits 854 | 841.
+// 117 | 109; forward 32768 rows, 4096 -> 11008 (22.3 rounds) 2500 | 2460; the same in 4 bits 854 | 841 (all with 32 x 32 products).
 struct Piece {
     int tile, half;
 };

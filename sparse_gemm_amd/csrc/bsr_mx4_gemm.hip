@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256, 2) void k_mx4_rows(GemmArgs g, int ntiles) {
             for (int v = 0; v < 16; ++v) acc[r][c][v] = 0.f;
 
     if (steps > 0) {
-        Stager<kRows, BM, 4, 32> ga;
+        Stager<kRows, BM, 4, kFrag32> ga;
         ga.init({static_cast<const uint16_t *>(g.act), (uint32_t)((int64_t)(g.gather ? g.T : g.R) * g.C * 2), g.C, t.at, t.at + t.n,
                  g.gather, g.R, g.T}, g.C);
         const int64_t wbytes = (int64_t)g.Nout * (g.C / 2);
@@ -113,17 +113,17 @@ __global__ __launch_bounds__(256, 2) void k_mx4_rows(GemmArgs g, int ntiles) {
 }
 
 // ------------------------------------------------------------------------------------------
-// Both sides in 4 bits, on the scaled matrix cores (v_mfma_scale_f32_32x32x64_f8f6f4: 32 x 32 x 64 products
+// Both sides in 4 bits, on the scaled matrix cores (v_mfma_scale_f32_16x16x128_f8f6f4: 16 x 16 x 128 products
 // of codes, one scale byte per 32 of them on each side, fp32 sums).
 //
 // Steps of 256 columns: a row's 128 bytes of codes are staged exactly like 64 bf16 columns (8 chunks of 16
-// bytes, one group each), its 8 scale bytes beside them. Half-wave h of a fragment takes the groups 4 h + j,
-// j = 0 .. 3 being the step's four products, so that its four scale bytes are one 32-bit word whose byte j the j-th
-// product selects. Two stages a side: the loads of step s + 2 are issued behind the barrier that ends the
-// reads of step s, among the products of its last chunk.
-// 16384 rows, 8 experts, 4096 -> 4096: 171 us, 3.2 PFLOP/s; 32768 rows, 4096 -> 11008: 841 us, 3.5 (the instructions alone, on
-// random data: 8.0). Copies that skip work, of 836: no loads in the loop 700, no LDS reads 744, neither 632, a
-// single step 215: starts and ends of tiles and the matrix cores themselves hold most of it.
+// bytes, one group each), its 8 scale bytes beside them. Lane quarter h of a fragment takes the groups 2 h + j, j = 0, 1 being the
+// step's two chunks, so that its two scale bytes are one 16-bit word whose byte j the products of chunk j select. Two stages
+// a side; as in the bf16 products the fragments of one chunk are read while the other is multiplied, and a barrier between them
+// ends the reads of step s: the loads of step s + 2 are issued in its second chunk.
+// 16384 rows, 8 experts, 4096 -> 4096: 161 us, 3.4 PFLOP/s; 32768 rows, 4096 -> 11008: 790 us, 3.7 (with 32 x 32 x 64 products 171
+// and 840; the instructions alone, on random data, 7.3 against 6.4). Copies of that older form that skip work, of 836: no loads in the loop
+// 700, no LDS reads 744, neither 632, a single step 215: starts and ends of tiles and the matrix cores themselves hold most of it.
 // ------------------------------------------------------------------------------------------
 typedef int codes_x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -131,8 +131,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ codes_x8 codes8(i32x4 v) { return codes_x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 template <int J>
-__device__ __forceinline__ f32x16 mfma_mx4(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(codes8(a), codes8(b), c, 4, 4, J, sa, J, sb);
+__device__ __forceinline__ f32x4 mfma_mx4(i32x4 a, i32x4 b, f32x4 c, int sa, int sb) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes8(a), codes8(b), c, 4, 4, J, sa, J, sb);
 }
 
 template <int BM, int BN>
@@ -144,8 +144,8 @@ constexpr int mx4_lds() {
 // The tile of t's rows and the columns from col.
 template <int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void mx4_tile(const GemmArgs &g, const Rows &t, int col, unsigned char *smem) {
-    constexpr int NW = WM * WN, RT = BM / WM / 32, CT = BN / WN / 32;
-    static_assert(BM == NW * 32 && BN <= NW * 32 && CT == 2, "one load of scales a wave and side");
+    constexpr int NW = WM * WN, RT = BM / WM / 16, CT = BN / WN / 16;
+    static_assert(BM == NW * 32 && BN <= NW * 32 && CT == 4, "one load of scales a wave and side");
     constexpr int AB = BM * 128, BB = BN * 128, AS = 2 * (AB + BB), BS = AS + 2 * BM * 8;   // LDS: A, B, scales of A, of B
     const bool live = t.e < g.E;
     const int e = live ? t.e : 0, kb = (g.C + 255) / 256, steps = live ? kb : 0;
@@ -155,19 +155,17 @@ __device__ __forceinline__ void mx4_tile(const GemmArgs &g, const Rows &t, int c
     const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN), lh = lane >> 5;
     const uint32_t base = lds_addr(smem);
 
-    f32x16 acc[RT][CT];
+    f32x4 acc[RT][CT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[r][c][v] = 0.f;
+        for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if (steps > 0) {
         // codes: 16-bit units, 128 bytes a row and step
-        Stager<kRows, BM, NW, 32> ga;
-        Stager<kRows, BN, NW, 32> gb;
-        constexpr int LB = Stager<kRows, BN, NW, 32>::kLoads;
+        Stager<kRows, BM, NW, kFrag16Pairs> ga;
+        Stager<kRows, BN, NW, kFrag16Pairs> gb;
+        constexpr int LB = Stager<kRows, BN, NW, kFrag16Pairs>::kLoads;
         ga.init({static_cast<const uint16_t *>(g.act), (uint32_t)abytes, g.C / 4, t.at, t.at + t.n, g.gather, g.R, g.T}, g.C / 4);
         gb.init({static_cast<const uint16_t *>(g.w) + e * (wbytes / 2), (uint32_t)wbytes, g.C / 4, col, g.Nout, nullptr, 0,
                  0}, g.C / 4);
@@ -191,85 +189,85 @@ __device__ __forceinline__ void mx4_tile(const GemmArgs &g, const Rows &t, int c
         auto issue_b = [&](int st, int s, int j) __attribute__((always_inline)) {
             gb.issue(base + 2 * AB + (uint32_t)st * BB, s, j);
         };
-        // words of the last step whose groups do not exist are dropped byte by byte
-        const int left = g.C / 32 - (kb - 1) * 8 - 4 * lh;   // groups of this half in the last step
-        const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+        // bytes of the last step whose groups do not exist are dropped
+        const int h = lane >> 4, l16 = lane & 15, left = g.C / 32 - (kb - 1) * 8 - 2 * h;   // groups of this quarter in the last step
+        const uint32_t keep = left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
 
+        // a lane's fragment address for r = 0 and chunk 0: chunk 1 flips its lowest chunk bit
+        const uint32_t lane_f = (uint32_t)(l16 * 128 + (((2 * h) ^ Stager<kRows, BM, NW, kFrag16Pairs>::swz_rows(l16)) << 4));
+        const uint32_t lane_a = base + (uint32_t)m0 * 128u + lane_f, lane_b = base + 2 * AB + (uint32_t)n0 * 128u + lane_f;
+        const uint32_t lane_s = base + (uint32_t)(l16 * 8 + 2 * h);
         i32x4 fa[2][RT], fb[2][CT];
-        int wa[RT], wb[CT], na[RT], nb[CT];
-        auto frag = [&](const unsigned char *tile, int row, int j) __attribute__((always_inline)) {
-            const int r = row + (lane & 31);
-            return *reinterpret_cast<const i32x4 *>(tile + r * 128 + (((4 * lh + j) ^ swz8(r)) << 4));
+        int wa[RT], wb[2][CT];   // scale bytes of the quarter's two groups: chunk j takes byte j
+        auto frag = [&](uint32_t at, int r, int kc) __attribute__((always_inline)) {
+            typedef __attribute__((address_space(3))) const i32x4 lds_i32x4;
+            return *(lds_i32x4 *)((at ^ (uint32_t)(kc << 4)) + (uint32_t)r * 2048u);
         };
-        auto read_frags = [&](int set, int st, int j) __attribute__((always_inline)) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r) fa[set][r] = frag(smem + st * AB, m0 + 32 * r, j);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) fb[set][c] = frag(smem + 2 * AB + st * BB, n0 + 32 * c, j);
+        auto scale = [&](uint32_t at, uint32_t mask) __attribute__((always_inline)) {
+            typedef __attribute__((address_space(3))) const uint16_t lds_u16;
+            return (int)((uint32_t)*(lds_u16 *)at & mask);
         };
-        auto read_scales = [&](int st, int s) __attribute__((always_inline)) {
-            const uint32_t mask = s == steps - 1 ? keep : 0xFFFFFFFFu;
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-                na[r] = (int)(*reinterpret_cast<const uint32_t *>(smem + AS + st * (BM * 8) + (m0 + 32 * r + (lane & 31)) * 8 + 4 * lh) & mask);
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-                nb[c] = (int)(*reinterpret_cast<const uint32_t *>(smem + BS + st * (BN * 8) + (n0 + 32 * c + (lane & 31)) * 8 + 4 * lh) & mask);
+        auto read_a = [&](int st, int kc, int r) __attribute__((always_inline)) { fa[kc][r] = frag(lane_a + (uint32_t)st * AB, r, kc); };
+        auto read_b = [&](int st, int kc, int c) __attribute__((always_inline)) { fb[kc][c] = frag(lane_b + (uint32_t)st * BB, c, kc); };
+        auto scale_a = [&](int st, uint32_t mask, int r) __attribute__((always_inline)) {
+            wa[r] = scale(lane_s + (uint32_t)(AS + st * (BM * 8) + (m0 + 16 * r) * 8), mask);
         };
-        auto take_scales = [&]() __attribute__((always_inline)) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r) wa[r] = na[r];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) wb[c] = nb[c];
+        auto scale_b = [&](int to, int st, uint32_t mask, int c) __attribute__((always_inline)) {
+            wb[to][c] = scale(lane_s + (uint32_t)(BS + st * (BN * 8) + (n0 + 16 * c) * 8), mask);
         };
-        auto products = [&](auto jc, auto &&after) __attribute__((always_inline)) {
-            constexpr int J = decltype(jc)::value, set = J & 1;
+        auto load = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
+            for (int j = 0; j < 4; ++j) issue_a(st, st, j);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r][c] = mfma_mx4<J>(fb[set][c], fa[set][r], acc[r][c], wb[c], wa[r]);
-                __builtin_amdgcn_sched_barrier(0);
-                after(c);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int j = 0; j < LB; ++j) issue_b(st, st, j);
+            issue_scales(st, st);
         };
-        auto nothing = [](int) {};
-        auto load = [&](int st, int s) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) issue_a(st, s, j);
-#pragma unroll
-            for (int j = 0; j < LB; ++j) issue_b(st, s, j);
-            issue_scales(st, s);
-        };
-        load(0, 0);
-        load(1, 1);
+        load(0);
+        load(1);
         wait_vm<6 + LB, 6 + LB>(6 + LB);
         __syncthreads();
-        read_frags(0, 0, 0);
-        read_scales(0, 0);
-        take_scales();
+        uint32_t mask = steps == 1 ? keep : 0xFFFFu;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) read_b(0, 0, c), scale_b(0, 0, mask, c);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) read_a(0, 0, r), scale_a(0, mask, r);
+        read_a(0, 1, 0);
+        read_a(0, 1, 1);
         for (int s = 0; s < steps; ++s) {
             const int st = s & 1;
-            read_frags(1, st, 1);
-            products(std::integral_constant<int, 0>{}, nothing);
-            read_frags(0, st, 2);
-            products(std::integral_constant<int, 1>{}, nothing);
-            read_frags(1, st, 3);
-            products(std::integral_constant<int, 2>{}, nothing);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                if (r < 2) {
+                    read_b(st, 1, 2 * r);
+                    read_b(st, 1, 2 * r + 1);
+                }
+                if (r + 2 < RT) read_a(st, 1, r + 2);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) acc[r][c] = mfma_mx4<0>(fb[0][c], fa[0][r], acc[r][c], wb[0][c], wa[r]);
+            }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
             wait_vm<0, 0>(0);                                     // step s + 1 has landed
             __syncthreads();
-            read_frags(0, st ^ 1, 0);
-            read_scales(st ^ 1, s + 1);
-            products(std::integral_constant<int, 3>{}, [&](int c) __attribute__((always_inline)) {
+            mask = s + 1 == steps - 1 ? keep : 0xFFFFu;
 #pragma unroll
-                for (int j = 0; j < (c == 0 ? 4 : LB); ++j) {
-                    if (c == 0) issue_a(st, s + 2, j);
-                    else issue_b(st, s + 2, j);
+            for (int r = 0; r < RT; ++r) {
+                if (r < 2) {
+#pragma unroll
+                    for (int c = 2 * r; c < 2 * r + 2; ++c) read_b(st ^ 1, 0, c), scale_b(1, st ^ 1, mask, c);
                 }
-                if (c == 1) issue_scales(st, s + 2);
-            });
-            take_scales();
+                read_a(st ^ 1, 0, r);
+#pragma unroll
+                for (int j = r * 4 / RT; j < (r + 1) * 4 / RT; ++j) issue_a(st, s + 2, j);
+#pragma unroll
+                for (int j = r * LB / RT; j < (r + 1) * LB / RT; ++j) issue_b(st, s + 2, j);
+                if (r == 0) issue_scales(st, s + 2);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) acc[r][c] = mfma_mx4<1>(fb[1][c], fa[1][r], acc[r][c], wb[0][c], wa[r]);
+                scale_a(st ^ 1, mask, r);
+                if (r >= RT - 2) read_a(st ^ 1, 1, r - (RT - 2));
+            }
+#pragma unroll
+            for (int c = 0; c < CT; ++c) wb[0][c] = wb[1][c];
         }
         wait_vm<0, 0>(0);
     }
@@ -302,7 +300,7 @@ int32_t launched(const char *what) {
 }
 
 // 256 x 256 tiles with 8 waves where the groups fill them, else 128 x 128 with 4, two work-groups a CU. 16384 rows of 8
-// experts, 4096 -> 4096: 181 us against 200; 8 rows, 4096 -> 14336 (weights' bytes): 42 us with the small tile.
+// experts, 4096 -> 4096: 161 us against 190; 8 rows, 4096 -> 14336 (weights' bytes): 42 us with the small tile.
 bool wide(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 + 1) * ((cols + 255) / 256) >= 192; }
 
 }  // namespace
