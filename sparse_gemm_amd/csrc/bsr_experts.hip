@@ -551,6 +551,8 @@ int32_t launch_expert_plan(const int32_t *index, int T, int k, int E, int32_t *o
 
 int32_t launch_combine_fwd(const uint16_t *Y, int T, int k, int N, const int32_t *slot_row, const float *weight,
                            uint16_t *out, void *stream) {
+    // as many outputs of 8 columns as the other operators' grids hold, whatever the pieces of a row round up to
+    if (const int32_t bad = check_grid(((int64_t)T * (N / 8) + 255) / 256, 256, "bsr_expert_combine_fwd")) return bad;
     const int pieces = (N + 511) / 512;
     const dim3 grid((unsigned)((std::min(T, kCombineTokens) * pieces + 3) / 4),
                     (unsigned)((T + kCombineTokens - 1) / kCombineTokens));
