@@ -6,11 +6,12 @@
 //     weight grad   m output column, n input column, c row:   A = dY[c][m],   B = x(c)[n]
 // Work-groups find their expert and rows from offsets on the device.
 //
-// Large products are bound by the matrix cores' rate at the clock that the power allows. 16384 tokens, k = 2 of 8
-// experts, 4096 -> 11008: 2.37 ms, 1.25 PFLOP/s; one dense 16384 x 4096 -> 4096: 393 us, 1.40 PFLOP/s (the matrix
-// instructions alone, on random data: 2.1). Copies that skip work, of a dense 16384 x 16384 -> 4096 in 1591 us: no loads in the loop 1079, no
-// waits for loads 1579, no barrier 1518, no LDS reads 1347: the 64 KB a step through L2, not their latency, cost most. Gradients of 8192 tokens, k = 2 of 8, 4096 -> 4096:
-// input 464 us (1.19 PFLOP/s), weight 459 us (1.20). Ragged groups cost partly empty tiles and the last round of tiles.
+// Large products are bound by the matrix cores and, beside them, by the 64 KB a step that come through L2. 16384 tokens,
+// k = 2 of 8 experts, 4096 -> 11008: 2.29 ms, 1.29 PFLOP/s; one dense 16384 x 4096 -> 4096: 393 us, 1.40 PFLOP/s (the
+// matrix instructions alone, on random data: 2.1). Copies that skip work, of a dense 16384 x 16384 -> 4096 in 1591 us: no loads
+// in the loop 1079, no waits for loads 1579, no barrier 1518, no LDS reads 1347: the loads' rate, not their latency.
+// Gradients of 8192 tokens, k = 2 of 8, 4096 -> 4096: input 464 us (1.19 PFLOP/s), weight 459 us (1.20). Ragged groups
+// cost partly empty tiles and the last round of tiles.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
