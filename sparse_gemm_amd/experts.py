@@ -129,9 +129,13 @@ PLAN_SLOTS = 1024   # BSR_EXPERT_PLAN_SLOTS: up to here a plan needs no workspac
 
 class ExpertPlan:
     """Which rows belong to which expert, on the device: offsets [E+1], row_token [T*k], slot_row [T, k] (int32).
-    The three tensors are not to be replaced or moved afterwards (their addresses are kept)."""
+    The plan keeps the three tensors and every call asks them for their addresses, so that a copy (copy, deepcopy, pickle)
+    works on its own memory; copies are checked like plans from tensors."""
 
-    __slots__ = ("offsets", "row_token", "slot_row", "T", "k", "E", "R", "device", "_offsets", "_token", "_row")
+    __slots__ = ("_offsets", "_token", "_row", "T", "k", "E", "R", "device")
+    offsets = property(lambda self: self._offsets)
+    row_token = property(lambda self: self._token)
+    slot_row = property(lambda self: self._row)
 
     def __init__(self, offsets: torch.Tensor, row_token: torch.Tensor, slot_row: torch.Tensor):
         d = offsets.get_device()
@@ -140,10 +144,13 @@ class ExpertPlan:
         T, k = sizes(slot_row, "slot_row", 2)
         E = sizes(offsets, "offsets", 1)[0] - 1
         self.T, self.k, self.R, self.E, self.device = T, k, T * k, E, d
-        self._offsets = pointer(offsets, "offsets", (E + 1,), _I32, d)
-        self._token = pointer(row_token, "row_token", (T * k,), _I32, d)
-        self._row = pointer(slot_row, "slot_row", (T, k), _I32, d)
-        self.offsets, self.row_token, self.slot_row = offsets, row_token, slot_row
+        pointer(offsets, "offsets", (E + 1,), _I32, d)
+        pointer(row_token, "row_token", (T * k,), _I32, d)
+        pointer(slot_row, "slot_row", (T, k), _I32, d)
+        self._offsets, self._token, self._row = offsets, row_token, slot_row
+
+    def __reduce__(self):
+        return type(self), (self._offsets, self._token, self._row)
 
     @classmethod
     def from_index(cls, index: torch.Tensor, E: int) -> "ExpertPlan":
@@ -156,15 +163,15 @@ class ExpertPlan:
         ip = pointer(index, "index", (T, k), _I32, d)
         self = cls.__new__(cls)
         self.T, self.k, self.R, self.E, self.device = T, k, R, E, d
-        self.offsets = o = empty_strided((max(E, 0) + 1,), (1,), _I32)
-        self.row_token = t = empty_strided((R,), (1,), _I32)
-        self.slot_row = s = new2(T, k, _I32)
-        self._offsets, self._token, self._row = op, tp, sp = o.data_ptr(), t.data_ptr(), s.data_ptr()
+        self._offsets = o = empty_strided((max(E, 0) + 1,), (1,), _I32)
+        self._token = t = empty_strided((R,), (1,), _I32)
+        self._row = s = new2(T, k, _I32)
         need, ws = 0, None
         if R > PLAN_SLOTS:
             need = C.bsr_expert_plan_workspace(T, k, E)
             ws = empty_strided((need,), (1,), torch.uint8)
-        status = C.bsr_expert_plan(ip, T, k, E, op, tp, sp, None if ws is None else ws.data_ptr(), need, raw_stream(d))
+        status = C.bsr_expert_plan(ip, T, k, E, o.data_ptr(), t.data_ptr(), s.data_ptr(),
+                                   None if ws is None else ws.data_ptr(), need, raw_stream(d))
         if status:
             _lib.check(status, "bsr_expert_plan")
         return self
@@ -186,7 +193,8 @@ def expert_fwd(plan: ExpertPlan, X: torch.Tensor, W: torch.Tensor, bias: Optiona
         op = out.data_ptr()
     else:
         op = pointer(out, "out", (R, N), _BF16, d)
-    status = C.bsr_expert_fwd(xp, T, R, E, N, K, plan._offsets, plan._token if gather else None, wp, bp, op, raw_stream(d))
+    status = C.bsr_expert_fwd(xp, T, R, E, N, K, plan._offsets.data_ptr(), plan._token.data_ptr() if gather else None,
+                              wp, bp, op, raw_stream(d))
     if status:
         _lib.check(status, "bsr_expert_fwd")
     return out
@@ -206,7 +214,7 @@ def expert_bwd_input(plan: ExpertPlan, dY: torch.Tensor, W: torch.Tensor, out: O
         op = out.data_ptr()
     else:
         op = pointer(out, "out", (R, K), _BF16, d)
-    status = C.bsr_expert_bwd_input(gp, R, E, N, K, plan._offsets, wp, op, raw_stream(d))
+    status = C.bsr_expert_bwd_input(gp, R, E, N, K, plan._offsets.data_ptr(), wp, op, raw_stream(d))
     if status:
         _lib.check(status, "bsr_expert_bwd_input")
     return out
@@ -224,8 +232,8 @@ def expert_bwd_weight(plan: ExpertPlan, dY: torch.Tensor, X: torch.Tensor, gathe
     dW = new3(E, N, K, _BF16) if out is None else out
     op = pointer(dW, "out", (E, N, K), _BF16, d)
     db = new2(E, N, _BF16) if want_dbias else None
-    status = C.bsr_expert_bwd_weight(gp, xp, T, R, E, N, K, plan._offsets, plan._token if gather else None, op,
-                                     db.data_ptr() if want_dbias else None, raw_stream(d))
+    status = C.bsr_expert_bwd_weight(gp, xp, T, R, E, N, K, plan._offsets.data_ptr(), plan._token.data_ptr() if gather else None,
+                                     op, db.data_ptr() if want_dbias else None, raw_stream(d))
     if status:
         _lib.check(status, "bsr_expert_bwd_weight")
     return dW, db
@@ -246,7 +254,7 @@ def combine_fwd(plan: ExpertPlan, Y: torch.Tensor, weight: Optional[torch.Tensor
         op = out.data_ptr()
     else:
         op = pointer(out, "out", (T, N), _BF16, d)
-    status = C.bsr_expert_combine_fwd(yp, T, k, N, plan._row, wp, op, raw_stream(d))
+    status = C.bsr_expert_combine_fwd(yp, T, k, N, plan._row.data_ptr(), wp, op, raw_stream(d))
     if status:
         _lib.check(status, "bsr_expert_combine_fwd")
     return out
@@ -263,8 +271,8 @@ def combine_bwd(plan: ExpertPlan, dout: torch.Tensor, Y: torch.Tensor,
     yp = pointer(Y, "Y", (R, N), _BF16, d)
     wp = None if weight is None else pointer(weight, "weight", (T, k), _F32, d)
     dY, dw = new2(R, N, _BF16), new2(T, k, _F32)
-    status = C.bsr_expert_combine_bwd(gp, yp, T, k, plan.E, N, plan._offsets, plan._row, wp, dY.data_ptr(), dw.data_ptr(),
-                                      raw_stream(d))
+    status = C.bsr_expert_combine_bwd(gp, yp, T, k, plan.E, N, plan._offsets.data_ptr(), plan._row.data_ptr(), wp,
+                                      dY.data_ptr(), dw.data_ptr(), raw_stream(d))
     if status:
         _lib.check(status, "bsr_expert_combine_bwd")
     return dY, dw

@@ -118,15 +118,15 @@ def expert_fwd(plan: ExpertPlan, X: Union[torch.Tensor, Mx4], W: Mx4, bias: Opti
         op = out.data_ptr()
     else:
         op = pointer(out, "out", (R, N), _BF16, d)
-    token = plan._token if gather else None
+    token = plan._token.data_ptr() if gather else None
     if isinstance(X, Mx4):
         xc = pointer(X.codes, "X.codes", (rows, half), _U8, d)
         xs = pointer(X.scales, "X.scales", (chunks(K), rows, 8), _U8, d)
-        status = C.bsr_expert_fwd_mx4_mx4(xc, xs, T, R, E, N, K, plan._offsets, token, cp, sp, bp, op, raw_stream(d))
+        status = C.bsr_expert_fwd_mx4_mx4(xc, xs, T, R, E, N, K, plan._offsets.data_ptr(), token, cp, sp, bp, op, raw_stream(d))
         what = "bsr_expert_fwd_mx4_mx4"
     else:
         xp = pointer(X, "X", (rows, K), _BF16, d)
-        status = C.bsr_expert_fwd_mx4(xp, T, R, E, N, K, plan._offsets, token, cp, sp, bp, op, raw_stream(d))
+        status = C.bsr_expert_fwd_mx4(xp, T, R, E, N, K, plan._offsets.data_ptr(), token, cp, sp, bp, op, raw_stream(d))
         what = "bsr_expert_fwd_mx4"
     if status:
         _lib.check(status, what)

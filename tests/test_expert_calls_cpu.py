@@ -1,0 +1,96 @@
+"""What the Python face of the expert layers passes to the library, without a GPU: tensors on the CPU pass for
+tensors on GPU 0, and a stand-in for the library records the arguments of each call."""
+import copy
+import pickle
+
+import pytest
+import torch
+
+from sparse_gemm_amd import experts, mx4
+from sparse_gemm_amd.experts import ExpertPlan
+
+
+class Recorder:
+    """Every function returns status 0 and leaves (name, arguments) in `calls`."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    rec = Recorder()
+    for module in (experts, mx4):
+        monkeypatch.setattr(module, "C", rec)
+        monkeypatch.setattr(module, "current_device", lambda: 0)
+        monkeypatch.setattr(module, "raw_stream", lambda d: None)
+        monkeypatch.setattr(module, "empty_strided", lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype))
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    return rec
+
+
+def bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def a_plan(T=4, k=2, E=3):
+    return ExpertPlan(torch.zeros(E + 1, dtype=torch.int32), torch.zeros(T * k, dtype=torch.int32),
+                      torch.zeros((T, k), dtype=torch.int32))
+
+
+def plan_calls(plan):
+    """Every call that takes a plan, as (the call, the plan's tensors that it passes)."""
+    T, k, E, R, N, K = plan.T, plan.k, plan.E, plan.R, 64, 64
+    W, q = bf(E, N, K), mx4.Mx4(torch.zeros((E, N, K // 2), dtype=torch.uint8), torch.zeros((E, 1, N, 8), dtype=torch.uint8))
+    x4 = mx4.Mx4(torch.zeros((T, K // 2), dtype=torch.uint8), torch.zeros((1, T, 8), dtype=torch.uint8))
+    return [(lambda: experts.expert_fwd(plan, bf(T, K), W), ("offsets", "row_token")),
+            (lambda: experts.expert_fwd(plan, bf(R, K), W, gather=False), ("offsets",)),
+            (lambda: experts.expert_bwd_input(plan, bf(R, N), W), ("offsets",)),
+            (lambda: experts.expert_bwd_weight(plan, bf(R, N), bf(T, K)), ("offsets", "row_token")),
+            (lambda: experts.combine_fwd(plan, bf(R, N)), ("slot_row",)),
+            (lambda: experts.combine_bwd(plan, bf(T, N), bf(R, N)), ("offsets", "slot_row")),
+            (lambda: mx4.expert_fwd(plan, bf(T, K), q), ("offsets", "row_token")),
+            (lambda: mx4.expert_fwd(plan, x4, q), ("offsets", "row_token"))]
+
+
+def built(library):
+    return ExpertPlan.from_index(torch.zeros((4, 2), dtype=torch.int32), 3)
+
+
+@pytest.mark.parametrize("make", [lambda library: a_plan(), built], ids=["tensors", "index"])
+@pytest.mark.parametrize("copied", [copy.copy, copy.deepcopy, lambda p: pickle.loads(pickle.dumps(p)),
+                                    lambda p: copy.deepcopy({"plan": [p]})["plan"][0]], ids=["copy", "deepcopy", "pickle", "nested"])
+def test_a_copied_plan_passes_its_own_memory(library, make, copied):
+    original = make(library)
+    plan = copied(original)
+    assert (plan.T, plan.k, plan.E, plan.R, plan.device) == (4, 2, 3, 8, 0)
+    for call, names in plan_calls(plan):
+        library.calls.clear()
+        call()
+        (name, args), = library.calls
+        for n in names:
+            assert getattr(plan, n).data_ptr() in args, (name, n)
+        if copied is not copy.copy:
+            for n in ("offsets", "row_token", "slot_row"):
+                assert getattr(original, n).data_ptr() not in args, (name, n)
+
+
+def test_a_plan_keeps_its_tensors(library):
+    plan = a_plan()
+    for n in ("offsets", "row_token", "slot_row"):
+        with pytest.raises(AttributeError):
+            setattr(plan, n, torch.zeros(1, dtype=torch.int32))
+
+
+def test_a_plan_without_its_gpu_is_refused(library, monkeypatch):
+    """A plan's copy is checked like a plan from tensors: one whose tensors came back on the CPU is no plan."""
+    data = pickle.dumps(a_plan())
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: -1)
+    with pytest.raises(ValueError):
+        pickle.loads(data)
