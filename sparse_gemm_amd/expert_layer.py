@@ -1,5 +1,6 @@
 """ExpertFFN: a feed-forward layer whose tokens each use k of E experts, with autograd over the library's
-router, grouped products and sum; its experts can be held in 4 bits for serving."""
+router, grouped products and sum; its experts can be held in 4 bits for serving. Gradients of the first order: a second
+derivative raises."""
 from __future__ import annotations
 
 import math
@@ -10,6 +11,7 @@ from torch import nn
 from torch.nn import functional as F
 
 from . import experts, mx4
+from .autograd import first_order
 from .experts import ExpertPlan
 
 
@@ -23,6 +25,7 @@ class _RouteFn(torch.autograd.Function):
         return index, weight
 
     @staticmethod
+    @first_order
     def backward(ctx, _, dweight):
         logits, index, weight = ctx.saved_tensors
         return experts.router_bwd(logits, index, weight, dweight.float().contiguous(), ctx.renormalize), None, None
@@ -41,6 +44,7 @@ class _ExpertLinearFn(torch.autograd.Function):
         return experts.expert_fwd(plan, x, W, bias, gather)
 
     @staticmethod
+    @first_order
     def backward(ctx, dY):
         x, W = ctx.saved_tensors
         plan = ctx.plan
@@ -69,6 +73,7 @@ class _CombineFn(torch.autograd.Function):
         return experts.combine_fwd(plan, Y, weight)
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         Y, weight = ctx.saved_tensors
         dY, dw = experts.combine_bwd(ctx.plan, dout.to(torch.bfloat16).contiguous(), Y, weight)
