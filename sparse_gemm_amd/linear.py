@@ -17,6 +17,7 @@ import torch
 from torch import nn
 
 from . import binding
+from .autograd import first_order
 from .binding import Pattern
 
 
@@ -29,6 +30,7 @@ class _BsrLinearFn(torch.autograd.Function):
         return binding.linear_fwd(pattern, x2d, values, bias)
 
     @staticmethod
+    @first_order
     def backward(ctx, dY: torch.Tensor):
         x2d, values = ctx.saved_tensors
         p = ctx.pattern
