@@ -56,6 +56,12 @@ def _quantize(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, values
         _lib.check(status, "bsr_mx4_quantize")
 
 
+def _own_piece(c: int, rows: int) -> Optional[torch.Tensor]:
+    """Where one expert's scales [c, rows, 8] stand during a call, if they do not lie on whole 16 bytes among all experts'
+    (c * rows odd): the library takes 16-byte aligned arrays."""
+    return new3(c, rows, 8, _U8) if c * rows % 2 else None
+
+
 def quantize(X: torch.Tensor, want_values: bool = False):
     """Mx4 of X [rows, K] or [E, rows, K] (bf16, K a multiple of 32) via bsr_mx4_quantize. want_values: also the
     bf16 values that the codes stand for (X [rows, K] only), as (Mx4, values)."""
@@ -70,8 +76,11 @@ def quantize(X: torch.Tensor, want_values: bool = False):
         c = chunks(K)
         codes = new3(E, rows, K // 2, _U8)
         scales = empty_strided((E, c, rows, 8), (c * rows * 8, rows * 8, 8, 1), _U8)
+        own = _own_piece(c, rows)
         for e in range(E):
-            _quantize(X[e], codes[e], scales[e], None, d)
+            _quantize(X[e], codes[e], scales[e] if own is None else own, None, d)
+            if own is not None:
+                scales[e].copy_(own)
         return Mx4(codes, scales)
     rows, K = sizes(X, "X", 2)
     pointer(X, "X", (rows, K), _BF16, d)
@@ -93,9 +102,12 @@ def dequantize(q: Mx4) -> torch.Tensor:
     cp = pointer(q.codes, "codes", (*lead, rows, half), _U8, d)
     sp = pointer(q.scales, "scales", (*lead, chunks(K), rows, 8), _U8, d)
     out = torch.empty((*lead, rows, K), dtype=_BF16, device=q.codes.device)
+    own = _own_piece(chunks(K), rows) if lead else None
     for e in range(lead[0] if lead else 1):
-        status = C.bsr_mx4_dequantize(cp + e * rows * half, sp + e * chunks(K) * rows * 8, rows, K,
-                                      out.data_ptr() + e * rows * K * 2, raw_stream(d))
+        if own is not None:
+            own.copy_(q.scales[e])
+        status = C.bsr_mx4_dequantize(cp + e * rows * half, sp + e * chunks(K) * rows * 8 if own is None else own.data_ptr(),
+                                      rows, K, out.data_ptr() + e * rows * K * 2, raw_stream(d))
         if status:
             _lib.check(status, "bsr_mx4_dequantize")
     return out

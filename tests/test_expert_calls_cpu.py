@@ -1,6 +1,7 @@
 """What the Python face of the expert layers passes to the library, without a GPU: tensors on the CPU pass for
 tensors on GPU 0, and a stand-in for the library records the arguments of each call."""
 import copy
+import ctypes
 import pickle
 
 import pytest
@@ -94,3 +95,30 @@ def test_a_plan_without_its_gpu_is_refused(library, monkeypatch):
     monkeypatch.setattr(torch.Tensor, "get_device", lambda self: -1)
     with pytest.raises(ValueError):
         pickle.loads(data)
+
+
+@pytest.mark.parametrize("E,rows,K", [(3, 5, 32), (3, 41, 32), (2, 3, 256), (3, 7, 544), (1, 3, 32), (3, 5, 288), (3, 40, 320), (2, 0, 32)])
+def test_every_experts_scales_are_aligned(library, E, rows, K):
+    """[E, rows, K] goes to the library expert by expert, whose scales need not lie on whole 16 bytes among all experts'.
+    Stand-ins write the expert's number into its scales, and read it."""
+    c, n = mx4.chunks(K), rows * mx4.chunks(K) * 8
+    read = []
+
+    def quantize(x, r, k, codes, scales, values, stream):
+        assert (r, k) == (rows, K) and x % 16 == codes % 16 == scales % 16 == 0
+        ctypes.memset(scales, len(library.calls) + 1, n)
+        library.calls.append(scales)
+        return 0
+
+    def dequantize(codes, scales, r, k, values, stream):
+        assert (r, k) == (rows, K) and codes % 16 == scales % 16 == values % 16 == 0
+        read.append(ctypes.string_at(scales, n))
+        return 0
+
+    library.bsr_mx4_quantize, library.bsr_mx4_dequantize = quantize, dequantize
+    q = mx4.quantize(bf(E, rows, K))
+    assert len(library.calls) == E and q.scales.shape == (E, c, rows, 8)
+    for e in range(E):
+        assert (q.scales[e] == e + 1).all()
+    mx4.dequantize(q)
+    assert read == [bytes([e + 1]) * n for e in range(E)]
