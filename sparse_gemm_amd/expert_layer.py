@@ -15,6 +15,13 @@ from .autograd import first_order
 from .experts import ExpertPlan
 
 
+def _whole(t: torch.Tensor) -> torch.Tensor:
+    """t as the library takes it: contiguous and 16-byte aligned. A slice of odd sizes (of [T, k], of logits with an odd E, or the
+    gradient of a concatenation's part) is contiguous without being aligned."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class _RouteFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, renormalize):
@@ -28,12 +35,12 @@ class _RouteFn(torch.autograd.Function):
     @first_order
     def backward(ctx, _, dweight):
         logits, index, weight = ctx.saved_tensors
-        return experts.router_bwd(logits, index, weight, dweight.float().contiguous(), ctx.renormalize), None, None
+        return experts.router_bwd(logits, index, weight, _whole(dweight.float()), ctx.renormalize), None, None
 
 
 def route(logits: torch.Tensor, k: int, renormalize: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
     """(index [T, k], weight [T, k]) of logits [T, E]; weight carries the gradient."""
-    return _RouteFn.apply(logits.contiguous(), k, renormalize)
+    return _RouteFn.apply(_whole(logits), k, renormalize)
 
 
 class _ExpertLinearFn(torch.autograd.Function):
@@ -48,7 +55,7 @@ class _ExpertLinearFn(torch.autograd.Function):
     def backward(ctx, dY):
         x, W = ctx.saved_tensors
         plan = ctx.plan
-        dY = dY.to(torch.bfloat16).contiguous()
+        dY = _whole(dY.to(torch.bfloat16))
         dX = dW = db = None
         if ctx.needs_input_grad[0]:
             dX = experts.expert_bwd_input(plan, dY, W)
@@ -62,7 +69,7 @@ class _ExpertLinearFn(torch.autograd.Function):
 def expert_linear(plan: ExpertPlan, x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
                   gather: bool = True) -> torch.Tensor:
     """Rows [R, N] of x [T, K] (gather) or [R, K] times each expert's W [E, N, K], with gradients."""
-    return _ExpertLinearFn.apply(x.contiguous(), W, bias, plan, gather)
+    return _ExpertLinearFn.apply(_whole(x), W, bias, plan, gather)
 
 
 class _CombineFn(torch.autograd.Function):
@@ -76,13 +83,13 @@ class _CombineFn(torch.autograd.Function):
     @first_order
     def backward(ctx, dout):
         Y, weight = ctx.saved_tensors
-        dY, dw = experts.combine_bwd(ctx.plan, dout.to(torch.bfloat16).contiguous(), Y, weight)
+        dY, dw = experts.combine_bwd(ctx.plan, _whole(dout.to(torch.bfloat16)), Y, weight)
         return dY, dw, None
 
 
 def combine(plan: ExpertPlan, Y: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
     """out [T, N]: a token's rows of Y [R, N], weighted and summed, with gradients."""
-    return _CombineFn.apply(Y.contiguous(), weight.contiguous(), plan)
+    return _CombineFn.apply(_whole(Y), _whole(weight), plan)
 
 
 class ExpertFFN(nn.Module):
@@ -133,7 +140,7 @@ class ExpertFFN(nn.Module):
         if self.quantized and torch.is_grad_enabled() and x.requires_grad:
             raise RuntimeError("a quantised ExpertFFN has no backward pass")
         lead = x.shape[:-1]
-        x = x.reshape(-1, self.dim).to(torch.bfloat16).contiguous()
+        x = _whole(x.reshape(-1, self.dim).to(torch.bfloat16))
         index, weight = route(F.linear(x, self.router), self.k, self.renormalize)
         plan = ExpertPlan.from_index(index, self.num_experts)
         if not self.quantized:

@@ -7,7 +7,7 @@ import pickle
 import pytest
 import torch
 
-from sparse_gemm_amd import experts, mx4
+from sparse_gemm_amd import expert_layer, experts, mx4
 from sparse_gemm_amd.experts import ExpertPlan
 
 
@@ -122,3 +122,51 @@ def test_every_experts_scales_are_aligned(library, E, rows, K):
         assert (q.scales[e] == e + 1).all()
     mx4.dequantize(q)
     assert read == [bytes([e + 1]) * n for e in range(E)]
+
+
+def off_by_one(t):
+    """t's values in contiguous memory that is not 16-byte aligned."""
+    flat = torch.empty(t.numel() + 8, dtype=t.dtype)
+    at = 1 if flat.data_ptr() % 16 == 0 else 0
+    v = flat[at:at + t.numel()].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16
+    return v
+
+
+def test_autograd_functions_take_contiguous_slices(library, monkeypatch):
+    """Slices of odd sizes are contiguous and not 16-byte aligned, which the library refuses: inputs, and incoming gradients
+    (the gradient of a concatenation's part is such a slice), are copied where that is so."""
+    T, k, E, N, K = 3, 1, 3, 64, 64
+
+    def aligned(rec, name):
+        def call(*args):
+            rec.calls.append(name)
+            bad = [a for a in args if isinstance(a, int) and a > 1 << 20 and a % 16]
+            assert not bad, name
+            return 0
+        return call
+
+    monkeypatch.setattr(Recorder, "__getattr__", aligned)
+    plan = a_plan(T, k, E)
+    logits = off_by_one(torch.zeros(T, E)).requires_grad_()
+    index, weight = expert_layer.route(logits, k)
+    weight.backward(off_by_one(torch.ones(T, k)))
+    x, W, b = off_by_one(bf(T, K)).requires_grad_(), bf(E, N, K).requires_grad_(), bf(E, N).requires_grad_()
+    expert_layer.expert_linear(plan, x, W, b).backward(off_by_one(bf(T * k, N)))
+    y, w = off_by_one(bf(T * k, N)).requires_grad_(), off_by_one(torch.ones(T, k)).requires_grad_()
+    expert_layer.combine(plan, y, w).backward(off_by_one(bf(T, N)))
+    assert library.calls == ["bsr_router_fwd", "bsr_router_bwd", "bsr_expert_fwd", "bsr_expert_bwd_input", "bsr_expert_combine_fwd",
+                             "bsr_expert_bwd_weight", "bsr_expert_combine_fwd", "bsr_expert_combine_bwd"]
+
+
+def test_autograd_functions_do_not_copy_aligned_tensors(library):
+    plan, T, N = a_plan(4, 2, 3), 4, 64
+    x, W, y, w = bf(T, N), bf(3, N, N), bf(8, N), torch.ones(4, 2)
+    logits = torch.zeros(4, 3)
+    expert_layer.route(logits, 2)
+    expert_layer.expert_linear(plan, x, W)
+    expert_layer.combine(plan, y, w)
+    for (name, args), tensors in zip(library.calls, ([logits], [x, W], [y, w])):
+        for t in tensors:
+            assert t.data_ptr() in args, name

@@ -1,0 +1,48 @@
+"""The autograd functions of the expert layers on slices, on frozen weights and under torch's transforms."""
+import pytest
+import torch
+
+from gpu_util import dev
+from sparse_gemm_amd import expert_layer, experts
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def test_slices_give_the_results_of_whole_tensors():
+    """Logits, activations, rows and weights at an odd offset of a larger tensor, and gradients that are slices of a
+    concatenation's: bit for bit what aligned copies give."""
+    T, k, E, N, K = 5, 1, 3, 24, 40
+    g = gen(0)
+
+    def both(*shape, dtype=torch.bfloat16):
+        whole = torch.randn(shape, generator=g).to(dtype).to(dev())
+        flat = torch.empty(whole.numel() + 1, dtype=dtype, device=dev())
+        flat[1:] = whole.flatten()
+        part = flat[1:].view(shape)
+        assert part.is_contiguous() and part.data_ptr() % 16
+        return whole.requires_grad_(), part.requires_grad_()
+
+    logits, x, y, w = both(T, E, dtype=torch.float32), both(T, K), both(T * k, N), both(T, k, dtype=torch.float32)
+    W = torch.randn(E, N, K, generator=g).bfloat16().to(dev())
+    lead = torch.ones(T, k, device=dev(), requires_grad=True)
+    results = []
+    for i in (0, 1):
+        index, weight = expert_layer.route(logits[i], k, renormalize=False)
+        plan = experts.ExpertPlan.from_index(index, E)
+        rows = expert_layer.expert_linear(plan, x[i], W)
+        out = expert_layer.combine(plan, y[i], w[i])
+        # in a concatenation the gradient of `weight` is the last T * k of 2 T * k elements
+        up = torch.arange(2 * T * k, dtype=torch.float32, device=dev()).view(2 * T, k)
+        if i:
+            (torch.cat([lead, weight]) * up).sum().backward()
+        else:
+            (weight * up[T:]).sum().backward()
+        rows.float().square().sum().backward()
+        out.float().square().sum().backward()
+        results.append([index, weight, rows, out, logits[i].grad, x[i].grad, y[i].grad, w[i].grad])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
