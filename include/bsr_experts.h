@@ -20,9 +20,10 @@
  *
  * The kernels clamp what they read from offsets to [0, R] and drop tokens and rows out of range, so
  * a plan that does not hold these invariants gives wrong results but no access out of bounds.
- * Size limits (BSR_ERR_INVALID_ARG beyond them): R <= 2^24; X and one expert's weight each at most
- * 0xF0000000 bytes (so does dY in the weight gradient); N and K below 2^20 and multiples of 8 (rows of 16-byte
- * pieces); less than 2^32 threads a launch. All experts' weights together may be of any size.
+ * Size limits (BSR_ERR_INVALID_ARG beyond them): R <= 2^24; at most 0xF0000000 bytes for one expert's weight, for an X
+ * whose rows are gathered by token, and for X and dY of the weight gradient; N and K below 2^20 and multiples of 8 (rows
+ * of 16-byte pieces); less than 2^32 threads a launch. Sorted rows (X of the forward without row_token, dY of the input
+ * gradient), results, and all experts' weights together may be of any size.
  */
 #ifndef BSR_EXPERTS_H
 #define BSR_EXPERTS_H

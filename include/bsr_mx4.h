@@ -44,13 +44,13 @@ int32_t bsr_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t 
 
 /* bsr_expert_fwd with 4-bit weights: Y[r] = x(r) . W4[e]^T + bias[e], bf16 activations, fp32 sums.
  * codes [E][N][K/2], scales [E][ceil(K/256)][N][8]; K a multiple of 32, N of 8. The plain linear layer is
- * E = 1 with offsets {0, R}. */
+ * E = 1 with offsets {0, R}. X, gathered or sorted, at most 0xF0000000 bytes. */
 int32_t bsr_expert_fwd_mx4(const bsr_bf16 *X, int64_t T, int64_t R, int32_t E, int32_t N, int32_t K,
                            const int32_t *offsets, const int32_t *row_token, const uint8_t *codes,
                            const uint8_t *scales, const bsr_bf16 *bias, bsr_bf16 *Y, void *stream);
 
 /* The same with both sides in 4 bits: x(r) is the row of xcodes [T or R][K/2] and
- * xscales [ceil(K/256)][T or R][8]. Products of codes and scales are exact, sums are fp32. */
+ * xscales [ceil(K/256)][T or R][8], xcodes at most 0xF0000000 bytes. Products of codes and scales are exact, sums are fp32. */
 int32_t bsr_expert_fwd_mx4_mx4(const uint8_t *xcodes, const uint8_t *xscales, int64_t T, int64_t R, int32_t E,
                                int32_t N, int32_t K, const int32_t *offsets, const int32_t *row_token,
                                const uint8_t *codes, const uint8_t *scales, const bsr_bf16 *bias, bsr_bf16 *Y,

@@ -41,8 +41,9 @@ int32_t check_logits(int32_t type, int32_t renormalize) {
     return BSR_OK;
 }
 
-// Sizes of a grouped product; bits: 16 or 4 per activation, wbits per weight.
-int32_t check_product(int64_t T, int64_t R, int32_t E, int32_t N, int32_t K, bool gathered, int bits, int wbits) {
+// Sizes of a grouped product; bits: 16 or 4 per activation, wbits per weight. by_tile: activations that are not gathered are
+// read behind a descriptor of a tile's rows, so that their size has no limit.
+int32_t check_product(int64_t T, int64_t R, int32_t E, int32_t N, int32_t K, bool gathered, int bits, int wbits, bool by_tile) {
     if (E < 1 || E > kMaxExperts) return fail(BSR_ERR_INVALID_ARG, "E must lie in [1, 1024], got " + std::to_string(E));
     if (R < 0 || R > kMaxExpertRows) return fail(BSR_ERR_INVALID_ARG, "R must lie in [0, 2^24]");
     if (gathered && (T < 0 || T > kMaxExpertRows)) return fail(BSR_ERR_INVALID_ARG, "T must lie in [0, 2^24]");
@@ -50,7 +51,7 @@ int32_t check_product(int64_t T, int64_t R, int32_t E, int32_t N, int32_t K, boo
     const int kstep = wbits == 4 ? 32 : 8;
     if (K < kstep || K % kstep || K >= (1 << 20))
         return fail(BSR_ERR_INVALID_ARG, "K must be a positive multiple of " + std::to_string(kstep) + " below 2^20");
-    const uint64_t rows = gathered ? (uint64_t)T : (uint64_t)R;
+    const uint64_t rows = gathered ? (uint64_t)T : by_tile ? 0 : (uint64_t)R;
     if (rows * K * bits / 8 > kMaxOperandBytes)
         return fail(BSR_ERR_INVALID_ARG, "activations of more than 0xF0000000 bytes");
     if ((uint64_t)N * K * wbits / 8 > kMaxOperandBytes)
@@ -130,7 +131,7 @@ int32_t bsr_expert_fwd(const bsr_bf16 *X, int64_t T, int64_t R, int32_t E, int32
                        const int32_t *offsets, const int32_t *row_token, const bsr_bf16 *W, const bsr_bf16 *bias,
                        bsr_bf16 *Y, void *stream) {
     BSR_TRY_BEGIN
-    BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 16, 16));
+    BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 16, 16, true));
     const bool none = R == 0;
     BSR_CHECK(check_ptrs({{X, "X", none || (row_token && T == 0), 16}, {offsets, "offsets", none, 16},
                           {row_token, "row_token", true, 16}, {W, "W", none, 16}, {bias, "bias", true, 16},
@@ -143,7 +144,7 @@ int32_t bsr_expert_fwd(const bsr_bf16 *X, int64_t T, int64_t R, int32_t E, int32
 int32_t bsr_expert_bwd_input(const bsr_bf16 *dY, int64_t R, int32_t E, int32_t N, int32_t K, const int32_t *offsets,
                              const bsr_bf16 *W, bsr_bf16 *dX, void *stream) {
     BSR_TRY_BEGIN
-    BSR_CHECK(check_product(0, R, E, N, K, false, 16, 16));
+    BSR_CHECK(check_product(0, R, E, N, K, false, 16, 16, true));
     const bool none = R == 0;
     BSR_CHECK(check_ptrs({{dY, "dY", none, 16}, {offsets, "offsets", none, 16}, {W, "W", none, 16}, {dX, "dX", none, 16}}));
     if (none) return BSR_OK;
@@ -155,7 +156,7 @@ int32_t bsr_expert_bwd_weight(const bsr_bf16 *dY, const bsr_bf16 *X, int64_t T, 
                               int32_t K, const int32_t *offsets, const int32_t *row_token, bsr_bf16 *dW,
                               bsr_bf16 *dbias, void *stream) {
     BSR_TRY_BEGIN
-    BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 16, 16));
+    BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 16, 16, false));
     if ((uint64_t)R * N * 2 > kMaxOperandBytes) return fail(BSR_ERR_INVALID_ARG, "dY of more than 0xF0000000 bytes");
     const bool none = R == 0;   // the gradients are then 0
     BSR_CHECK(check_ptrs({{dY, "dY", none, 16}, {X, "X", none || (row_token && T == 0), 16}, {offsets, "offsets", false, 16},
@@ -230,7 +231,7 @@ int32_t bsr_expert_fwd_mx4(const bsr_bf16 *X, int64_t T, int64_t R, int32_t E, i
                            const int32_t *offsets, const int32_t *row_token, const uint8_t *codes,
                            const uint8_t *scales, const bsr_bf16 *bias, bsr_bf16 *Y, void *stream) {
     BSR_TRY_BEGIN
-    BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 16, 4));
+    BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 16, 4, false));
     const bool none = R == 0;
     BSR_CHECK(check_ptrs({{X, "X", none || (row_token && T == 0), 16}, {offsets, "offsets", none, 16},
                           {row_token, "row_token", true, 16}, {codes, "codes", none, 16}, {scales, "scales", none, 16},
@@ -245,7 +246,7 @@ int32_t bsr_expert_fwd_mx4_mx4(const uint8_t *xcodes, const uint8_t *xscales, in
                                const uint8_t *codes, const uint8_t *scales, const bsr_bf16 *bias, bsr_bf16 *Y,
                                void *stream) {
     BSR_TRY_BEGIN
-    BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 4, 4));
+    BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 4, 4, false));
     const bool none = R == 0, nox = none || (row_token && T == 0);
     BSR_CHECK(check_ptrs({{xcodes, "xcodes", nox, 16}, {xscales, "xscales", nox, 16}, {offsets, "offsets", none, 16},
                           {row_token, "row_token", true, 16}, {codes, "codes", none, 16}, {scales, "scales", none, 16},
