@@ -234,12 +234,7 @@ int32_t launch_expert_bwd_input_few(const ExpertShape &s, int mt, const uint16_t
                                     void *stream) {
     const FewArgs g{dY, W, nullptr, nullptr, dX, s.offsets, nullptr, s.T, s.R, s.E, s.K, s.N};
     const char *what = "bsr_expert_bwd_input";
-    // 32 columns a tile (half lines, two work-groups a CU) while tiles of 64 leave half of the CUs without one: one row of
-    // 8 experts, 10744 -> 312: 23 us against 31, one expert, 4096 -> 4096: 10 against 12; where they do not, 4 rows of 64
-    // experts, 1536 -> 2048: 92 against 80.
-    const bool narrow = max_row_tiles(s.R, s.E, 16 * mt) * ((s.K + 63) / 64) <= kCUs / 2;
-    if (narrow && mt == 1) return launch<kColsW, 1, 32, 3>(g, stream, what);
-    if (narrow && mt == 2) return launch<kColsW, 2, 32, 3>(g, stream, what);
+    if (few_cols_bwd_input(mt, s.R, s.E, s.K) == 32) return launch<kColsW, 1, 32, 3>(g, stream, what);
     return mt == 1 ? launch<kColsW, 1, 64, 3>(g, stream, what)
                    : mt == 2 ? launch<kColsW, 2, 64, 3>(g, stream, what) : launch<kColsW, 4, 64, 2>(g, stream, what);
 }
@@ -248,12 +243,8 @@ int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, int mt, const uint16_t *
                                   const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream) {
     const FewArgs g{X, codes, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
     const char *what = "bsr_expert_fwd_mx4";
-    // Up to 16 rows a tile: 32 columns while tiles of 64 leave CUs without one. One row, one expert: 4096 -> 4096 7.5 us
-    // against 9.6, 8192 -> 312 of 8 experts 11.4 against 15.6; where they do not, 4 rows of 32 experts, 2048 -> 1024: 11.0
-    // against 8.9.
-    if (mt == 1 && max_row_tiles(s.R, s.E, 16) * ((s.N + 63) / 64) <= kCUs) return launch<kMx4W, 1, 32, 4>(g, stream, what);
-    return mt == 1 ? launch<kMx4W, 1, 64, 4>(g, stream, what)
-                   : mt == 2 ? launch<kMx4W, 2, 64, 3>(g, stream, what) : launch<kMx4W, 4, 64, 3>(g, stream, what);
+    if (few_cols_mx4(mt, s.R, s.E, s.N) == 32) return launch<kMx4W, 1, 32, 4>(g, stream, what);
+    return mt == 1 ? launch<kMx4W, 1, 64, 4>(g, stream, what) : launch<kMx4W, 2, 64, 3>(g, stream, what);
 }
 
 }  // namespace bsr

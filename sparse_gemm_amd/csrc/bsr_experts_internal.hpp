@@ -30,7 +30,7 @@ int32_t launch_combine_fwd(const uint16_t *Y, int T, int k, int N, const int32_t
 int32_t launch_combine_bwd(const uint16_t *dout, const uint16_t *Y, int T, int k, int E, int N, const int32_t *offsets,
                            const int32_t *slot_row, const float *weight, uint16_t *dY, float *dweight, void *stream);
 
-// What a grouped product reads besides its operands. rows_a: rows of the gathered matrix (T) or R.
+// What a grouped product reads besides its operands. T: rows of the gathered matrix.
 struct ExpertShape {
     int T, R, E, N, K;
     const int32_t *offsets, *row_token;
@@ -84,7 +84,24 @@ constexpr TileKind kBwdInputTiles[] = {{1, 16, 64, 256, 256, 0.65, 0.65}, {2, 32
                                        {4, 64, 64, 256, 256, 1.05, 1.05}, {128, 128, 128, 64, 512, 0.50, 1.00},
                                        {256, 256, 256, 64, 256, 1.60, 1.60}};
 constexpr TileKind kFwdMx4Tiles[] = {{1, 16, 64, 256, 512, 0.45, 0.75}, {2, 32, 64, 256, 512, 0.60, 0.90},
-                                     {4, 64, 64, 256, 256, 0.90, 0.90}, {128, 128, 128, 64, 512, 0.56, 1.00}};
+                                     {128, 128, 128, 64, 512, 0.56, 1.00}};
+
+// Row tiles that R rows in E groups and the rows past the plan can need.
+inline int64_t max_row_tiles(int64_t R, int64_t E, int64_t bm) { return (R + std::min(E + 1, R) * (bm - 1)) / bm; }
+
+// Output columns of a few-row tile of 16 mt rows. Input gradient: 32 (half lines, two work-groups a CU) while tiles of 64 leave
+// half of the 256 CUs without one: one row of 8 experts, 10744 -> 312: 23 us against 31, one expert, 4096 -> 4096: 10 against
+// 12; where they do not, 4 rows of 64 experts, 1536 -> 2048: 92 against 80. (Where tiles of 32 rows would leave as many idle,
+// tiles of 16 are estimated faster.)
+inline int few_cols_bwd_input(int mt, int64_t R, int64_t E, int64_t cols) {
+    return mt == 1 && max_row_tiles(R, E, 16) * ((cols + 63) / 64) <= 128 ? 32 : 64;
+}
+// 4-bit weights, up to 16 rows a tile: 32 while tiles of 64 leave CUs without one. One row, one expert: 4096 -> 4096 7.5 us
+// against 9.6, 8192 -> 312 of 8 experts 11.4 against 15.6; where they do not, 4 rows of 32 experts, 2048 -> 1024: 11.0
+// against 8.9.
+inline int few_cols_mx4(int mt, int64_t R, int64_t E, int64_t cols) {
+    return mt == 1 && max_row_tiles(R, E, 16) * ((cols + 63) / 64) <= 256 ? 32 : 64;
+}
 
 int32_t launch_expert_fwd_few(const ExpertShape &s, int mt, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
                               uint16_t *Y, void *stream);

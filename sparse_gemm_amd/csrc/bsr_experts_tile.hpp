@@ -24,8 +24,6 @@
 namespace bsr {
 namespace dev {
 
-typedef int i32x8 __attribute__((ext_vector_type(8), aligned(4)));
-
 enum Operand { kRows, kCols };
 
 constexpr uint32_t kPast = 0xF0000000u;   // an offset at or past the end of every operand: such a load reads zeros
@@ -450,8 +448,5 @@ __device__ __forceinline__ Piece piece_of(int64_t block, int tiles) {
 }  // namespace dev
 
 constexpr int kPieces = 128;   // work-groups that halves add to a grid: a half round
-
-// Row tiles that R rows in E groups and the rows past the plan can need.
-inline int64_t max_row_tiles(int64_t R, int64_t E, int64_t bm) { return (R + std::min(E + 1, R) * (bm - 1)) / bm; }
 
 }  // namespace bsr
