@@ -88,3 +88,10 @@ def test_every_variant_runs_on_the_gpu(tiles):
     assert set(tiles("f", sizes(PRODUCTS + LARGE + WIDE))) == FWD
     assert set(tiles("b", sizes(PRODUCTS + LARGE + swapped))) == BWD_INPUT
     assert set(tiles("m", sizes(MX_PRODUCTS))) == FWD_MX4
+
+
+def test_halved_tiles_are_tested(tiles):
+    """The GPU test of halved tiles takes sizes whose products run in 256 x 256 tiles, in both directions."""
+    from test_gpu_expert_halves import HALVES, ONE_EXPERT
+    assert set(tiles("f", [(T * k, E, N, K) for _, T, k, E, N, K in HALVES + ONE_EXPERT])) == {(256, 256)}
+    assert set(tiles("b", [(T * k, E, K, N) for _, T, k, E, N, K in HALVES])) == {(256, 256)}
