@@ -129,15 +129,17 @@ class ExpertFFN(nn.Module):
 
     @torch.no_grad()
     def quantize_(self) -> "ExpertFFN":
-        """Hold the expert weights in 4 bits (bsr_mx4_quantize) and drop the bf16 ones; forward only from then on."""
+        """Hold the expert weights in 4 bits (bsr_mx4_quantize) and drop the bf16 ones; forward only from then on, with the
+        router and the biases frozen."""
         if not self.quantized:
             up, down = mx4.quantize(self.up.data), mx4.quantize(self.down.data)
             self.up_codes, self.up_scales, self.down_codes, self.down_scales = up.codes, up.scales, down.codes, down.scales
             self.up = self.down = None
+            self.requires_grad_(False)
         return self
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        if self.quantized and torch.is_grad_enabled() and x.requires_grad:
+        if self.quantized and torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in self.parameters())):
             raise RuntimeError("a quantised ExpertFFN has no backward pass")
         lead = x.shape[:-1]
         x = _whole(x.reshape(-1, self.dim).to(torch.bfloat16))

@@ -170,3 +170,23 @@ def test_autograd_functions_do_not_copy_aligned_tensors(library):
     for (name, args), tensors in zip(library.calls, ([logits], [x, W], [y, w])):
         for t in tensors:
             assert t.data_ptr() in args, name
+
+
+@pytest.mark.parametrize("tokens", [3, 100])
+def test_a_quantised_layer_trains_nothing(library, tokens):
+    """quantize_() freezes what is left of the parameters, so that a model's optimiser finds no gradients missing; a layer
+    that is asked to train after all refuses, whether its input wants a gradient or not."""
+    m = expert_layer.ExpertFFN(64, 64, 4, 2, bias=True, device="cpu").quantize_()
+    x = bf(tokens, 64)
+    assert {n for n, _ in m.named_parameters()} == {"router", "up_bias", "down_bias"}
+    assert not any(p.requires_grad for p in m.parameters())
+    assert not m(x).requires_grad
+    with pytest.raises(RuntimeError, match="no backward"):
+        m(x.clone().requires_grad_())
+    for name in ("router", "up_bias", "down_bias"):
+        m.requires_grad_(False)
+        getattr(m, name).requires_grad_()
+        with pytest.raises(RuntimeError, match="no backward"):
+            m(x)
+        with torch.no_grad():
+            assert m(x).shape == (tokens, 64)
