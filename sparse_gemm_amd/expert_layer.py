@@ -139,7 +139,8 @@ class ExpertFFN(nn.Module):
         return self
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        if self.quantized and torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in self.parameters())):
+        if self.quantized and torch.is_grad_enabled() and (x.requires_grad or any(
+                p is not None and p.requires_grad for p in (self.router, self.up_bias, self.down_bias))):
             raise RuntimeError("a quantised ExpertFFN has no backward pass")
         lead = x.shape[:-1]
         x = _whole(x.reshape(-1, self.dim).to(torch.bfloat16))
