@@ -85,7 +85,7 @@ int32_t bsr_expert_bwd_input(const bsr_bf16 *dY, int64_t R, int32_t E, int32_t N
                              const bsr_bf16 *W, bsr_bf16 *dX, void *stream);
 
 /* Grouped weight gradient: dW[e] = sum over the rows r of e of dY[r]^T . x(r), dbias[e] = sum of dY[r]
- * (NULL to skip). X, T and row_token as for the forward. dW [E][N][K] bf16, dbias [E][N] bf16; experts
+ * (either NULL to skip it, not both). X, T and row_token as for the forward. dW [E][N][K] bf16, dbias [E][N] bf16; experts
  * without rows get 0. Sums in fp32, in a fixed order: the result is deterministic. */
 int32_t bsr_expert_bwd_weight(const bsr_bf16 *dY, const bsr_bf16 *X, int64_t T, int64_t R, int32_t E, int32_t N,
                               int32_t K, const int32_t *offsets, const int32_t *row_token, bsr_bf16 *dW,

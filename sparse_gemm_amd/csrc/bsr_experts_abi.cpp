@@ -160,7 +160,7 @@ int32_t bsr_expert_bwd_weight(const bsr_bf16 *dY, const bsr_bf16 *X, int64_t T, 
     if ((uint64_t)R * N * 2 > kMaxOperandBytes) return fail(BSR_ERR_INVALID_ARG, "dY of more than 0xF0000000 bytes");
     const bool none = R == 0;   // the gradients are then 0
     BSR_CHECK(check_ptrs({{dY, "dY", none, 16}, {X, "X", none || (row_token && T == 0), 16}, {offsets, "offsets", false, 16},
-                          {row_token, "row_token", true, 16}, {dW, "dW", false, 16}, {dbias, "dbias", true, 16}}));
+                          {row_token, "row_token", true, 16}, {dW, "dW", dbias != nullptr, 16}, {dbias, "dbias", true, 16}}));
     return launch_expert_bwd_weight({(int)T, (int)R, E, N, K, offsets, row_token}, dY, X, dW, dbias, stream);
     BSR_TRY_END
 }

@@ -165,7 +165,9 @@ int32_t launch_expert_bwd_weight(const ExpertShape &s, const uint16_t *dY, const
         hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(w ? 512 : 256), 0, st, dY, X, s.offsets, s.row_token, s.T,
                            s.R, s.N, s.K, dW, (int)mt, (int)nt);
     };
-    if (w && s.row_token) run(k_expert_weight<256, 256, 2, 4, true>);
+    if (!dW) {
+        // the bias alone
+    } else if (w && s.row_token) run(k_expert_weight<256, 256, 2, 4, true>);
     else if (w) run(k_expert_weight<256, 256, 2, 4, false>);
     else if (s.row_token) run(k_expert_weight<128, 128, 2, 2, true>);
     else run(k_expert_weight<128, 128, 2, 2, false>);

@@ -62,7 +62,8 @@ class _ExpertLinearFn(torch.autograd.Function):
             if ctx.gather:
                 dX = experts.combine_fwd(plan, dX)
         if ctx.needs_input_grad[1] or (ctx.has_bias and ctx.needs_input_grad[2]):
-            dW, db = experts.expert_bwd_weight(plan, dY, x, ctx.gather, ctx.has_bias and ctx.needs_input_grad[2])
+            dW, db = experts.expert_bwd_weight(plan, dY, x, ctx.gather, ctx.has_bias and ctx.needs_input_grad[2],
+                                               want_dW=ctx.needs_input_grad[1])
         return dX, dW, db, None, None
 
 

@@ -221,16 +221,21 @@ def expert_bwd_input(plan: ExpertPlan, dY: torch.Tensor, W: torch.Tensor, out: O
 
 
 def expert_bwd_weight(plan: ExpertPlan, dY: torch.Tensor, X: torch.Tensor, gather: bool = True, want_dbias: bool = False,
-                      out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
-    """(dW [E, N, K], dbias [E, N] or None) via bsr_expert_bwd_weight; X and gather as for expert_fwd."""
+                      out: Optional[torch.Tensor] = None,
+                      want_dW: bool = True) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(dW [E, N, K] or None, dbias [E, N] or None) via bsr_expert_bwd_weight; X and gather as for expert_fwd."""
     T, R, E, d = plan.T, plan.R, plan.E, plan.device
     if d != current_device():
-        return elsewhere(expert_bwd_weight, d, plan, dY, X, gather, want_dbias, out)
+        return elsewhere(expert_bwd_weight, d, plan, dY, X, gather, want_dbias, out, want_dW)
     N, K = sizes(dY, "dY", 2)[1], sizes(X, "X", 2)[1]
     gp = pointer(dY, "dY", (R, N), _BF16, d)
     xp = pointer(X, "X", (T if gather else R, K), _BF16, d)
-    dW = new3(E, N, K, _BF16) if out is None else out
-    op = pointer(dW, "out", (E, N, K), _BF16, d)
+    dW = op = None
+    if want_dW:
+        dW = new3(E, N, K, _BF16) if out is None else out
+        op = pointer(dW, "out", (E, N, K), _BF16, d)
+    elif out is not None or not want_dbias:
+        raise ValueError("without dW there is no out, and dbias must be wanted")
     db = new2(E, N, _BF16) if want_dbias else None
     status = C.bsr_expert_bwd_weight(gp, xp, T, R, E, N, K, plan._offsets.data_ptr(), plan._token.data_ptr() if gather else None,
                                      op, db.data_ptr() if want_dbias else None, raw_stream(d))

@@ -190,3 +190,19 @@ def test_a_quantised_layer_trains_nothing(library, tokens):
             m(x)
         with torch.no_grad():
             assert m(x).shape == (tokens, 64)
+
+
+@pytest.mark.parametrize("train_W", [False, True])
+@pytest.mark.parametrize("train_b", [False, True])
+def test_only_wanted_gradients_are_computed(library, train_W, train_b):
+    plan, T, R, E, N, K = a_plan(), 4, 8, 3, 64, 64
+    x, W, b = bf(T, K).requires_grad_(), bf(E, N, K).requires_grad_(train_W), bf(E, N).requires_grad_(train_b)
+    y = expert_layer.expert_linear(plan, x, W, b)
+    library.calls.clear()
+    y.backward(bf(R, N))
+    calls = dict(library.calls)
+    assert ("bsr_expert_bwd_weight" in calls) == (train_W or train_b)
+    if train_W or train_b:
+        dW, db = calls["bsr_expert_bwd_weight"][9:11]
+        assert (dW is not None) == train_W and (db is not None) == train_b
+    assert (W.grad is not None) == train_W and (b.grad is not None) == train_b

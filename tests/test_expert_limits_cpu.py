@@ -5,7 +5,7 @@ import pytest
 from sparse_gemm_amd import _lib
 
 P = 4096     # an aligned address that no refused call reads
-INVALID = 1
+INVALID, MISALIGNED = 1, 3
 TOP = 0xF0000000
 BIG, WIDE = 1 << 18, 8192     # rows and columns of 4 GiB in bf16, past the limit of one buffer resource
 
@@ -57,3 +57,11 @@ def test_rows_out_of_range(R):
     L = _lib.load()
     assert "R must" in why(L.bsr_expert_bwd_input(P, R, 8, 64, 64, P, P, P, None))
     assert "R must" in why(L.bsr_expert_fwd(P, 0, R, 8, 64, 64, P, None, P, None, P, None))
+
+
+def test_the_weight_gradient_may_be_the_bias_alone():
+    L = _lib.load()
+    # every pointer in its place but the last, which is refused for its alignment
+    assert L.bsr_expert_bwd_weight(P, P, 4, 8, 2, 64, 64, P, P, None, P + 4, None) == MISALIGNED
+    assert "dbias" in L.bsr_last_error().decode()
+    assert "dW is NULL" in why(L.bsr_expert_bwd_weight(P, P, 4, 8, 2, 64, 64, P, P, None, None, None))

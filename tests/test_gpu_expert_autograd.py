@@ -46,3 +46,19 @@ def test_slices_give_the_results_of_whole_tensors():
         results.append([index, weight, rows, out, logits[i].grad, x[i].grad, y[i].grad, w[i].grad])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,E,N", [(70, 3, 136), (0, 2, 64)])
+def test_the_bias_alone(T, E, N):
+    """The bias gradient without the weight gradient is the one that comes with it."""
+    K = 72
+    g = gen(T)
+    p = experts.ExpertPlan.from_index(torch.randint(-1, E, (T, 2), generator=g, dtype=torch.int32).to(dev()), E)
+    dY, X = torch.randn(2 * T, N, generator=g).bfloat16().to(dev()), torch.randn(T, K, generator=g).bfloat16().to(dev())
+    _, want = experts.expert_bwd_weight(p, dY, X, want_dbias=True)
+    none, db = experts.expert_bwd_weight(p, dY, X, want_dbias=True, want_dW=False)
+    assert none is None and torch.equal(db, want)
+    with pytest.raises(ValueError):
+        experts.expert_bwd_weight(p, dY, X, want_dW=False)
+    with pytest.raises(ValueError):
+        experts.expert_bwd_weight(p, dY, X, want_dbias=True, want_dW=False, out=torch.empty(E, N, K, dtype=torch.bfloat16, device=dev()))

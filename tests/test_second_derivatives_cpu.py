@@ -29,7 +29,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(experts, "expert_fwd", lambda plan, x, W, bias, gather: x @ W[0].t() + (0 if bias is None else bias))
     monkeypatch.setattr(experts, "expert_bwd_input", lambda plan, dY, W: dY @ W[0])
     monkeypatch.setattr(experts, "expert_bwd_weight",
-                        lambda plan, dY, x, gather, want: ((dY.t() @ x)[None], dY.sum(0, keepdim=True) if want else None))
+                        lambda plan, dY, x, gather, want, want_dW: ((dY.t() @ x)[None], dY.sum(0, keepdim=True) if want else None))
     monkeypatch.setattr(experts, "combine_fwd", lambda plan, Y, w=None: Y.clone() if w is None else (w * Y).to(Y.dtype))
     monkeypatch.setattr(experts, "combine_bwd", lambda plan, d, Y, w: ((w * d).to(Y.dtype), (d * Y).sum(1, keepdim=True).float()))
 
