@@ -67,10 +67,20 @@ def elsewhere(f, device: int, *args):
         return f(*args)
 
 
+MOST = (1 << 31) - 1   # what the library takes as a 32-bit number; beyond that ctypes would pass the low bits
+
+
+def narrow(n: int, name: str) -> None:
+    if n > MOST:
+        raise ValueError(f"{name} has a dimension of 2^31 or more")
+
+
 def sizes(t: torch.Tensor, name: str, dims: int) -> torch.Size:
     shape = t.shape
     if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
+    if t.numel() > MOST:
+        narrow(max(shape[1:] or shape), name)   # rows are taken as 64-bit numbers
     return shape
 
 
@@ -92,7 +102,7 @@ def router_fwd(logits: torch.Tensor, k: int, renormalize: bool = True, out=None)
     else:
         index, weight = out
         ip, wp = pointer(index, "index", (T, k), _I32, d), pointer(weight, "weight", (T, k), _F32, d)
-    status = C.bsr_router_fwd(lp, kind, T, E, k, renormalize, ip, wp, raw_stream(d))
+    status = C.bsr_router_fwd(lp, kind, T, E, min(k, MOST), renormalize, ip, wp, raw_stream(d))
     if status:
         _lib.check(status, "bsr_router_fwd")
     return index, weight
@@ -166,7 +176,7 @@ class ExpertPlan:
         self._offsets = o = empty_strided((max(E, 0) + 1,), (1,), _I32)
         self._token = t = empty_strided((R,), (1,), _I32)
         self._row = s = new2(T, k, _I32)
-        need, ws = 0, None
+        E, need, ws = min(E, MOST), 0, None
         if R > PLAN_SLOTS:
             need = C.bsr_expert_plan_workspace(T, k, E)
             ws = empty_strided((need,), (1,), torch.uint8)

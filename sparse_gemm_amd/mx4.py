@@ -7,7 +7,7 @@ from typing import Optional, Union
 import torch
 
 from . import _lib
-from .experts import C, ExpertPlan, current_device, elsewhere, empty_strided, new2, new3, pointer, raw_stream, sizes
+from .experts import C, ExpertPlan, current_device, elsewhere, empty_strided, narrow, new2, new3, pointer, raw_stream, sizes
 
 _BF16, _U8 = torch.bfloat16, torch.uint8
 GROUP = 32      # elements that share a scale
@@ -72,6 +72,7 @@ def quantize(X: torch.Tensor, want_values: bool = False):
         if want_values:
             raise ValueError("want_values needs X of 2 dimensions")
         E, rows, K = X.shape
+        narrow(K, "X")
         pointer(X, "X", (E, rows, K), _BF16, d)
         c = chunks(K)
         codes = new3(E, rows, K // 2, _U8)
@@ -97,6 +98,7 @@ def dequantize(q: Mx4) -> torch.Tensor:
         return elsewhere(dequantize, d, q)
     *lead, rows, half = q.codes.shape
     K = 2 * half
+    narrow(K, "the matrix")
     if len(lead) > 1:
         raise ValueError("codes must have 2 or 3 dimensions")
     cp = pointer(q.codes, "codes", (*lead, rows, half), _U8, d)

@@ -206,3 +206,37 @@ def test_only_wanted_gradients_are_computed(library, train_W, train_b):
         dW, db = calls["bsr_expert_bwd_weight"][9:11]
         assert (dW is not None) == train_W and (db is not None) == train_b
     assert (W.grad is not None) == train_W and (b.grad is not None) == train_b
+
+
+def test_sizes_past_32_bits_are_refused(library):
+    """The library takes widths, experts and slots as 32-bit numbers; a larger one would reach it cut to its low bits."""
+    big = (1 << 32) + 64
+    meta = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="meta")   # noqa: E731
+    plan = a_plan(1, 1, 1)
+    u8, i32, f32 = torch.uint8, torch.int32, torch.float32
+    calls = [lambda: mx4.quantize(meta(1, big)), lambda: mx4.quantize(meta(2, 1, big)),
+             lambda: mx4.dequantize(mx4.Mx4(meta(1, big // 2 + 32, dtype=u8), meta(big // 256, 1, 8, dtype=u8))),
+             lambda: experts.router_fwd(meta(1, big, dtype=f32), 2),
+             lambda: experts.router_bwd(meta(1, big, dtype=f32), meta(1, 2, dtype=i32), meta(1, 2, dtype=f32), meta(1, 2, dtype=f32)),
+             lambda: ExpertPlan.from_index(meta(1, big, dtype=i32), 8),
+             lambda: ExpertPlan(meta(big, dtype=i32), meta(2, dtype=i32), meta(1, 2, dtype=i32)),
+             lambda: experts.expert_fwd(plan, meta(1, 64), meta(1, big, 64)),
+             lambda: experts.expert_fwd(plan, meta(1, big), meta(1, 64, big)),
+             lambda: experts.expert_bwd_input(plan, meta(1, big), meta(1, big, 64)),
+             lambda: experts.expert_bwd_weight(plan, meta(1, big), meta(1, 64)),
+             lambda: experts.expert_bwd_weight(plan, meta(1, 64), meta(1, big)),
+             lambda: experts.combine_fwd(plan, meta(1, big)), lambda: experts.combine_bwd(plan, meta(1, big), meta(1, big)),
+             lambda: mx4.expert_fwd(plan, meta(1, 64), mx4.Mx4(meta(1, big, 32, dtype=u8), meta(1, 1, big, 8, dtype=u8)))]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+        assert not library.calls, i
+
+
+def test_slots_and_experts_reach_the_library_whole(library, monkeypatch):
+    """k and E come from the caller, and are refused by the library, not cut."""
+    monkeypatch.setattr(experts, "empty_strided", lambda shape, strides, dtype: torch.empty(4, dtype=dtype))
+    experts.router_fwd(torch.zeros(1, 8), (1 << 32) + 2)
+    ExpertPlan.from_index(torch.zeros((1, 2), dtype=torch.int32), (1 << 32) + 8)
+    (_, router), (_, plan) = library.calls
+    assert router[4] == plan[3] == (1 << 31) - 1
