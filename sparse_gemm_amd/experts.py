@@ -29,8 +29,10 @@ C = _Calls()
 
 # What a call of a few microseconds spends on the host is most of its time. The current stream's handle and the
 # current device come without building objects for them, and outputs from the allocation call that torch's
-# compiled graphs use, where this torch has it (on the current device, shape and strides as tuples).
-raw_stream, current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# compiled graphs use (on the current device, shape and strides as tuples). These names are private to torch: where it lacks
+# one, the public call stands in.
+raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 try:
     from torch._C._dynamo.guards import _empty_strided_cuda as empty_strided
 except ImportError:

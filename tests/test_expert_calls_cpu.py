@@ -2,12 +2,16 @@
 tensors on GPU 0, and a stand-in for the library records the arguments of each call."""
 import copy
 import ctypes
+import os
 import pickle
+import subprocess
+import sys
 
 import pytest
 import torch
 
-from sparse_gemm_amd import expert_layer, experts, mx4
+from conftest import ROOT
+from sparse_gemm_amd import _lib, expert_layer, experts, mx4
 from sparse_gemm_amd.experts import ExpertPlan
 
 
@@ -240,3 +244,42 @@ def test_slots_and_experts_reach_the_library_whole(library, monkeypatch):
     ExpertPlan.from_index(torch.zeros((1, 2), dtype=torch.int32), (1 << 32) + 8)
     (_, router), (_, plan) = library.calls
     assert router[4] == plan[3] == (1 << 31) - 1
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_tensors_without_memory_are_refused(library, monkeypatch):
+    """Fake tensors (torch's tracing) have no address, and the library itself refuses that before anything is enqueued."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    plan, real = a_plan(), experts._Calls()
+    monkeypatch.setattr(experts, "C", real)
+    monkeypatch.setattr(mx4, "C", real)
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        calls = [lambda: experts.router_fwd(torch.zeros(4, 3), 2), lambda: ExpertPlan.from_index(torch.zeros((4, 2), dtype=torch.int32), 3),
+                 lambda: experts.expert_fwd(plan, bf(4, 64), bf(3, 64, 64)), lambda: experts.combine_fwd(plan, bf(8, 64)),
+                 lambda: mx4.quantize(bf(4, 64))]
+        for call in calls:
+            with pytest.raises(_lib.BsrError, match="is NULL"):
+                call()
+
+
+def test_the_module_needs_no_private_names():
+    """Without torch's private calls for stream, device and allocation the public ones take their place."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+if hasattr(torch._C._dynamo.guards, "_empty_strided_cuda"):
+    del torch._C._dynamo.guards._empty_strided_cuda
+from sparse_gemm_amd import experts, mx4
+assert experts.current_device is torch.cuda.current_device
+torch.cuda.current_stream = lambda d: type("Stream", (), {"cuda_stream": 70 + d})
+assert experts.raw_stream(1) == mx4.raw_stream(1) == 71
+try:
+    experts.router_fwd(torch.zeros(4, 8), 2)
+except ValueError:
+    print("refused")
+"""
+    env = {**os.environ, "PYTHONPATH": ROOT}
+    out = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert out.stdout.strip() == "refused", out.stderr
