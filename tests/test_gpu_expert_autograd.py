@@ -62,3 +62,20 @@ def test_the_bias_alone(T, E, N):
         experts.expert_bwd_weight(p, dY, X, want_dW=False)
     with pytest.raises(ValueError):
         experts.expert_bwd_weight(p, dY, X, want_dbias=True, want_dW=False, out=torch.empty(E, N, K, dtype=torch.bfloat16, device=dev()))
+
+
+@pytest.mark.filterwarnings("ignore")
+def test_a_compiled_layer_is_the_eager_one():
+    """torch.compile finds calls that it cannot trace and leaves them as they are: the same bits, forward and backward."""
+    torch.manual_seed(0)
+    m = expert_layer.ExpertFFN(64, 64, 4, 2, device=dev())
+    x = torch.randn(24, 64, device=dev()).bfloat16()
+    want = m(x)
+    want.sum().backward()
+    grads = [p.grad.clone() for p in m.parameters()]
+    m.zero_grad()
+    got = torch.compile(m, backend="eager")(x)
+    got.sum().backward()
+    assert torch.equal(got, want)
+    for p, g in zip(m.parameters(), grads):
+        assert torch.equal(p.grad, g)
