@@ -380,8 +380,8 @@ __global__ __launch_bounds__(kPlanRound) void k_plan_write(const int32_t *__rest
 
 // ------------------------------------------------------------------------------------------
 // The sum over a token's rows and its gradient: 8 columns a thread, so that a wave takes 1 KB of a row. 8191 tokens, k = 8,
-// N = 2048: forward 55 us (302 MB, 5.5 TB/s; 75 us behind other work, with nothing of Y in the last-level cache), backward, one
-// wave a slot, 113 us (570 MB, 5.0 TB/s; 99 behind the forward, which leaves Y there).
+// N = 2048: forward 55 us (302 MB, 5.5 TB/s; 76 us behind other work, with nothing of Y in the last-level cache), backward, one
+// wave a slot, 113 us (570 MB, 5.0 TB/s; 100 behind the forward, which leaves Y there).
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void unpack8(u32x4 v, float *f) {
 #pragma unroll

@@ -1,14 +1,16 @@
-// bsr_experts_few.hip -- the grouped forward for few rows an expert (decode), on bf16 weights
-// (include/bsr_experts.h) and on microscaled 4-bit weights (include/bsr_mx4.h).
+// bsr_experts_few.hip -- grouped products for few rows an expert (decode): forward and input gradient on bf16 weights
+// (include/bsr_experts.h), forward on microscaled 4-bit weights (include/bsr_mx4.h).
 //
-// Bound by the weights' bytes. A work-group owns up to 16 MT rows of one expert and BN output columns, and
+// The weights' bytes are the least that they need. A work-group owns up to 16 MT rows of one expert and BN output columns, and
 // streams the BN weight rows in steps of 256 columns (512 bytes of bf16 or 128 bytes of codes a row; for the input
 // gradient 2 BN bytes of 256 weight rows: whole cache lines in most cases) through a ring of NS LDS stages by
 // direct-to-LDS loads, NS - 1 steps ahead. Its four waves split each step's contraction, 64 each, for all BN
 // columns of the output (16 x 16 x 32 products, fp32 sums) and add their sums through LDS at the end, in a fixed
 // order: with the contraction split inside the work-group, BN can be small, and a narrow layer still fills the card.
-// 4 tokens, k = 2 of 8 experts, 4096 -> 14336 in 4 bits: 40 us, 6.2 TB/s. 8 tokens, k = 8 of 64, 4096 -> 1536 in bf16:
-// 75 us, 6.7 TB/s (some weights still cached). One token, k = 2 of 8, 2048 -> 1024 in bf16: 6 us, eight dependent steps.
+// Weights not in the caches, bytes of the experts that have rows: 8 of 8, 4096 -> 14336, one row each: in bf16 146 us, 6.4 TB/s,
+// in 4 bits 51 us, 4.9 TB/s; 4 tokens, k = 2 of 8, there (5.5 experts on average) 45 us, 4.4 TB/s. 64 of 64, 4096 -> 1536, in
+// bf16: 128 us, 6.3 TB/s. Nothing is read twice (219 MB counted for 7 experts' 218): the 4-bit tiles have 16 steps each in about three
+// rounds of work-groups, whose starts and ends weigh. One token, k = 2 of 8, 2048 -> 1024 in bf16: 6 us, eight dependent steps.
 //   bf16: lane (r = l % 16, g = l / 16) takes the columns 64 w + 32 i + 8 g + 0 .. 7 of wave w's product i
 //   4-bit: the columns 64 w + 16 g + 8 i + 0 .. 7, so that its 16 codes are 8 neighbouring bytes of one group
 #include <hip/hip_runtime.h>

@@ -7,11 +7,12 @@
 // Work-groups find their expert and rows from offsets on the device.
 //
 // Large products are bound by the matrix cores and, beside them, by the 64 KB a step that come through L2. 16384 tokens,
-// k = 2 of 8 experts, 4096 -> 11008: 2.29 ms, 1.29 PFLOP/s; one dense 16384 x 4096 -> 4096: 393 us, 1.40 PFLOP/s (the
-// matrix instructions alone, on random data: 2.1). Copies that skip work, of a dense 16384 x 16384 -> 4096 in 1591 us: no loads
-// in the loop 1079, no waits for loads 1579, no barrier 1518, no LDS reads 1347: the loads' rate, not their latency.
-// Gradients of 8192 tokens, k = 2 of 8, 4096 -> 4096: input 464 us (1.19 PFLOP/s), weight 459 us (1.20). Ragged groups
-// cost partly empty tiles and the last round of tiles.
+// k = 2 of 8 experts, 4096 -> 11008: 2.28 ms, 1.30 PFLOP/s, matrix cores busy 71% of the time at 1.71 GHz; one dense 16384 x
+// 4096 -> 4096: 394 us, 1.40 PFLOP/s (the matrix instructions alone, on random data: 2.1). Copies that skip work, of a dense
+// 16384 x 16384 -> 4096 in 1591 us: no loads in the loop 1079, no waits for loads 1579, no barrier 1518, no LDS reads 1347: the
+// loads' rate, not their latency.
+// Gradients of 8192 tokens, k = 2 of 8, 4096 -> 4096: input 445 us (1.23 PFLOP/s), weight 481 us (1.14), their matrix cores busy
+// 65 and 56%. Ragged groups cost partly empty tiles and the last round of tiles.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -61,8 +62,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_rows(GemmArgs g, int 
 
 // Weight gradient: one BM x BN tile of one expert's dW a work-group, over all rows of the expert. Every XCD takes an eighth
 // of every expert's tiles: the experts' row counts differ, and whole experts a XCD would leave some of them idle (64
-// narrow experts, 16396 rows, dW 1000 x 2048: 272 -> 155 us together with token loads a step ahead; now 127 us, at least 54 of
-// them for the 262 MB of dW).
+// narrow experts, 16396 rows, dW 1000 x 2048: 272 -> 155 us together with token loads a step ahead; now 130 us, at least 54 of
+// them for the 262 MB of dW). The eighth is rounded up: an expert of fewer than 8 tiles leaves XCDs without one.
 template <int BM, int BN, int WM, int WN, bool Gathered>
 __global__ __launch_bounds__(WM *WN * 64, 1) void k_expert_weight(const uint16_t *__restrict__ dY, const uint16_t *__restrict__ X,
                                                                const int32_t *__restrict__ offsets,
@@ -157,6 +158,17 @@ int32_t launch_expert_bwd_input(const ExpertShape &s, const uint16_t *dY, const 
 int32_t launch_expert_bwd_weight(const ExpertShape &s, const uint16_t *dY, const uint16_t *X, uint16_t *dW,
                                  uint16_t *dbias, void *stream) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    // 256 x 256 tiles from 192 of them on. dW in us, 256 x 256 | 128 x 128, with 64, 512 and 2048 rows an expert:
+    //   8 experts, 4096 x 4096 (2048 tiles)   62 | 72    149 | 185   448 | 584
+    //   64 experts, 1000 x 2048 (2048)        66 | 74    167 | 192   528 | 672
+    //   1 expert, 4096 x 4096 (256)           10 | 11     20 | 25     58 | 76
+    //   8 experts, 1280 x 1280 (200)          10 | 10     21 | 25     57 | 72
+    //   1 expert, 2048 x 4096 (128)            8 | 7      16 | 12     50 | 39
+    //   8 experts, 1024 x 1024 (128)           8 | 6      17 | 15     48 | 40
+    //   4 experts, 1000 x 1776 (112)           9 | 8      19 | 14     50 | 40
+    // Experts of few tiles, which the XCDs share unevenly, lie on the wrong side of it:
+    //   64 experts, 512 x 512 (256)           19 | 11     47 | 37    148 | 123
+    //   16 experts, 768 x 768 (144)           10 | 9      23 | 25     65 | 76
     const bool w = (int64_t)s.E * ((s.N + 255) / 256) * ((s.K + 255) / 256) >= 192;
     const int64_t bm = w ? 256 : 128, mt = (s.N + bm - 1) / bm, nt = (s.K + bm - 1) / bm;
     const int64_t blocks = (mt * nt + 7) / 8 * 8 * s.E;

@@ -53,7 +53,7 @@ inline int32_t check_grid(int64_t blocks, int threads, const char *what) {
 //   forward 1024 -> 2048, E = 8     16: 9 | 13    32: 12 | 13    48: 13 | 13     64: 22 | 13
 //   forward 4096 -> 14336, E = 8    16: 160 | 166   24: 203 | 196   32: 208 | 169
 //   input gradient of 4096 -> 14336, E = 1   16: 38 | 108    128: 43 | 108    384: 114 | 109
-//   4-bit forward 4096 -> 14336, E = 8       16: 54 | 105    24: 61 | 105     48: 99 | 110     64: 132 | 116
+//   4-bit forward 4096 -> 14336, E = 8       16: 58 | 103    24: 65 | 103     48: 100 | 113    64: 107 | 115    96: 159 | 125
 struct TileKind {
     int id, rows, cols, step, slots;
     double alone, shared;

@@ -29,8 +29,9 @@ struct GemmArgs {
 // are (32 bytes a row and step) and turned into bf16 fragments in registers: half-wave h of a row takes the
 // group of columns 32 h .. 32 h + 31, one 16-byte read a step whose word i is its operand of the i-th product, so
 // the activation fragments take the columns 32 h + 8 i + 0 .. 7. Three stages a side, loads two steps ahead; two
-// work-groups a CU. Bound like the bf16 products (the expansion runs beside the matrix cores): 2048 rows, 8 experts,
-// 4096 -> 14336: 284 us, 850 TFLOP/s.
+// work-groups a CU. 2048 rows, 8 experts, 4096 -> 14336: 295 us, 815 TFLOP/s, matrix cores busy 48% of the time: each code is expanded
+// by the two waves that share its column, and the tile is the small one. In 16 x 16 x 32 products, which read LDS and convert more for
+// a product: 288 us against 278 at that time.
 // ------------------------------------------------------------------------------------------
 constexpr int kA = 128 * 128, kB = 128 * 32, kS = 128 * 8, kStage = kA + kB + kS;
 
@@ -121,9 +122,10 @@ __global__ __launch_bounds__(256, 2) void k_mx4_rows(GemmArgs g, int ntiles) {
 // step's two chunks, so that its two scale bytes are one 16-bit word whose byte j the products of chunk j select. Two stages
 // a side; as in the bf16 products the fragments of one chunk are read while the other is multiplied, and a barrier between them
 // ends the reads of step s: the loads of step s + 2 are issued in its second chunk.
-// 16384 rows, 8 experts, 4096 -> 4096: 161 us, 3.4 PFLOP/s; 32768 rows, 4096 -> 11008: 790 us, 3.7 (with 32 x 32 x 64 products 171
-// and 840; the instructions alone, on random data, 7.3 against 6.4). Copies of that older form that skip work, of 836: no loads in the loop
-// 700, no LDS reads 744, neither 632, a single step 215: starts and ends of tiles and the matrix cores themselves hold most of it.
+// 16384 rows, 8 experts, 4096 -> 4096: 170 us, 3.2 PFLOP/s; 32768 rows, 4096 -> 11008: 818 us, 3.6; matrix cores busy 38 and 44% of the
+// time. With 32 x 32 x 64 products, before: 171 and 840 against 161 and 790 (the instructions alone, on random data, 6.4 against 7.3
+// PFLOP/s). Copies of that former kernel that skip work, of 836: no loads in the loop 700, no LDS reads 744, neither 632, a single
+// step 215: starts and ends of tiles and the matrix cores themselves held most of it.
 // ------------------------------------------------------------------------------------------
 typedef int codes_x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -300,7 +302,7 @@ int32_t launched(const char *what) {
 }
 
 // 256 x 256 tiles with 8 waves where the groups fill them, else 128 x 128 with 4, two work-groups a CU. 16384 rows of 8
-// experts, 4096 -> 4096: 161 us against 190; 8 rows, 4096 -> 14336 (weights' bytes): 42 us with the small tile.
+// experts, 4096 -> 4096: 161 us against 190; one row each of 8 experts, 4096 -> 14336 (250 MB of weights): 55 us with the small tile.
 bool wide(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 + 1) * ((cols + 255) / 256) >= 192; }
 
 }  // namespace

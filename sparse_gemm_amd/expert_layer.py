@@ -96,7 +96,8 @@ def combine(plan: ExpertPlan, Y: torch.Tensor, weight: torch.Tensor) -> torch.Te
 class ExpertFFN(nn.Module):
     """y = sum over a token's k experts of weight * down_e(silu(gate_e x) * up_e x).
 
-    The router's logits are x . router^T; up holds gate and up weights one after the other ([E, 2 * hidden, dim]).
+    The router's logits are x . router^T, a library product rounded to bf16 like the layer's other results (the router itself
+    takes f32 logits too); silu(gate), its product with up and each product of the experts are rounded to bf16 once. up holds gate and up weights one after the other ([E, 2 * hidden, dim]).
     quantize_() replaces the expert weights by their 4-bit form for serving: batches of up to `prompt_tokens` tokens
     then keep their activations in bf16, larger ones quantise them too: faster, and less exact by the activations'
     own rounding to 4 bits (up layer 4096 -> 14336 of 8 experts, k = 2: 16 tokens 44 against 46 us, 64 tokens 53 against

@@ -1,5 +1,9 @@
 """Python face of include/bsr_mx4.h: microscaled 4-bit values (32 E2M1 codes share one power-of-two scale
-byte) and the grouped product on 4-bit weights."""
+byte) and the grouped product on 4-bit weights.
+
+A plain linear layer on 4-bit weights W [1, N, K] is one expert that takes every row, its plan made once for a number of rows T:
+    plan = ExpertPlan.from_index(torch.zeros((T, 1), dtype=torch.int32, device=x.device), 1)
+    y = mx4.expert_fwd(plan, x, W)"""
 from __future__ import annotations
 
 from typing import Optional, Union
