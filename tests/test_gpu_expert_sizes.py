@@ -210,3 +210,25 @@ def test_combine_past_4_gib():
 
 def near_f32(got, ref, S, terms):
     assert bool(((got.double() - ref).abs() <= (terms + 4) * 2.0 ** -23 * S).all())
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_4_bit_weights_with_activations_up_to_the_limit(gather):
+    """bf16 activations of exactly the most bytes on 4-bit weights."""
+    K, N, E = 4096, 64, 3
+    R = TOP // (2 * K)
+    p, offsets, token = a_plan(R, E, 2)
+    say(f"case 4-bit weights R={R} N={N} K={K} gather={gather}")
+    W = mx4.quantize(randn(E, N, K, seed=18, std=0.05))
+    wv = mx4.dequantize(W)
+    X = randn(R, K, seed=19)
+    Y = mx4.expert_fwd(p, X, W, gather=gather)
+    check_rows(Y, offsets, lambda a, b: X[token[a:b]] if gather else X[a:b], lambda e: wv[e], K)
+
+
+def test_expansion_past_4_gib():
+    """Codes of 4 GB, values of 16 GB: both passes write the same."""
+    rows, K = TOP * 2 // 1024, 1024
+    say(f"case expansion rows={rows} K={K}")
+    q, values = mx4.quantize(randn(rows, K, seed=20), want_values=True)
+    assert torch.equal(mx4.dequantize(q), values)
