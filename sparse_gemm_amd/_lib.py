@@ -36,7 +36,12 @@ EXPORTS = ("bsr_abi_version", "bsr_pattern_create_from_mask", "bsr_pattern_creat
            "bsr_router_fwd", "bsr_router_bwd", "bsr_expert_plan_workspace", "bsr_expert_plan", "bsr_expert_fwd",
            "bsr_expert_bwd_input", "bsr_expert_bwd_weight", "bsr_expert_combine_fwd", "bsr_expert_combine_bwd",
            # include/bsr_mx4.h
-           "bsr_mx4_quantize", "bsr_mx4_dequantize", "bsr_expert_fwd_mx4", "bsr_expert_fwd_mx4_mx4")
+           "bsr_mx4_quantize", "bsr_mx4_dequantize", "bsr_expert_fwd_mx4", "bsr_expert_fwd_mx4_mx4",
+           # include/bsr_fp8_blocks.h
+           "bsr_fp8_quantize_rows", "bsr_fp8_quantize_blocks", "bsr_fp8_dequantize_rows", "bsr_fp8_dequantize_blocks",
+           "bsr_expert_fwd_fp8", "bsr_expert_fwd_fp8_fp8",
+           # include/bsr_expert_ffn.h
+           "bsr_expert_ffn_workspace", "bsr_expert_ffn")
 
 
 class BsrError(RuntimeError):
@@ -105,6 +110,17 @@ def load() -> ctypes.CDLL:
     L.bsr_mx4_dequantize.argtypes = [P, P, i64, i32, P, P]
     L.bsr_expert_fwd_mx4.argtypes = [P, i64, i64, i32, i32, i32, P, P, P, P, P, P, P]
     L.bsr_expert_fwd_mx4_mx4.argtypes = [P, P, i64, i64, i32, i32, i32, P, P, P, P, P, P, P]
+    L.bsr_fp8_quantize_rows.argtypes = [P, i64, i32, P, P, P, P]
+    L.bsr_fp8_quantize_blocks.argtypes = [P, i32, i32, i32, P, P, P, P, P]
+    L.bsr_fp8_dequantize_rows.argtypes = [P, P, i64, i32, P, P]
+    L.bsr_fp8_dequantize_blocks.argtypes = [P, P, i32, i32, i32, P, P]
+    L.bsr_expert_fwd_fp8.argtypes = [P, i64, i64, i32, i32, i32, P, P, P, P, P, P, P]
+    L.bsr_expert_fwd_fp8_fp8.argtypes = [P, P, i64, i64, i32, i32, i32, P, P, P, P, P, P, P]
+    L.bsr_expert_ffn_workspace.argtypes, L.bsr_expert_ffn_workspace.restype = [i32, i32, i32, i32, i32], sz
+    L.bsr_expert_ffn.argtypes = [P, i32, i32, i32, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P, sz, P]
+    for f in ("bsr_fp8_quantize_rows", "bsr_fp8_quantize_blocks", "bsr_fp8_dequantize_rows", "bsr_fp8_dequantize_blocks",
+              "bsr_expert_fwd_fp8", "bsr_expert_fwd_fp8_fp8", "bsr_expert_ffn"):
+        getattr(L, f).restype = i32
     for f in ("bsr_router_fwd", "bsr_router_bwd", "bsr_expert_plan", "bsr_expert_fwd", "bsr_expert_bwd_input",
               "bsr_expert_bwd_weight", "bsr_expert_combine_fwd", "bsr_expert_combine_bwd", "bsr_mx4_quantize",
               "bsr_mx4_dequantize", "bsr_expert_fwd_mx4", "bsr_expert_fwd_mx4_mx4"):

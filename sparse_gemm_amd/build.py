@@ -19,7 +19,7 @@ ARCH = "gfx950"
 SOURCES = ["bsr_abi.cpp", "bsr_error.cpp", "bsr_pattern.cpp", "bsr_select.cpp", "bsr_kernels.hip", "bsr_wide.hip",
            "bsr_convert.hip", "bsr_fp8.hip", "bsr_sparse24.hip", "bsr_rebuild.hip",
            "bsr_experts_abi.cpp", "bsr_experts.hip", "bsr_experts_gemm.hip", "bsr_experts_few.hip", "bsr_mx4.hip",
-           "bsr_mx4_gemm.hip"]
+           "bsr_mx4_gemm.hip", "bsr_fp8_blocks.hip", "bsr_fp8_gemm.hip", "bsr_expert_ffn.hip"]
 # Kernels whose 4 x 4 grids of 32 x 32 accumulators (256 registers per lane) must live in the
 # accumulation registers: built without the flag that keeps accumulators in general registers.
 AGPR_SOURCES = {"bsr_wide.hip"}

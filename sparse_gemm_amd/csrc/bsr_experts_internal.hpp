@@ -1,5 +1,6 @@
 // bsr_experts_internal.hpp -- launchers of the expert-layer kernels (include/bsr_experts.h) and of the
-// microscaled 4-bit kernels (include/bsr_mx4.h).
+// microscaled 4-bit kernels (include/bsr_mx4.h), of the 8-bit ones (include/bsr_fp8_blocks.h) and of the whole layer for a few
+// tokens (include/bsr_expert_ffn.h).
 #pragma once
 
 #include <algorithm>
@@ -7,7 +8,9 @@
 #include <cstdint>
 #include <string>
 
+#include "bsr_expert_ffn.h"
 #include "bsr_experts.h"
+#include "bsr_fp8_blocks.h"
 #include "bsr_internal.hpp"
 #include "bsr_mx4.h"
 
@@ -122,5 +125,22 @@ int32_t launch_expert_fwd_mx4(const ExpertShape &s, const uint16_t *X, const uin
 int32_t launch_expert_fwd_mx4_mx4(const ExpertShape &s, const uint8_t *xcodes, const uint8_t *xscales,
                                   const uint8_t *codes, const uint8_t *scales, const uint16_t *bias, uint16_t *Y,
                                   void *stream);
+
+int32_t launch_fp8_quantize_rows(const uint16_t *X, int64_t rows, int K, uint8_t *codes, uint8_t *scales, uint16_t *values,
+                                 void *stream);
+int32_t launch_fp8_quantize_blocks(const uint16_t *W, int E, int N, int K, uint8_t *codes, uint8_t *scales, uint8_t *codes_t,
+                                   uint8_t *scales_t, void *stream);
+int32_t launch_fp8_dequantize_rows(const uint8_t *codes, const uint8_t *scales, int64_t rows, int K, uint16_t *values, void *stream);
+int32_t launch_fp8_dequantize_blocks(const uint8_t *codes, const uint8_t *scales, int E, int N, int K, uint16_t *values,
+                                     void *stream);
+int32_t launch_expert_fwd_fp8(const ExpertShape &s, const uint16_t *X, const uint8_t *codes, const uint8_t *scales,
+                              const uint16_t *bias, uint16_t *Y, void *stream);
+int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, const uint8_t *xscales, const uint8_t *codes,
+                                  const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream);
+
+size_t expert_ffn_workspace_bytes(int T, int hidden, int E, int k);
+int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,
+                          int form, const void *up, const uint8_t *up_scales, const void *down, const uint8_t *down_scales,
+                          const uint16_t *up_bias, const uint16_t *down_bias, uint16_t *out, void *workspace, void *stream);
 
 }  // namespace bsr

@@ -1,6 +1,6 @@
 """ExpertFFN: a feed-forward layer whose tokens each use k of E experts, with autograd over the library's
-router, grouped products and sum; its experts can be held in 4 bits for serving. Gradients of the first order: a second
-derivative raises."""
+router, grouped products and sum. It can train with products in 8 bits, its experts can be held in 4 or 8 bits for serving, and a few
+tokens can take the whole layer in one call. Gradients of the first order: a second derivative raises."""
 from __future__ import annotations
 
 import math
@@ -10,7 +10,7 @@ import torch
 from torch import nn
 from torch.nn import functional as F
 
-from . import experts, mx4
+from . import experts, few_tokens, fp8, mx4
 from .autograd import first_order
 from .experts import ExpertPlan
 
@@ -73,6 +73,55 @@ def expert_linear(plan: ExpertPlan, x: torch.Tensor, W: torch.Tensor, bias: Opti
     return _ExpertLinearFn.apply(_whole(x), W, bias, plan, gather)
 
 
+class _ExpertLinearFp8Fn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, bias, plan, gather, want_dx):
+        ctx.plan, ctx.gather, ctx.has_bias = plan, gather, bias is not None
+        if want_dx:
+            Wq, Wt = fp8.quantize_blocks(W, transposed=True)
+            ctx.save_for_backward(x, W, Wt.codes, Wt.scales)
+        else:
+            Wq = fp8.quantize_blocks(W)
+            ctx.save_for_backward(x, W)
+        return fp8.expert_fwd(plan, fp8.quantize_rows(x), Wq, bias, gather)
+
+    @staticmethod
+    @first_order
+    def backward(ctx, dY):
+        x, _, *Wt = ctx.saved_tensors
+        plan = ctx.plan
+        dY = _whole(dY.to(torch.bfloat16))
+        dX = dW = db = None
+        if ctx.needs_input_grad[0]:
+            dX = fp8.expert_fwd(plan, fp8.quantize_rows(dY), fp8.Fp8Blocks(*Wt), gather=False)
+            if ctx.gather:
+                dX = experts.combine_fwd(plan, dX)
+        if ctx.needs_input_grad[1] or (ctx.has_bias and ctx.needs_input_grad[2]):
+            dW, db = experts.expert_bwd_weight(plan, dY, x, ctx.gather, ctx.has_bias and ctx.needs_input_grad[2],
+                                               want_dW=ctx.needs_input_grad[1])
+        return dX, dW, db, None, None, None
+
+
+def expert_linear_fp8(plan: ExpertPlan, x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                      gather: bool = True) -> torch.Tensor:
+    """expert_linear with its products in 8 bits, for training on bf16 weights: x is quantised by row and W by block (fp8.quantize_rows,
+    fp8.quantize_blocks; N and K multiples of 16) in every call, and so is the incoming gradient for the input gradient
+    q(dY) . q(W). The weight and bias gradients are expert_linear's, on x and dY in bf16: they contract over the rows, along which
+    neither has scales. The rounding to codes counts as the identity in the gradients."""
+    x = _whole(x)
+    return _ExpertLinearFp8Fn.apply(x, W, bias, plan, gather, torch.is_grad_enabled() and x.requires_grad)
+
+
+def expert_ffn(x: torch.Tensor, router: torch.Tensor, up, down, k: int, renormalize: bool = True,
+               up_bias: Optional[torch.Tensor] = None, down_bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A whole layer of experts for up to 16 tokens x [T, dim] in one call, few_tokens.expert_ffn: weights in bf16, Mx4 or
+    Fp8Blocks, forward only (raises where a gradient is wanted). Against the single calls it keeps the router's logits and each
+    expert's result in 32 bits, and rounds silu(gate) * up to bf16 once."""
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, router, up, down, up_bias, down_bias)):
+        raise RuntimeError("expert_ffn has no backward pass")
+    return few_tokens.expert_ffn(_whole(x), router, up, down, k, renormalize, up_bias, down_bias)
+
+
 class _CombineFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Y, weight, plan):
@@ -101,13 +150,22 @@ class ExpertFFN(nn.Module):
     quantize_() replaces the expert weights by their 4-bit form for serving: batches of up to `prompt_tokens` tokens
     then keep their activations in bf16, larger ones quantise them too: faster, and less exact by the activations'
     own rounding to 4 bits (up layer 4096 -> 14336 of 8 experts, k = 2: 16 tokens 44 against 46 us, 64 tokens 53 against
-    46, 256 tokens 114 against 50)."""
+    46, 256 tokens 114 against 50). quantize_("fp8") does the same in 8 bits.
+    fp8: the products of the experts in 8 bits while the layer trains on its bf16 weights (expert_linear_fp8; dim and hidden
+    multiples of 16).
+    decode_tokens: batches of up to so many tokens (16 at most) whose gradient nobody wants take expert_ffn, in any form of the weights."""
+
+    fp8, decode_tokens = False, 0   # of layers stored before these existed
 
     def __init__(self, dim: int, hidden: int, num_experts: int, k: int, renormalize: bool = True, bias: bool = False,
-                 prompt_tokens: int = 64, device=None):
+                 prompt_tokens: int = 64, device=None, fp8: bool = False, decode_tokens: int = 0):
         super().__init__()
+        if fp8 and (dim % 16 or hidden % 16):
+            raise ValueError("products in 8 bits need dim and hidden to be multiples of 16")
+        if not 0 <= decode_tokens <= few_tokens.TOKENS:
+            raise ValueError(f"decode_tokens must lie in [0, {few_tokens.TOKENS}]")
         self.dim, self.hidden, self.num_experts, self.k, self.renormalize = dim, hidden, num_experts, k, renormalize
-        self.prompt_tokens = prompt_tokens
+        self.prompt_tokens, self.fp8, self.decode_tokens = prompt_tokens, fp8, decode_tokens
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         mk = lambda *s: nn.Parameter(torch.empty(s, dtype=torch.bfloat16, device=device))  # noqa: E731
         self.router = mk(num_experts, dim)
@@ -129,16 +187,31 @@ class ExpertFFN(nn.Module):
     def quantized(self) -> bool:
         return self.up_codes is not None
 
+    @property
+    def form(self) -> str:
+        """How the expert weights are held: "bf16", "mx4" or "fp8"."""
+        return "bf16" if not self.quantized else "mx4" if self.up_scales.dim() == 4 else "fp8"
+
     @torch.no_grad()
-    def quantize_(self) -> "ExpertFFN":
-        """Hold the expert weights in 4 bits (bsr_mx4_quantize) and drop the bf16 ones; forward only from then on, with the
-        router and the biases frozen."""
+    def quantize_(self, form: str = "mx4") -> "ExpertFFN":
+        """Hold the expert weights in 4 bits ("mx4": bsr_mx4_quantize) or 8 ("fp8": bsr_fp8_quantize_blocks) and drop the bf16
+        ones; forward only from then on, with the router and the biases frozen."""
+        if form not in ("mx4", "fp8"):
+            raise ValueError(f"form must be 'mx4' or 'fp8', got {form!r}")
+        if self.quantized and form != self.form:
+            raise RuntimeError(f"the weights are held as {self.form} already")
         if not self.quantized:
-            up, down = mx4.quantize(self.up.data), mx4.quantize(self.down.data)
+            quantize = mx4.quantize if form == "mx4" else fp8.quantize_blocks
+            up, down = quantize(self.up.data), quantize(self.down.data)
             self.up_codes, self.up_scales, self.down_codes, self.down_scales = up.codes, up.scales, down.codes, down.scales
             self.up = self.down = None
             self.requires_grad_(False)
         return self
+
+    def _held(self):
+        """The compact up and down weights."""
+        make = mx4.Mx4 if self.form == "mx4" else fp8.Fp8Blocks
+        return make(self.up_codes, self.up_scales), make(self.down_codes, self.down_scales)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if self.quantized and torch.is_grad_enabled() and (x.requires_grad or any(
@@ -146,17 +219,24 @@ class ExpertFFN(nn.Module):
             raise RuntimeError("a quantised ExpertFFN has no backward pass")
         lead = x.shape[:-1]
         x = _whole(x.reshape(-1, self.dim).to(torch.bfloat16))
+        if 0 < x.shape[0] <= self.decode_tokens and not (torch.is_grad_enabled() and (
+                x.requires_grad or any(p.requires_grad for p in self.parameters()))):
+            held = (self.up, self.down) if not self.quantized else self._held()
+            return expert_ffn(x, self.router, *held, self.k, self.renormalize, self.up_bias, self.down_bias).reshape(*lead, self.dim)
         index, weight = route(F.linear(x, self.router), self.k, self.renormalize)
         plan = ExpertPlan.from_index(index, self.num_experts)
         if not self.quantized:
-            gate, up = expert_linear(plan, x, self.up, self.up_bias).chunk(2, dim=1)
-            y = expert_linear(plan, F.silu(gate) * up, self.down, self.down_bias, gather=False)
+            linear = expert_linear_fp8 if self.fp8 else expert_linear
+            gate, up = linear(plan, x, self.up, self.up_bias).chunk(2, dim=1)
+            y = linear(plan, F.silu(gate) * up, self.down, self.down_bias, gather=False)
             return combine(plan, y, weight).reshape(*lead, self.dim)
-        form = mx4.quantize if x.shape[0] > self.prompt_tokens else (lambda t: t)
-        h = mx4.expert_fwd(plan, form(x), mx4.Mx4(self.up_codes, self.up_scales), self.up_bias)
+        held, (quantize, expert_fwd) = self._held(), {"mx4": (mx4.quantize, mx4.expert_fwd),
+                                                      "fp8": (fp8.quantize_rows, fp8.expert_fwd)}[self.form]
+        form = quantize if x.shape[0] > self.prompt_tokens else (lambda t: t)
+        h = expert_fwd(plan, form(x), held[0], self.up_bias)
         gate, up = h.chunk(2, dim=1)
         h = form((F.silu(gate) * up).contiguous())
-        y = mx4.expert_fwd(plan, h, mx4.Mx4(self.down_codes, self.down_scales), self.down_bias, gather=False)
+        y = expert_fwd(plan, h, held[1], self.down_bias, gather=False)
         return experts.combine_fwd(plan, y, weight.detach()).reshape(*lead, self.dim)
 
     def extra_repr(self) -> str:
