@@ -68,6 +68,175 @@ __global__ __launch_bounds__(64) void k_fp8_simple(GemmArgs g, int ntiles) {
     store4_bf16(g.out + (int64_t)(t.at + l16) * g.Nout + col, acc[0], acc[1], acc[2], acc[3]);
 }
 
+// ------------------------------------------------------------------------------------------
+// Both sides in 8 bits, on the scaled matrix cores (v_mfma_scale_f32_16x16x128_f8f6f4: 16 x 16 x 128 products of codes, one scale
+// byte per 32 of them on each side, the same one for the four 32s of a group).
+//
+// What the instruction does to its sums, found with single products at all positions: the products of 8 neighbouring bytes are
+// aligned to the largest of their exponents and cut at 2^-13 of it (a sum of 8 such products has 13 to 16 bits); the sums of eight
+// and the accumulator are added in fp32. On normal data the result is off by 2^-20 of the sum of magnitudes (K = 4096), 2^-5 of
+// what rounding to bf16 does to it. The older instructions that lose nothing (16 x 16 x 32 on fp8) run at the rate of bf16.
+//
+// A step is one group of 128 columns: a row's 128 bytes of codes are staged like 64 bf16 columns, lane quarter h of a fragment takes
+// the chunks 2 h and 2 h + 1 on both sides. Two stages a side. The upper half of a wave's rows is read while the lower half is
+// multiplied; then every fragment of step s is in registers, a barrier frees its stage for the loads of s + 2, and the lower half of
+// the rows and, column by column as they fall free, the weights of s + 1 are read while the upper half is multiplied.
+// Scale bytes: rows' through LDS, four steps a load; weights' one uniform byte a step, 64 steps a load (one a lane).
+// ------------------------------------------------------------------------------------------
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// Chunk q of row r of a stage lies at q ^ swz_pairs(r): the 16 rows of a fragment, two chunks each, take different banks.
+__device__ __forceinline__ int swz_pairs(int r) { return Stager<kRows, 64, 1, kFrag16Pairs>::swz_rows(r); }
+
+template <int BM, int BN>
+constexpr int fp8_lds() {
+    const int stages = 2 * (BM + BN) * 128 + 2 * BM * 4, out = BM * BN * 2;
+    return stages > out ? stages : out;
+}
+
+// The tile of t's rows and the columns from col.
+template <int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void fp8_tile(const GemmArgs &g, const Rows &t, int col, unsigned char *smem) {
+    constexpr int NW = WM * WN, RT = BM / WM / 16, CT = BN / WN / 16, HR = RT / 2;
+    static_assert(CT == 4 && RT % 2 == 0 && BM % 64 == 0, "the schedule below");
+    constexpr int AB = BM * 128, BB = BN * 128, AS = 2 * (AB + BB);   // LDS: A, B, scales of A
+    const bool live = t.e < g.E;
+    const int e = live ? t.e : 0, kb = (g.C + 127) / 128, nb = (g.Nout + 127) / 128, steps = live ? kb : 0;
+    const int64_t wbytes = (int64_t)g.Nout * g.C, abytes = (int64_t)(g.gather ? g.T : g.R) * g.C;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = (wave % WM) * (BM / WM), n0 = (wave / WM) * (BN / WN);
+    const uint32_t base = lds_addr(smem);
+
+    f32x4 acc[RT][CT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if (steps > 0) {
+        // Codes: load j of a wave takes the rows 8 (wave + NW j) + lane / 8 of a side, chunk lane % 8 of 16 bytes (swizzled within
+        // the row). Rows past the tile's are read (or read zeros past the matrix) and only reach outputs that do not exist.
+        constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;
+        const int lr = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ swz_pairs(lane >> 3), left = (g.C - 16 * chunk + 127) / 128;
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(g.act, (uint32_t)abytes);
+        const __amdgpu_buffer_rsrc_t rb = make_rsrc(static_cast<const uint8_t *>(g.w) + e * wbytes, (uint32_t)wbytes);
+        uint32_t aoff[LA];
+#pragma unroll
+        for (int j = 0; j < LA; ++j) {
+            const int r = lr + 8 * NW * j;
+            int src = t.at + r;
+            if (g.gather) src = r < t.n ? g.gather[t.at + r] : -1;
+            aoff[j] = (unsigned)src < (unsigned)(g.gather ? g.T : g.R) ? (uint32_t)src * (uint32_t)g.C + 16u * chunk : kPast;
+        }
+        const uint32_t boff = (uint32_t)(col + lr) * (uint32_t)g.C + 16u * chunk, bstep = 8u * NW * (uint32_t)g.C;
+        auto issue_a = [&](int s, int j) __attribute__((always_inline)) {
+            dma16(ra, base + (uint32_t)(s & 1) * AB + (uint32_t)(wave + NW * j) * 1024u, s < left ? aoff[j] + (uint32_t)s * 128u : kPast, 0);
+        };
+        auto issue_b = [&](int s, int j) __attribute__((always_inline)) {
+            dma16(rb, base + 2 * AB + (uint32_t)(s & 1) * BB + (uint32_t)(wave + NW * j) * 1024u,
+                  s < left ? boff + (uint32_t)j * bstep + (uint32_t)s * 128u : kPast, 0);
+        };
+        // rows' scale bytes of 4 steps: a word a lane, 64 rows a load (waves past BM / 64 load the same words again)
+        const int arows = g.gather ? g.T : g.R, sw = wave % (BM / 64), ar = sw * 64 + lane;
+        const int arow = ar >= t.n ? -1 : g.gather ? g.gather[t.at + ar] : t.at + ar;
+        const __amdgpu_buffer_rsrc_t rsa = make_rsrc(g.act_scales, (uint32_t)((int64_t)((g.C + 511) / 512) * arows * 4));
+        const int slim = (unsigned)arow < (unsigned)arows ? steps : 0;
+        auto issue_scales = [&](int s) __attribute__((always_inline)) {   // s a multiple of 4
+            dma4(rsa, base + AS + (uint32_t)(s >> 2 & 1) * (BM * 4) + (uint32_t)sw * 256u,
+                 s < slim ? ((uint32_t)(s >> 2) * (uint32_t)arows + (uint32_t)arow) * 4u : kPast);
+        };
+        // weights' scale bytes: lane l keeps that of step l of 64
+        const uint8_t *ws = g.w_scales + ((int64_t)e * nb + min((col + n0) / 128, nb - 1)) * kb;
+        int held = ws[min(lane, kb - 1)];
+
+        const int h = lane >> 4, l16 = lane & 15;
+        const uint32_t lane_f = (uint32_t)(l16 * 128 + (((2 * h) ^ swz_pairs(l16)) << 4));
+        const uint32_t lane_a = base + (uint32_t)m0 * 128u + lane_f, lane_b = base + 2 * AB + (uint32_t)n0 * 128u + lane_f;
+        const uint32_t lane_s = base + AS + (uint32_t)(m0 + l16) * 4u;
+        i32x8 fa[RT], fb[CT];
+        int wa[RT];
+        auto frag = [&](uint32_t at) __attribute__((always_inline)) {
+            typedef __attribute__((address_space(3))) const i32x4 lds_i32x4;
+            const i32x4 lo = *(lds_i32x4 *)(at), hi = *(lds_i32x4 *)(at ^ 16u);
+            return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        };
+        auto read_a = [&](int s, int r) __attribute__((always_inline)) {
+            typedef __attribute__((address_space(3))) const uint8_t lds_u8;
+            fa[r] = frag(lane_a + (uint32_t)(s & 1) * AB + (uint32_t)r * 2048u);
+            wa[r] = *(lds_u8 *)(lane_s + (uint32_t)(s >> 2 & 1) * (BM * 4) + (uint32_t)r * 64u + (uint32_t)(s & 3));
+        };
+        auto read_b = [&](int s, int c) __attribute__((always_inline)) { fb[c] = frag(lane_b + (uint32_t)(s & 1) * BB + (uint32_t)c * 2048u); };
+        auto load = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < LA; ++j) issue_a(s, j);
+#pragma unroll
+            for (int j = 0; j < LB; ++j) issue_b(s, j);
+        };
+        issue_scales(0);
+        load(0);
+        load(1);
+        wait_vm<LA + LB, LA + LB>(LA + LB);
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < CT; ++c) read_b(0, c);
+#pragma unroll
+        for (int r = 0; r < HR; ++r) read_a(0, r);
+        for (int s = 0; s < steps; ++s) {
+            if ((s & 63) == 0 && s > 0) held = ws[min(s + lane, kb - 1)];
+            const int wb = __builtin_amdgcn_readlane(held, s & 63);
+            auto product = [&](int r, int c) __attribute__((always_inline)) {
+                acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[c], fa[r], acc[r][c], 0, 0, 0, wb, 0, wa[r]);
+            };
+#pragma unroll
+            for (int r = HR; r < RT; ++r) read_a(s, r);
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int r = 0; r < HR; ++r) product(r, c);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
+            wait_vm<0, 0>(0);                                     // step s + 1 has landed
+            __syncthreads();
+            if (((s + 2) & 3) == 0) issue_scales(s + 2);
+#pragma unroll
+            for (int r = 0; r < HR; ++r) read_a(s + 1, r);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+#pragma unroll
+                for (int j = c * LA / CT; j < (c + 1) * LA / CT; ++j) issue_a(s + 2, j);
+#pragma unroll
+                for (int j = c * LB / CT; j < (c + 1) * LB / CT; ++j) issue_b(s + 2, j);
+#pragma unroll
+                for (int r = HR; r < RT; ++r) product(r, c);
+                read_b(s + 1, c);
+            }
+        }
+        wait_vm<0, 0>(0);   // the last loads (of zeros) leave the stages
+    }
+    store_tile<BM, BN, WM, WN>(acc, live && g.bias ? g.bias + (int64_t)e * g.Nout + col : nullptr,
+                               g.out + (int64_t)t.at * g.Nout + col, g.Nout, t.n, g.Nout - col, smem);
+}
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM *WN * 64, 1) void k_fp8_fp8(GemmArgs g, int ntiles) {
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[fp8_lds<BM, BN>()];
+    const RowTiles<BM> tiles(g.offsets, g.E, g.R);
+    const int total = tiles.total;
+    const Piece piece = piece_of<BN == 256>(blockIdx.x, total * ntiles);
+    if (piece.tile < 0) return;
+    const TileOrder o = tile_order(piece.tile, total, ntiles, kRowsTogether);
+    const Rows t = tiles.find(o.row);
+    const int col = o.col * BN + (piece.half > 0 ? BN / 2 : 0);
+    if (t.n <= 0 || col >= g.Nout) return;
+    if constexpr (BN == 256) {
+        if (piece.half >= 0) return fp8_tile<BM, BN / 2, 4, 2>(g, t, col, smem);
+    }
+    fp8_tile<BM, BN, WM, WN>(g, t, col, smem);
+}
+
+// 256 x 256 tiles with 8 waves where the groups fill them, else 128 x 128 with 4, two work-groups a CU.
+bool wide(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 + 1) * ((cols + 255) / 256) >= 192; }
+
 template <bool Fp8Act>
 int32_t launch(const GemmArgs &g, void *stream, const char *what) {
     const int64_t ntiles = (g.Nout + 15) / 16, blocks = max_row_tiles(g.R, g.E, 16) * ntiles;
@@ -88,8 +257,20 @@ int32_t launch_expert_fwd_fp8(const ExpertShape &s, const uint16_t *X, const uin
 
 int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, const uint8_t *xscales, const uint8_t *codes,
                                   const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream) {
-    return launch<true>({xcodes, codes, xscales, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K}, stream,
-                        "bsr_expert_fwd_fp8_fp8");
+    const GemmArgs g{xcodes, codes, xscales, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
+    const char *what = "bsr_expert_fwd_fp8_fp8";
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool w = wide(s.R, s.E, s.N);
+    const int64_t bm = w ? 256 : 128, ntiles = (s.N + bm - 1) / bm;
+    const int64_t blocks = max_row_tiles(s.R, s.E, bm) * ntiles + (w ? kPieces : 0);
+    if (const int32_t bad = check_grid(blocks, 512, what)) return bad;
+    if (w)
+        hipLaunchKernelGGL((k_fp8_fp8<256, 256, 2, 4>), dim3((unsigned)blocks), dim3(512), 0, st, g, (int)ntiles);
+    else
+        hipLaunchKernelGGL((k_fp8_fp8<128, 128, 2, 2>), dim3((unsigned)blocks), dim3(256), 0, st, g, (int)ntiles);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return fail(BSR_ERR_HIP, std::string(what) + ": " + hipGetErrorString(err));
+    return BSR_OK;
 }
 
 }  // namespace bsr
