@@ -39,16 +39,6 @@ __global__ __launch_bounds__(256) void k_fp8_rows_quantize(const uint16_t *__res
     }
 }
 
-// out[j] = byte j of a[0], a[1], a[2], a[3], lowest first.
-__device__ __forceinline__ void transpose4(const uint32_t (&a)[4], uint32_t (&out)[4]) {
-    const uint32_t t0 = __builtin_amdgcn_perm(a[1], a[0], 0x05010400), t1 = __builtin_amdgcn_perm(a[1], a[0], 0x07030602);
-    const uint32_t t2 = __builtin_amdgcn_perm(a[3], a[2], 0x05010400), t3 = __builtin_amdgcn_perm(a[3], a[2], 0x07030602);
-    out[0] = __builtin_amdgcn_perm(t2, t0, 0x05040100);
-    out[1] = __builtin_amdgcn_perm(t2, t0, 0x07060302);
-    out[2] = __builtin_amdgcn_perm(t3, t1, 0x05040100);
-    out[3] = __builtin_amdgcn_perm(t3, t1, 0x07060302);
-}
-
 // One 128 x 128 block a work-group: thread t holds rows 8 (t / 16) + 0 .. 7 of the 8 columns from 8 (t % 16), so that a
 // transposed row's 8 codes come from its own registers.
 __global__ __launch_bounds__(256) void k_fp8_blocks_quantize(const uint16_t *__restrict__ W, int N, int K, int nb, int kb,

@@ -39,6 +39,16 @@ __device__ __forceinline__ uint32_t fp8_quantize4(uint32_t w0, uint32_t w1, floa
     return c;
 }
 
+// out[j] = byte j of a[0], a[1], a[2], a[3], lowest first.
+__device__ __forceinline__ void transpose4(const uint32_t (&a)[4], uint32_t (&out)[4]) {
+    const uint32_t t0 = __builtin_amdgcn_perm(a[1], a[0], 0x05010400), t1 = __builtin_amdgcn_perm(a[1], a[0], 0x07030602);
+    const uint32_t t2 = __builtin_amdgcn_perm(a[3], a[2], 0x05010400), t3 = __builtin_amdgcn_perm(a[3], a[2], 0x07030602);
+    out[0] = __builtin_amdgcn_perm(t2, t0, 0x05040100);
+    out[1] = __builtin_amdgcn_perm(t2, t0, 0x07060302);
+    out[2] = __builtin_amdgcn_perm(t3, t1, 0x05040100);
+    out[3] = __builtin_amdgcn_perm(t3, t1, 0x07060302);
+}
+
 // The 8 values of 8 codes.
 __device__ __forceinline__ bf16x8 fp8_expand8(uint2 codes, float scale) {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes.x, scale, false);

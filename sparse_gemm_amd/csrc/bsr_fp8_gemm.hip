@@ -78,10 +78,15 @@ __global__ __launch_bounds__(64) void k_fp8_simple(GemmArgs g, int ntiles) {
 // what rounding to bf16 does to it. The older instructions that lose nothing (16 x 16 x 32 on fp8) run at the rate of bf16.
 //
 // A step is one group of 128 columns: a row's 128 bytes of codes are staged like 64 bf16 columns, lane quarter h of a fragment takes
-// the chunks 2 h and 2 h + 1 on both sides. Two stages a side. The upper half of a wave's rows is read while the lower half is
-// multiplied; then every fragment of step s is in registers, a barrier frees its stage for the loads of s + 2, and the lower half of
-// the rows and, column by column as they fall free, the weights of s + 1 are read while the upper half is multiplied.
-// Scale bytes: rows' through LDS, four steps a load; weights' one uniform byte a step, 64 steps a load (one a lane).
+// the chunks 2 h and 2 h + 1 on both sides. Of B two stages are held, of A a ring of units of 64 rows, a little less than three
+// stages' (the scale bytes have the rest of the LDS). A wave's rows are multiplied two row tiles at a time, the next two being read
+// meanwhile. Before the last two every fragment of step s is in registers, and a barrier frees its stage: beside the last two the
+// loads of s + 2 go out, and the first two row tiles and, column by column as they fall free, the weights of s + 1 are read. The
+// ring's spare units of A are loaded before the barrier.
+// Scale bytes: rows' through LDS, a word for 4 steps (loaded in each, without a branch in the loop); weights' one uniform byte a
+// step, 64 steps a load (one a lane).
+// Of 16384 x 4096 -> 4096 in 227 us: without the loads 190, without LDS reads either 169; with all steps' loads from the same lines
+// 215. Fragments of a whole half step ahead, which leave the compiler no registers: 239.
 // ------------------------------------------------------------------------------------------
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -89,18 +94,21 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // Chunk q of row r of a stage lies at q ^ swz_pairs(r): the 16 rows of a fragment, two chunks each, take different banks.
 __device__ __forceinline__ int swz_pairs(int r) { return Stager<kRows, 64, 1, kFrag16Pairs>::swz_rows(r); }
 
+// LDS of a tile: of A a ring of units of 64 rows, of B two stages, of A's scale bytes two pieces of 4 steps (a word a row).
 template <int BM, int BN>
-constexpr int fp8_lds() {
-    const int stages = 2 * (BM + BN) * 128 + 2 * BM * 4, out = BM * BN * 2;
-    return stages > out ? stages : out;
-}
+struct Fp8Layout {
+    static constexpr int kUnits = BM / 64, kRing = BM == 256 ? 11 : 5, kUnit = 64 * 128;
+    static constexpr int kB = kRing * kUnit, kS = kB + 2 * BN * 128, kStages = kS + 2 * BM * 4, kOut = BM * BN * 2;
+    static constexpr int kLds = kStages > kOut ? kStages : kOut;
+};
 
 // The tile of t's rows and the columns from col.
 template <int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void fp8_tile(const GemmArgs &g, const Rows &t, int col, unsigned char *smem) {
-    constexpr int NW = WM * WN, RT = BM / WM / 16, CT = BN / WN / 16, HR = RT / 2;
+    constexpr int NW = WM * WN, RT = BM / WM / 16, CT = BN / WN / 16;
     static_assert(CT == 4 && RT % 2 == 0 && BM % 64 == 0, "the schedule below");
-    constexpr int AB = BM * 128, BB = BN * 128, AS = 2 * (AB + BB);   // LDS: A, B, scales of A
+    using L = Fp8Layout<BM, BN>;
+    constexpr int U = L::kUnits, RU = L::kRing, EARLY = RU - 2 * U;   // units of a step that are loaded in the first half
     const bool live = t.e < g.E;
     const int e = live ? t.e : 0, kb = (g.C + 127) / 128, nb = (g.Nout + 127) / 128, steps = live ? kb : 0;
     const int64_t wbytes = (int64_t)g.Nout * g.C, abytes = (int64_t)(g.gather ? g.T : g.R) * g.C;
@@ -130,86 +138,109 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs &g, const Rows &t, int c
             aoff[j] = (unsigned)src < (unsigned)(g.gather ? g.T : g.R) ? (uint32_t)src * (uint32_t)g.C + 16u * chunk : kPast;
         }
         const uint32_t boff = (uint32_t)(col + lr) * (uint32_t)g.C + 16u * chunk, bstep = 8u * NW * (uint32_t)g.C;
-        auto issue_a = [&](int s, int j) __attribute__((always_inline)) {
-            dma16(ra, base + (uint32_t)(s & 1) * AB + (uint32_t)(wave + NW * j) * 1024u, s < left ? aoff[j] + (uint32_t)s * 128u : kPast, 0);
+        auto slot = [&](int q, int u) __attribute__((always_inline)) { return (uint32_t)(q + u - (q + u >= RU ? RU : 0)) * L::kUnit; };
+        auto issue_a = [&](int s, int q, int u) __attribute__((always_inline)) {   // unit u of step s, whose first unit lies at q
+#pragma unroll
+            for (int i = 0; i < 8 / NW; ++i) {
+                const int j = u * (8 / NW) + i;
+                dma16(ra, base + slot(q, u) + (uint32_t)(wave + NW * i) * 1024u, s < left ? aoff[j] + (uint32_t)s * 128u : kPast, 0);
+            }
         };
         auto issue_b = [&](int s, int j) __attribute__((always_inline)) {
-            dma16(rb, base + 2 * AB + (uint32_t)(s & 1) * BB + (uint32_t)(wave + NW * j) * 1024u,
+            dma16(rb, base + L::kB + (uint32_t)(s & 1) * (BN * 128) + (uint32_t)(wave + NW * j) * 1024u,
                   s < left ? boff + (uint32_t)j * bstep + (uint32_t)s * 128u : kPast, 0);
         };
         // rows' scale bytes of 4 steps: a word a lane, 64 rows a load (waves past BM / 64 load the same words again)
-        const int arows = g.gather ? g.T : g.R, sw = wave % (BM / 64), ar = sw * 64 + lane;
+        const int arows = g.gather ? g.T : g.R, sw = wave % U, ar = sw * 64 + lane;
         const int arow = ar >= t.n ? -1 : g.gather ? g.gather[t.at + ar] : t.at + ar;
         const __amdgpu_buffer_rsrc_t rsa = make_rsrc(g.act_scales, (uint32_t)((int64_t)((g.C + 511) / 512) * arows * 4));
         const int slim = (unsigned)arow < (unsigned)arows ? steps : 0;
-        auto issue_scales = [&](int s) __attribute__((always_inline)) {   // s a multiple of 4
-            dma4(rsa, base + AS + (uint32_t)(s >> 2 & 1) * (BM * 4) + (uint32_t)sw * 256u,
-                 s < slim ? ((uint32_t)(s >> 2) * (uint32_t)arows + (uint32_t)arow) * 4u : kPast);
+        auto issue_scales = [&](int s) __attribute__((always_inline)) {   // those of s and its three neighbours
+            dma4(rsa, base + L::kS + (uint32_t)(s >> 2 & 1) * (BM * 4) + (uint32_t)sw * 256u,
+                 (s & ~3) < slim ? ((uint32_t)(s >> 2) * (uint32_t)arows + (uint32_t)arow) * 4u : kPast);
         };
         // weights' scale bytes: lane l keeps that of step l of 64
         const uint8_t *ws = g.w_scales + ((int64_t)e * nb + min((col + n0) / 128, nb - 1)) * kb;
         int held = ws[min(lane, kb - 1)];
 
+        // a lane's two chunks of a fragment, for the first row of a unit, and for column tile 0 and stage 0
         const int h = lane >> 4, l16 = lane & 15;
-        const uint32_t lane_f = (uint32_t)(l16 * 128 + (((2 * h) ^ swz_pairs(l16)) << 4));
-        const uint32_t lane_a = base + (uint32_t)m0 * 128u + lane_f, lane_b = base + 2 * AB + (uint32_t)n0 * 128u + lane_f;
-        const uint32_t lane_s = base + AS + (uint32_t)(m0 + l16) * 4u;
+        const uint32_t f0 = (uint32_t)(l16 * 128 + (((2 * h) ^ swz_pairs(l16)) << 4)), f1 = f0 ^ 16u;
+        const uint32_t b0 = base + L::kB + (uint32_t)n0 * 128u + f0, b1 = base + L::kB + (uint32_t)n0 * 128u + f1;
+        const uint32_t lane_s = base + L::kS + (uint32_t)(m0 + l16) * 4u;
         i32x8 fa[RT], fb[CT];
         int wa[RT];
-        auto frag = [&](uint32_t at) __attribute__((always_inline)) {
-            typedef __attribute__((address_space(3))) const i32x4 lds_i32x4;
-            const i32x4 lo = *(lds_i32x4 *)(at), hi = *(lds_i32x4 *)(at ^ 16u);
+        typedef __attribute__((address_space(3))) const i32x4 lds_i32x4;
+        typedef __attribute__((address_space(3))) const uint8_t lds_u8;
+        auto frag = [&](uint32_t p0, uint32_t p1) __attribute__((always_inline)) {
+            const i32x4 lo = *(lds_i32x4 *)p0, hi = *(lds_i32x4 *)p1;
             return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         };
-        auto read_a = [&](int s, int r) __attribute__((always_inline)) {
-            typedef __attribute__((address_space(3))) const uint8_t lds_u8;
-            fa[r] = frag(lane_a + (uint32_t)(s & 1) * AB + (uint32_t)r * 2048u);
-            wa[r] = *(lds_u8 *)(lane_s + (uint32_t)(s >> 2 & 1) * (BM * 4) + (uint32_t)r * 64u + (uint32_t)(s & 3));
+        auto read_pair = [&](int s, int q, int pair) __attribute__((always_inline)) {   // of the step s whose first unit lies at q
+            const int r0 = m0 + 32 * pair;
+            const uint32_t at = base + slot(q, r0 / 64) + (uint32_t)(r0 % 64) * 128u;
+            const uint32_t sb = lane_s + (uint32_t)(s >> 2 & 1) * (BM * 4) + (uint32_t)(s & 3);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fa[2 * pair + i] = frag(at + f0 + (uint32_t)(i * 2048), at + f1 + (uint32_t)(i * 2048));
+                wa[2 * pair + i] = *(lds_u8 *)(sb + (uint32_t)((2 * pair + i) * 64));
+            }
         };
-        auto read_b = [&](int s, int c) __attribute__((always_inline)) { fb[c] = frag(lane_b + (uint32_t)(s & 1) * BB + (uint32_t)c * 2048u); };
-        auto load = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < LA; ++j) issue_a(s, j);
-#pragma unroll
-            for (int j = 0; j < LB; ++j) issue_b(s, j);
+        auto read_b = [&](int st, int c) __attribute__((always_inline)) {
+            fb[c] = frag(b0 + (uint32_t)(st * (BN * 128) + c * 2048), b1 + (uint32_t)(st * (BN * 128) + c * 2048));
         };
         issue_scales(0);
-        load(0);
-        load(1);
-        wait_vm<LA + LB, LA + LB>(LA + LB);
+#pragma unroll
+        for (int u = 0; u < U; ++u) issue_a(0, 0, u);
+#pragma unroll
+        for (int j = 0; j < LB; ++j) issue_b(0, j);
+#pragma unroll
+        for (int u = 0; u < U; ++u) issue_a(1, U, u);
+#pragma unroll
+        for (int j = 0; j < LB; ++j) issue_b(1, j);
+        wait_vm<LA + LB, LA + LB>(0);
         __syncthreads();
 #pragma unroll
         for (int c = 0; c < CT; ++c) read_b(0, c);
-#pragma unroll
-        for (int r = 0; r < HR; ++r) read_a(0, r);
-        for (int s = 0; s < steps; ++s) {
-            if ((s & 63) == 0 && s > 0) held = ws[min(s + lane, kb - 1)];
-            const int wb = __builtin_amdgcn_readlane(held, s & 63);
+        read_pair(0, 0, 0);
+        for (int s = 0, q = 0;;) {   // q: unit of the ring where step s begins
+            const int wb = __builtin_amdgcn_readlane(held, s & 63), st = s & 1;
+            const int qn = q + U - (q + U >= RU ? RU : 0), q2 = qn + U - (qn + U >= RU ? RU : 0);
             auto product = [&](int r, int c) __attribute__((always_inline)) {
                 acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[c], fa[r], acc[r][c], 0, 0, 0, wb, 0, wa[r]);
             };
 #pragma unroll
-            for (int r = HR; r < RT; ++r) read_a(s, r);
+            for (int pair = 0; pair < RT / 2 - 1; ++pair) {
+                read_pair(s, q, pair + 1);
+                constexpr int SLOTS = RT == 8 ? 2 : 1;   // pairs beside which units go out: 1 and 2, or the only one
+                if (RT < 8 || pair > 0) {
+                    const int k = RT < 8 ? 0 : pair - 1;
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
+                    for (int u = k * EARLY / SLOTS; u < (k + 1) * EARLY / SLOTS; ++u) issue_a(s + 2, q2, u);
+                }
 #pragma unroll
-                for (int r = 0; r < HR; ++r) product(r, c);
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int r = 2 * pair; r < 2 * pair + 2; ++r) product(r, c);
+            }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every LDS read of step s is in registers
-            wait_vm<0, 0>(0);                                     // step s + 1 has landed
+            wait_vm<EARLY * 8 / NW, EARLY * 8 / NW>(0);           // step s + 1 has landed
             __syncthreads();
-            if (((s + 2) & 3) == 0) issue_scales(s + 2);
+            read_pair(s + 1, qn, 0);
+            issue_scales(s + 2);
 #pragma unroll
-            for (int r = 0; r < HR; ++r) read_a(s + 1, r);
+            for (int u = EARLY; u < U; ++u) issue_a(s + 2, q2, u);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
 #pragma unroll
-                for (int j = c * LA / CT; j < (c + 1) * LA / CT; ++j) issue_a(s + 2, j);
-#pragma unroll
                 for (int j = c * LB / CT; j < (c + 1) * LB / CT; ++j) issue_b(s + 2, j);
 #pragma unroll
-                for (int r = HR; r < RT; ++r) product(r, c);
-                read_b(s + 1, c);
+                for (int r = RT - 2; r < RT; ++r) product(r, c);
+                read_b(st ^ 1, c);
             }
+            if (++s == steps) break;
+            q = qn;
+            if ((s & 63) == 0) held = ws[min(s + lane, kb - 1)];
         }
         wait_vm<0, 0>(0);   // the last loads (of zeros) leave the stages
     }
@@ -219,10 +250,10 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs &g, const Rows &t, int c
 
 template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM *WN * 64, 1) void k_fp8_fp8(GemmArgs g, int ntiles) {
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[fp8_lds<BM, BN>()];
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[Fp8Layout<BM, BN>::kLds];
     const RowTiles<BM> tiles(g.offsets, g.E, g.R);
     const int total = tiles.total;
-    const Piece piece = piece_of<BN == 256>(blockIdx.x, total * ntiles);
+    const Piece piece = piece_of<BN == 256, true>(blockIdx.x, total * ntiles);
     if (piece.tile < 0) return;
     const TileOrder o = tile_order(piece.tile, total, ntiles, kRowsTogether);
     const Rows t = tiles.find(o.row);
