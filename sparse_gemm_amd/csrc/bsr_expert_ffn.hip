@@ -22,96 +22,28 @@ namespace {
 using namespace dev;
 
 constexpr int kTok = BSR_EXPERT_FFN_TOKENS;
-constexpr int kWaves = 8;
+constexpr int kWaves = 16;             // of a work-group of the products: one a CU
+constexpr int kThreads = kWaves * 64;
+constexpr int kNone = 255;
 
 struct FfnArgs {
     const uint16_t *x;
     int T, dim, hidden, E, k;
+    int renorm, route, parts;   // route: who finds the experts (Route); parts: pieces of the logits' sums
     const uint16_t *router;
     const void *up, *down;
     const uint8_t *up_scales, *down_scales;
     const uint16_t *up_bias, *down_bias;
     uint16_t *out;
-    float *logits;
-    int32_t *index;
-    float *weight;
-    uint16_t *h;   // [T * k][hidden]
+    float *logits;     // [parts][T][E]
+    int32_t *index;    // [T][k]
+    float *weight;     // [T][k]
+    uint16_t *h;       // [T * k][hidden]
 };
 
-// ------------------------------------------------------------------------------------------
-// logits[t][e] = x[t] . router[e], one expert a work-group
-// ------------------------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void k_ffn_logits(FfnArgs g) {
-    __shared__ float part[4][kTok];
-    const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    float acc[kTok] = {};
-    for (int c = threadIdx.x * 8; c < g.dim; c += 2048) {
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(g.router + (int64_t)e * g.dim + c);
-#pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            if (t >= g.T) break;
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(g.x + (int64_t)t * g.dim + c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[t] = fmaf(__uint_as_float(v[j] << 16), __uint_as_float(w[j] << 16), acc[t]);
-                acc[t] = fmaf(__uint_as_float(v[j] & 0xFFFF0000u), __uint_as_float(w[j] & 0xFFFF0000u), acc[t]);
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) acc[t] += __shfl_xor(acc[t], d);
-        if (lane == 0) part[wave][t] = acc[t];
-    }
-    __syncthreads();
-    const int t = threadIdx.x;
-    if (t < g.T) g.logits[(int64_t)t * g.E + e] = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
-}
-
-// ------------------------------------------------------------------------------------------
-// The experts that some token chose, in ascending order, and each token's slot in them.
-// ------------------------------------------------------------------------------------------
-struct Chosen {
-    uint32_t bits[kMaxExperts / 32];
-    uint16_t expert[kTok * kMaxSlots];
-    uint8_t slot[kTok * kMaxSlots][kTok];   // [chosen expert][token]: its slot there, or kNone
-    int count;
-};
-constexpr int kNone = 255;
-
-__device__ __forceinline__ int place_of(const Chosen &c, int e) {   // chosen experts below e
-    int n = __popc(c.bits[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int w = 0; w < e >> 5; ++w) n += __popc(c.bits[w]);
-    return n;
-}
-
-__device__ __forceinline__ void choose(const FfnArgs &g, Chosen &c) {
-    const int slots = g.T * g.k;
-    for (int i = threadIdx.x; i < kMaxExperts / 32; i += blockDim.x) c.bits[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < slots; i += blockDim.x) {
-        const int e = g.index[i];
-        if ((unsigned)e < (unsigned)g.E) atomicOr(&c.bits[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int n = 0;
-        for (int w = 0; w < kMaxExperts / 32; ++w) n += __popc(c.bits[w]);
-        c.count = n;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < c.count * (kTok / 4); i += blockDim.x) reinterpret_cast<uint32_t *>(c.slot)[i] = ~0u;
-    __syncthreads();
-    for (int i = threadIdx.x; i < slots; i += blockDim.x) {
-        const int e = g.index[i];
-        if ((unsigned)e >= (unsigned)g.E) continue;
-        const int a = place_of(c, e);
-        c.expert[a] = (uint16_t)e;   // the same value from every slot
-        c.slot[a][i / g.k] = (uint8_t)(i % g.k);
-    }
-    __syncthreads();
-}
+// Who finds the experts: the work-groups of the up product, each for itself, from x and the router or from logits that a
+// launch before has summed in pieces; or the router's kernel.
+enum Route { kAllInOne, kFromLogits, kRouted };
 
 // ------------------------------------------------------------------------------------------
 // Lines of weights
@@ -145,7 +77,7 @@ struct Held {
     uint32_t byte;
 };
 
-// The line s of the rows n0 .. n0 + 7 (n0 a multiple of 8); zeros outside of the matrix.
+// Line s of the rows n0 .. n0 + 7 (n0 a multiple of 8); zeros outside of the matrix.
 template <int Form>
 __device__ __forceinline__ Held load_line(const Matrix<Form> &m, int n0, int s) {
     const int lane = threadIdx.x & 63, r = lane & 7, chunk = 2 * (lane >> 4) + (lane >> 3 & 1);
@@ -168,131 +100,405 @@ __device__ __forceinline__ bf16x8 expand(const Held &v, int p) {
     return mx4_expand8(v.codes[p], mx4_scale_bits(v.byte));
 }
 
-// Values of 16 tokens' rows for product p of the even (odd = 0) or odd chunks of line s; row: byte offset of this lane's
-// token (lane % 16) or kPast.
-template <int Form>
-__device__ __forceinline__ bf16x8 load_tokens(__amdgpu_buffer_rsrc_t x, uint32_t row, int cols, int s, int p, int odd) {
-    const int lane = threadIdx.x & 63, c = s * Line<Form>::kValues + (2 * (lane >> 4) + odd) * Line<Form>::kV + 8 * p;
+// The other operand: 16 tokens' values for the even chunks and, apart, for the odd ones; or, up to 8 tokens (Few), those for the
+// even chunks in the lower and for the odd chunks in the upper eight of its 16 columns: one product does for both.
+template <bool Few>
+struct Tokens {
+    static constexpr int kN = Few ? 1 : 2;          // operands a product
+    static constexpr int kOdd = Few ? 40 : 32;      // from the lane with the even chunks' sums to that with the odd chunks'
+    static __device__ __forceinline__ int token() { return threadIdx.x & (Few ? 7 : 15); }
+    static __device__ __forceinline__ int odd(int i) { return Few ? threadIdx.x >> 3 & 1 : i; }
+};
+
+// Operand i for product p of line s; row: byte offset of this lane's token or kPast.
+template <int Form, bool Few>
+__device__ __forceinline__ bf16x8 load_tokens(__amdgpu_buffer_rsrc_t x, uint32_t row, int cols, int s, int p, int i) {
+    const int lane = threadIdx.x & 63, c = s * Line<Form>::kValues + (2 * (lane >> 4) + Tokens<Few>::odd(i)) * Line<Form>::kV + 8 * p;
     return buf_load16(x, c < cols && row != kPast ? row + (uint32_t)c * 2u : kPast, 0);
 }
 
-__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-// Partial sums of a wave: item v of lane l is weight row 4 (l / 16 % 2) + v, token l % 16; the lanes from 32 on hold the odd chunks'.
-__device__ __forceinline__ f32x4 halves(f32x4 even, f32x4 odd) { return (threadIdx.x & 32) ? odd : even; }
-
-// Sum of (row, token) over the waves' partial sums.
-__device__ __forceinline__ float joined(const f32x4 (*part)[64], int row, int token) {
-    float s = 0.f;
+// Sums of one set of 8 rows: item v of lane l is row 4 (l / 16 % 2) + v, token l % 16 (Few: l % 8); those of the even chunks in the
+// lanes below 32 (Few: and l % 16 below 8), of the odd chunks in the lanes from 32 on (Few: and l % 16 from 8 on).
+template <bool Few>
+struct Sums {
+    f32x4 v[Tokens<Few>::kN];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-        s += part[w][(row >> 2) * 16 + token][row & 3] + part[w][(row >> 2) * 16 + 32 + token][row & 3];
-    return s;
+        for (int i = 0; i < Tokens<Few>::kN; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    __device__ __forceinline__ void add(bf16x8 w, const bf16x8 (&x)[Tokens<Few>::kN]) {
+#pragma unroll
+        for (int i = 0; i < Tokens<Few>::kN; ++i) v[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[i], v[i], 0, 0, 0);
+    }
+    __device__ __forceinline__ f32x4 all() const {
+        const f32x4 even = v[0], odd = v[Tokens<Few>::kN - 1];   // values: a choice between their places would put both into memory
+        const bool upper = threadIdx.x & 32;
+        return f32x4{upper ? odd[0] : even[0], upper ? odd[1] : even[1], upper ? odd[2] : even[2], upper ? odd[3] : even[3]};
+    }
+};
+
+// The waves' sums of one set of 8 rows. A group of 16 lanes joins 4 rows of one token: lane w takes those of wave w, 65 vectors apart
+// so that the 16 take different banks, and four row rotations add them up, in an order that is the same for every lane. With one
+// thread a sum, 32 reads each, the join took longer than the weights of a unit.
+typedef f32x4 Part[kWaves][65];
+
+template <bool Few>
+struct Group {
+    static constexpr int kCount = Few ? 16 : 32;   // of a set
+    int token, quad;                               // rows 4 quad .. 4 quad + 3
+    __device__ __forceinline__ explicit Group(int j) : token(j % (kCount / 2)), quad(j / (kCount / 2)) {}
+    __device__ __forceinline__ f32x4 join(const Part &part) const {
+        const int w = threadIdx.x & 15, at = quad * 16 + token;
+        f32x4 v = part[w][at] + part[w][at + Tokens<Few>::kOdd];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), 0x128, 0xf, 0xf, true));
+            v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), 0x124, 0xf, 0xf, true));
+            v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), 0x122, 0xf, 0xf, true));
+            v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), 0x121, 0xf, 0xf, true));
+        }
+        return v;
+    }
+};
+
+// Item (lane % 4) of v.
+__device__ __forceinline__ float pick(f32x4 v) {
+    const int i = threadIdx.x & 3;
+    const float a = i & 1 ? v[1] : v[0], b = i & 1 ? v[3] : v[2];
+    return i & 2 ? b : a;
 }
 
 // ------------------------------------------------------------------------------------------
-// h: 8 gate rows and their up rows of one chosen expert a unit; the waves split the columns.
+// Router
 // ------------------------------------------------------------------------------------------
-template <int Form>
-__global__ __launch_bounds__(kWaves * 64) void k_ffn_up(FfnArgs g) {
-    using L = Line<Form>;
-    __shared__ Chosen chosen;
-    __shared__ f32x4 part[2][kWaves][64];
-    choose(g, chosen);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = lane & 15;
+
+// Sums of 8 experts' logits over the lines first, first + step, ... below `to` by one wave.
+template <bool Few>
+__device__ __forceinline__ f32x4 logit_sums(const FfnArgs &g, int e0, int first, int step, int to) {
+    const Matrix<BSR_WEIGHTS_BF16> m(g.router, nullptr, 0, g.E, g.dim);
     const __amdgpu_buffer_rsrc_t x = make_rsrc(g.x, (uint32_t)(g.T * g.dim) * 2u);
+    const int token = Tokens<Few>::token();
     const uint32_t row = token < g.T ? (uint32_t)(token * g.dim) * 2u : kPast;
-    const int tiles = g.hidden / 8, steps = (g.dim + L::kValues - 1) / L::kValues, units = chosen.count * tiles;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        const int a = u / tiles, n0 = u % tiles * 8, e = __builtin_amdgcn_readfirstlane(chosen.expert[a]);
-        const Matrix<Form> m(g.up, g.up_scales, e, 2 * g.hidden, g.dim);
-        f32x4 acc[2][2] = {};   // [gate, up][even, odd]
-        for (int s = wave; s < steps; s += kWaves) {
-            const Held gate = load_line<Form>(m, n0, s), up = load_line<Form>(m, g.hidden + n0, s);
+    Sums<Few> acc;
+    acc.clear();
+#pragma unroll 4
+    for (int s = first; s < to; s += step) {
+        const Held w = load_line(m, e0, s);
+        bf16x8 v[Tokens<Few>::kN];
 #pragma unroll
-            for (int p = 0; p < L::kP; ++p) {
-                const bf16x8 wg = expand<Form>(gate, p), wu = expand<Form>(up, p);
-#pragma unroll
-                for (int odd = 0; odd < 2; ++odd) {
-                    const bf16x8 v = load_tokens<Form>(x, row, g.dim, s, p, odd);
-                    acc[0][odd] = mfma16(wg, v, acc[0][odd]);
-                    acc[1][odd] = mfma16(wu, v, acc[1][odd]);
+        for (int i = 0; i < Tokens<Few>::kN; ++i) v[i] = load_tokens<BSR_WEIGHTS_BF16, Few>(x, row, g.dim, s, 0, i);
+        acc.add(expand<BSR_WEIGHTS_BF16>(w, 0), v);
+    }
+    return acc.all();
+}
+
+// The joined logits of 8 experts to out[t][E].
+template <bool Few>
+__device__ __forceinline__ void store_logits(const FfnArgs &g, const Part &part, int e0, float *out) {
+    if (threadIdx.x >= Group<Few>::kCount * 16) return;
+    const Group<Few> j(threadIdx.x >> 4);
+    const float l = pick(j.join(part));
+    const int e = e0 + 4 * j.quad + (threadIdx.x & 3);
+    if ((threadIdx.x & 15) < 4 && j.token < g.T && e < g.E) out[j.token * g.E + e] = l;
+}
+
+// 8 experts and one of `parts` pieces of the columns a work-group.
+template <bool Few>
+__global__ __launch_bounds__(kThreads) void k_ffn_logits(FfnArgs g) {
+    __shared__ Part part;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), e0 = blockIdx.x * 8;
+    const int lines = (g.dim + 63) / 64, per = (lines + g.parts - 1) / g.parts, from = blockIdx.y * per;
+    part[wave][lane] = logit_sums<Few>(g, e0, from + wave, kWaves, min(from + per, lines));
+    __syncthreads();
+    store_logits<Few>(g, part, e0, g.logits + (int64_t)blockIdx.y * g.T * g.E);
+}
+
+// The experts that some token chose, in ascending order, and each token's slot in them.
+struct Chosen {
+    int16_t index[kTok * kMaxSlots];
+    uint32_t bits[kMaxExperts / 32];
+    uint16_t expert[kTok * kMaxSlots];
+    uint8_t slot[kTok * kMaxSlots][kTok];   // [chosen expert][token]: its slot there, or kNone
+    int count;
+};
+
+__device__ __forceinline__ int place_of(const Chosen &c, int e) {   // chosen experts below e
+    int n = __popc(c.bits[e >> 5] & ((1u << (e & 31)) - 1u));
+    for (int w = 0; w < e >> 5; ++w) n += __popc(c.bits[w]);
+    return n;
+}
+
+// From c.index.
+__device__ __forceinline__ void choose(const FfnArgs &g, Chosen &c) {
+    const int slots = g.T * g.k, words = (g.E + 31) / 32, i = threadIdx.x;   // slots <= 512 threads
+    if (i < words) c.bits[i] = 0;
+    __syncthreads();
+    const int e = i < slots ? c.index[i] : -1;
+    if (e >= 0) atomicOr(&c.bits[e >> 5], 1u << (e & 31));
+    __syncthreads();
+    int n = 0;
+    for (int w = 0; w < words; ++w) n += __popc(c.bits[w]);
+    if (i == 0) c.count = n;
+    for (int j = i; j < n * (kTok / 4); j += kThreads) reinterpret_cast<uint32_t *>(c.slot)[j] = ~0u;
+    __syncthreads();
+    if (e >= 0) {
+        const int a = place_of(c, e);
+        c.expert[a] = (uint16_t)e;   // the same value from every slot
+        c.slot[a][i / g.k] = (uint8_t)(i % g.k);
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void read_index(const FfnArgs &g, Chosen &c) {
+    const int i = threadIdx.x;
+    if (i < g.T * g.k) {
+        const int e = g.index[i];
+        c.index[i] = (unsigned)e < (unsigned)g.E ? (int16_t)e : (int16_t)-1;
+    }
+}
+
+// Router in the work-group: logits, ranks of all experts of a token by counting the better ones (ties to the lowest; NaN is
+// better than all; -infinity is never chosen), as bsr_router_fwd. One work-group writes index and weight for the down product.
+constexpr int kMostLogits = 4096;       // T * E of a work-group that routes
+constexpr int kMostRanks = 1 << 17;     // T * E * E: 128 comparisons a thread
+
+template <bool Few>
+__device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, float *logit) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (g.route == kAllInOne) {
+        for (int e0 = 0; e0 < g.E; e0 += 8) {
+            if (e0) __syncthreads();
+            part[wave][lane] = logit_sums<Few>(g, e0, wave, kWaves, (g.dim + 63) / 64);
+            __syncthreads();
+            store_logits<Few>(g, part, e0, logit);
+        }
+    } else {
+        for (int i = threadIdx.x; i < g.T * g.E; i += kThreads) {
+            float s = 0.f;
+            for (int p = 0; p < g.parts; ++p) s += g.logits[(int64_t)p * g.T * g.E + i];
+            logit[i] = s;
+        }
+    }
+    for (int i = threadIdx.x; i < g.T * g.k; i += kThreads) c.index[i] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < g.T * g.E; i += kThreads) {
+        const int t = i / g.E, e = i % g.E;
+        const float *row = logit + t * g.E, l = row[e];
+        const bool nan = l != l;
+        int rank = 0;
+        for (int o = 0; o < g.E; ++o) {
+            const float q = row[o];
+            const bool better = q > l || (q != q && !nan), same = q == l || (q != q && nan);
+            rank += better || (same && o < e) ? 1 : 0;
+        }
+        if (rank < g.k && l != -__builtin_inff()) c.index[t * g.k + rank] = (int16_t)e;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x < kTok * 16) {
+        const int t = threadIdx.x >> 4, j0 = threadIdx.x & 15;
+        if (t < g.T) {
+            const float *row = logit + t * g.E;
+            const int first = c.index[t * g.k];
+            const float m = first >= 0 ? row[first] : 0.f;
+            float den = 0.f;
+            if (g.renorm) {
+                for (int j = j0; j < g.k; j += 16) {
+                    const int e = c.index[t * g.k + j];
+                    if (e >= 0) den += __expf(row[e] - m);
                 }
+            } else {
+                for (int e = j0; e < g.E; e += 16) den += __expf(row[e] - m);
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) den += __shfl_xor(den, d);
+            for (int j = j0; j < g.k; j += 16) {
+                const int e = c.index[t * g.k + j];
+                g.index[t * g.k + j] = e;
+                g.weight[t * g.k + j] = e >= 0 ? __expf(row[e] - m) / den : 0.f;
             }
         }
-        __syncthreads();   // the last unit's sums have been read
-        part[0][wave][lane] = halves(acc[0][0], acc[0][1]);
-        part[1][wave][lane] = halves(acc[1][0], acc[1][1]);
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// h: Q times 8 gate rows and their up rows of one chosen expert a unit; the waves split the columns, Span of them each, and hold
+// their tokens' values there over all units. A unit's weights are loaded before the sums of the last one are joined.
+// Wide: more columns than the waves hold, taken in several spans whose tokens' values are loaded for every unit.
+// ------------------------------------------------------------------------------------------
+template <int Form, bool Few, int Span, int Q, bool Wide>
+__global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
+    using L = Line<Form>;
+    constexpr int LN = Span > L::kValues ? Span / L::kValues : 1, N = Tokens<Few>::kN;   // lines a wave
+    __shared__ Chosen chosen;
+    __shared__ Part part[2][2 * Q];
+    __shared__ float logit[kMostLogits];
+    if (g.route == kRouted) read_index(g, chosen);
+    else route<Few>(g, chosen, part[0][0], logit);
+    __syncthreads();
+    choose(g, chosen);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = Tokens<Few>::token();
+    const __amdgpu_buffer_rsrc_t x = make_rsrc(g.x, (uint32_t)(g.T * g.dim) * 2u);
+    const uint32_t row = token < g.T ? (uint32_t)(token * g.dim) * 2u : kPast;
+    const int tiles = (g.hidden + 8 * Q - 1) / (8 * Q), units = chosen.count * tiles;
+    const int spans = (g.dim + LN * kWaves * L::kValues - 1) / (LN * kWaves * L::kValues);
+    bf16x8 v[LN][L::kP][N];
+    Held w[LN][Q][2];
+    // lines of span z: neighbouring ones for neighbouring waves
+    auto load_x = [&](int z) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LN; ++i)
+#pragma unroll
+            for (int p = 0; p < L::kP; ++p)
+#pragma unroll
+                for (int n = 0; n < N; ++n) v[i][p][n] = load_tokens<Form, Few>(x, row, g.dim, (z * LN + i) * kWaves + wave, p, n);
+    };
+    auto load_w = [&](int u, int z) __attribute__((always_inline)) {
+        const int a = u / tiles, n0 = u % tiles * 8 * Q;
+        const Matrix<Form> m(g.up, g.up_scales, __builtin_amdgcn_readfirstlane(chosen.expert[a]), 2 * g.hidden, g.dim);
+#pragma unroll
+        for (int i = 0; i < LN; ++i)
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {   // (a unit's last rows may lie past the gate's: they are not stored)
+                w[i][q][0] = load_line<Form>(m, n0 + 8 * q, (z * LN + i) * kWaves + wave);
+                w[i][q][1] = load_line<Form>(m, g.hidden + n0 + 8 * q, (z * LN + i) * kWaves + wave);
+            }
+    };
+    if ((int)blockIdx.x >= units) return;
+    load_w(blockIdx.x, 0);
+    load_x(0);
+    int turn = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, turn ^= 1) {
+        Sums<Few> acc[Q][2];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) acc[q][0].clear(), acc[q][1].clear();
+        for (int z = 0;;) {
+#pragma unroll
+            for (int i = 0; i < LN; ++i)
+#pragma unroll
+                for (int p = 0; p < L::kP; ++p)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) acc[q][c].add(expand<Form>(w[i][q][c], p), v[i][p]);
+            if (!Wide || ++z == spans) break;
+            load_w(u, z);
+            load_x(z);
+        }
+        if (u + (int)gridDim.x < units) {
+            load_w(u + gridDim.x, 0);
+            if (Wide) load_x(0);
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) part[turn][2 * q + c][wave][lane] = acc[q][c].all();
         __syncthreads();
-        const int t = threadIdx.x >> 3, i = threadIdx.x & 7;
-        if (t < g.T) {
-            const int j = chosen.slot[a][t];
-            if (j != kNone) {
-                float gv = joined(part[0], i, t), uv = joined(part[1], i, t);
+        const int a = u / tiles, e = chosen.expert[a];
+        // groups 2 j and 2 j + 1, neighbours in a wave, join gate and up
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (threadIdx.x >= 2 * Group<Few>::kCount * 16) break;
+            const Group<Few> j(threadIdx.x >> 5);
+            const float mine = pick(j.join(part[turn][2 * q + (threadIdx.x >> 4 & 1)])), other = __shfl_xor(mine, 16);
+            const int n = u % tiles * 8 * Q + 8 * q + 4 * j.quad + (threadIdx.x & 3);
+            const int slot = j.token < g.T ? chosen.slot[a][j.token] : kNone;
+            if ((threadIdx.x & 31) < 4 && slot != kNone && n < g.hidden) {
+                float gv = mine, uv = other;
                 if (g.up_bias) {
-                    const uint16_t *b = g.up_bias + (int64_t)e * 2 * g.hidden + n0 + i;
+                    const uint16_t *b = g.up_bias + (int64_t)e * 2 * g.hidden + n;
                     gv += from_bf16(b[0]);
                     uv += from_bf16(b[g.hidden]);
                 }
-                g.h[(int64_t)(t * g.k + j) * g.hidden + n0 + i] = to_bf16(gv / (1.f + __expf(-gv)) * uv);
+                g.h[(int64_t)(j.token * g.k + slot) * g.hidden + n] = to_bf16(gv / (1.f + __expf(-gv)) * uv);
             }
         }
     }
 }
 
 // ------------------------------------------------------------------------------------------
-// out: 16 columns a work-group, over all chosen experts; the waves split the hidden columns.
+// out: 8 RS columns a work-group, over all chosen experts; the waves split the hidden columns, a line of each expert in turn.
 // ------------------------------------------------------------------------------------------
-template <int Form>
-__global__ __launch_bounds__(kWaves * 64) void k_ffn_down(FfnArgs g) {
+template <int Form, bool Few, int RS>
+__global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
     using L = Line<Form>;
+    constexpr int N = Tokens<Few>::kN;
     __shared__ Chosen chosen;
-    __shared__ f32x4 part[2][kWaves][64];
+    __shared__ Part part[RS];
+    read_index(g, chosen);
+    __syncthreads();
     choose(g, chosen);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = lane & 15;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = Tokens<Few>::token();
     const __amdgpu_buffer_rsrc_t h = make_rsrc(g.h, (uint32_t)(g.T * g.k) * (uint32_t)g.hidden * 2u);
-    const int n0 = blockIdx.x * 16, steps = (g.hidden + L::kValues - 1) / L::kValues;
-    f32x4 sum[2] = {};
-    for (int a = 0; a < chosen.count; ++a) {
+    const int n0 = blockIdx.x * 8 * RS, steps = (g.hidden + L::kValues - 1) / L::kValues, count = chosen.count;
+
+    struct Stage {
+        Held w[RS];
+        bf16x8 v[L::kP][N];
+    };
+    auto load = [&](Stage &st, int a, int s) __attribute__((always_inline)) {
         const Matrix<Form> m(g.down, g.down_scales, __builtin_amdgcn_readfirstlane(chosen.expert[a]), g.dim, g.hidden);
         const int j = chosen.slot[a][token];
         const uint32_t row = j != kNone ? (uint32_t)(token * g.k + j) * (uint32_t)g.hidden * 2u : kPast;
-        f32x4 acc[2][2] = {};   // [rows 0 .. 7, 8 .. 15][even, odd]
-        for (int s = (wave + kWaves - a * steps % kWaves) % kWaves; s < steps; s += kWaves) {
-            const Held lo = load_line<Form>(m, n0, s), hi = load_line<Form>(m, n0 + 8, s);
 #pragma unroll
-            for (int p = 0; p < L::kP; ++p) {
-                const bf16x8 wl = expand<Form>(lo, p), wh = expand<Form>(hi, p);
+        for (int i = 0; i < RS; ++i) st.w[i] = load_line<Form>(m, n0 + 8 * i, s);
 #pragma unroll
-                for (int odd = 0; odd < 2; ++odd) {
-                    const bf16x8 v = load_tokens<Form>(h, row, g.hidden, s, p, odd);
-                    acc[0][odd] = mfma16(wl, v, acc[0][odd]);
-                    acc[1][odd] = mfma16(wh, v, acc[1][odd]);
-                }
-            }
+        for (int p = 0; p < L::kP; ++p)
+#pragma unroll
+            for (int n = 0; n < N; ++n) st.v[p][n] = load_tokens<Form, Few>(h, row, g.hidden, s, p, n);
+    };
+    f32x4 sum[RS] = {};
+    Sums<Few> acc[RS];
+#pragma unroll
+    for (int i = 0; i < RS; ++i) acc[i].clear();
+    // expert a's sums, weighted, into the tokens that chose it (others' are dropped: infinite weights times no value)
+    auto close = [&](int a) __attribute__((always_inline)) {
+        const int j = chosen.slot[a][token];
+        const float w = j != kNone ? g.weight[token * g.k + j] : 0.f;
+#pragma unroll
+        for (int i = 0; i < RS; ++i) {
+            const f32x4 v = acc[i].all();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[i][q] = j != kNone ? fmaf(w, v[q], sum[i][q]) : sum[i][q];
+            acc[i].clear();
         }
-        if (j != kNone) {
-            const float w = g.weight[token * g.k + j];
+    };
+    int a = 0, s = wave;
+    auto norm = [&](int &aa, int &ss) __attribute__((always_inline)) {
+        while (ss >= steps) ss -= steps, ++aa;
+    };
+    norm(a, s);
+    if (a < count) {
+        Stage cur;
+        load(cur, a, s);
+        for (;;) {
+            int an = a, sn = s + kWaves;
+            norm(an, sn);
+            Stage nxt;
+            const bool more = an < count;
+            if (more) load(nxt, an, sn);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const f32x4 v = halves(acc[i][0], acc[i][1]);
+            for (int p = 0; p < L::kP; ++p)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) sum[i][q] = fmaf(w, v[q], sum[i][q]);
-            }
+                for (int i = 0; i < RS; ++i) acc[i].add(expand<Form>(cur.w[i], p), cur.v[p]);
+            if (an != a) close(a);
+            if (!more) break;
+            cur = nxt;
+            a = an;
+            s = sn;
         }
     }
-    part[0][wave][lane] = sum[0];
-    part[1][wave][lane] = sum[1];
+#pragma unroll
+    for (int i = 0; i < RS; ++i) part[i][wave][lane] = sum[i];
     __syncthreads();
-    const int t = threadIdx.x >> 4, i = threadIdx.x & 15, n = n0 + i;
-    if (t < g.T && n < g.dim) {
-        float v = joined(part[i >> 3], i & 7, t);
+    if (threadIdx.x >= RS * Group<Few>::kCount * 16) return;
+    const Group<Few> j((threadIdx.x >> 4) % Group<Few>::kCount);
+    const int set = (threadIdx.x >> 4) / Group<Few>::kCount, t = j.token, n = n0 + 8 * set + 4 * j.quad + (threadIdx.x & 3);
+    float v = pick(j.join(part[set]));
+    if ((threadIdx.x & 15) < 4 && t < g.T && n < g.dim) {
         if (g.down_bias)
-            for (int j = 0; j < g.k; ++j) {
-                const int e = g.index[t * g.k + j];
-                if ((unsigned)e < (unsigned)g.E) v = fmaf(g.weight[t * g.k + j], from_bf16(g.down_bias[(int64_t)e * g.dim + n]), v);
+            for (int i = 0; i < g.k; ++i) {
+                const int e = chosen.index[t * g.k + i];
+                if (e >= 0) v = fmaf(g.weight[t * g.k + i], from_bf16(g.down_bias[(int64_t)e * g.dim + n]), v);
             }
         g.out[(int64_t)t * g.dim + n] = to_bf16(v);
     }
@@ -306,34 +512,65 @@ int32_t launched(const char *what) {
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
+// Who finds the experts of a call.
+Route route_of(int T, int E, int64_t dim) {
+    if ((int64_t)T * E > kMostLogits || (int64_t)T * E * E > kMostRanks) return kRouted;
+    return E * dim <= 32768 ? kAllInOne : kFromLogits;
+}
+
+// Pieces of the logits' sums: 8 lines each, half a line a wave.
+int parts_of(Route r, int dim) { return r == kFromLogits ? std::min(8, (dim + 511) / 512) : 1; }
+
+template <int Form, bool Few>
+void launch_products(const FfnArgs &g, hipStream_t st) {
+    const int64_t most = std::min(g.E, g.T * g.k);
+    auto up = [&](auto kernel, int columns) {
+        const int64_t units = most * ((g.hidden + columns - 1) / columns);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(units, kCUs)), dim3(kThreads), 0, st, g);
+    };
+    if (g.dim > 256 * kWaves) up(k_ffn_up<Form, Few, 128, 1, true>, 8);
+    else if (g.dim <= 128 * kWaves && most * (g.hidden / 16) >= kCUs) up(k_ffn_up<Form, Few, 128, 2, false>, 16);
+    else up(k_ffn_up<Form, Few, 256, 1, false>, 8);
+    if (g.dim >= 16 * kCUs)
+        hipLaunchKernelGGL((k_ffn_down<Form, Few, 2>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kThreads), 0, st, g);
+    else
+        hipLaunchKernelGGL((k_ffn_down<Form, Few, 1>), dim3((unsigned)(g.dim / 8)), dim3(kThreads), 0, st, g);
+}
+
 template <int Form>
 void launch_products(const FfnArgs &g, hipStream_t st) {
-    const int64_t units = (int64_t)std::min(g.E, g.T * g.k) * (g.hidden / 8);
-    hipLaunchKernelGGL((k_ffn_up<Form>), dim3((unsigned)std::min<int64_t>(units, 2 * kCUs)), dim3(kWaves * 64), 0, st, g);
-    hipLaunchKernelGGL((k_ffn_down<Form>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kWaves * 64), 0, st, g);
+    if (g.T <= 8) launch_products<Form, true>(g, st);
+    else launch_products<Form, false>(g, st);
 }
 
 }  // namespace
 
-size_t expert_ffn_workspace_bytes(int T, int hidden, int E, int k) {
-    return up16((size_t)T * E * 4) + 2 * up16((size_t)T * k * 4) + (size_t)T * k * hidden * 2;
+size_t expert_ffn_workspace_bytes(int T, int dim, int hidden, int E, int k) {
+    return up16((size_t)parts_of(route_of(T, E, dim), dim) * T * E * 4) + 2 * up16((size_t)T * k * 4) + (size_t)T * k * hidden * 2;
 }
 
 int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,
                           int form, const void *up, const uint8_t *up_scales, const void *down, const uint8_t *down_scales,
                           const uint16_t *up_bias, const uint16_t *down_bias, uint16_t *out, void *workspace, void *stream) {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    FfnArgs g{x, T, dim, hidden, E, k, router, up, down, up_scales, down_scales, up_bias, down_bias, out, nullptr, nullptr, nullptr, nullptr};
+    const Route r = route_of(T, E, dim);
+    FfnArgs g{x, T, dim, hidden, E, k, renorm, r, parts_of(r, dim), router, up, down, up_scales, down_scales, up_bias, down_bias, out,
+              nullptr, nullptr, nullptr, nullptr};
     g.logits = reinterpret_cast<float *>(ws);
-    ws += up16((size_t)T * E * 4);
+    ws += up16((size_t)g.parts * T * E * 4);
     g.index = reinterpret_cast<int32_t *>(ws);
     ws += up16((size_t)T * k * 4);
     g.weight = reinterpret_cast<float *>(ws);
     ws += up16((size_t)T * k * 4);
     g.h = reinterpret_cast<uint16_t *>(ws);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    hipLaunchKernelGGL(k_ffn_logits, dim3((unsigned)E), dim3(256), 0, st, g);
-    if (const int32_t bad = launch_router_fwd(g.logits, BSR_LOGITS_F32, T, E, k, renorm, g.index, g.weight, stream)) return bad;
+    if (r != kAllInOne) {
+        const dim3 grid((unsigned)((E + 7) / 8), (unsigned)g.parts);
+        if (T <= 8) hipLaunchKernelGGL(k_ffn_logits<true>, grid, dim3(kThreads), 0, st, g);
+        else hipLaunchKernelGGL(k_ffn_logits<false>, grid, dim3(kThreads), 0, st, g);
+    }
+    if (r == kRouted)
+        if (const int32_t bad = launch_router_fwd(g.logits, BSR_LOGITS_F32, T, E, k, renorm, g.index, g.weight, stream)) return bad;
     if (form == BSR_WEIGHTS_BF16) launch_products<BSR_WEIGHTS_BF16>(g, st);
     else if (form == BSR_WEIGHTS_MX4) launch_products<BSR_WEIGHTS_MX4>(g, st);
     else launch_products<BSR_WEIGHTS_FP8>(g, st);

@@ -356,7 +356,7 @@ static int32_t check_ffn(int32_t T, int32_t dim, int32_t hidden, int32_t E, int3
 
 size_t bsr_expert_ffn_workspace(int32_t T, int32_t dim, int32_t hidden, int32_t E, int32_t k) {
     try {
-        return check_ffn(T, dim, hidden, E, k) == BSR_OK ? expert_ffn_workspace_bytes(T, hidden, E, k) : 0;
+        return check_ffn(T, dim, hidden, E, k) == BSR_OK ? expert_ffn_workspace_bytes(T, dim, hidden, E, k) : 0;
     } catch (...) {
         return 0;
     }
@@ -377,7 +377,7 @@ int32_t bsr_expert_ffn(const bsr_bf16 *x, int32_t T, int32_t dim, int32_t hidden
     if ((uint64_t)2 * hidden * dim * bits / 8 > kMaxOperandBytes)
         return fail(BSR_ERR_INVALID_ARG, "one expert's weight has more than 0xF0000000 bytes");
     const bool none = T == 0, bare = form == BSR_WEIGHTS_BF16;
-    const size_t need = expert_ffn_workspace_bytes(T, hidden, E, k);
+    const size_t need = expert_ffn_workspace_bytes(T, dim, hidden, E, k);
     BSR_CHECK(check_ptrs({{x, "x", none, 16}, {router, "router", none, 16}, {up, "up", none, 16},
                           {up_scales, "up_scales", none || bare, 16}, {down, "down", none, 16},
                           {down_scales, "down_scales", none || bare, 16}, {up_bias, "up_bias", true, 16},

@@ -138,7 +138,7 @@ int32_t launch_expert_fwd_fp8(const ExpertShape &s, const uint16_t *X, const uin
 int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, const uint8_t *xscales, const uint8_t *codes,
                                   const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream);
 
-size_t expert_ffn_workspace_bytes(int T, int hidden, int E, int k);
+size_t expert_ffn_workspace_bytes(int T, int dim, int hidden, int E, int k);
 int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,
                           int form, const void *up, const uint8_t *up_scales, const void *down, const uint8_t *down_scales,
                           const uint16_t *up_bias, const uint16_t *down_bias, uint16_t *out, void *workspace, void *stream);
