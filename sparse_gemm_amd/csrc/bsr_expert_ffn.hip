@@ -44,6 +44,7 @@ struct FfnArgs {
 // Who finds the experts: the work-groups of the up product, each for itself, from x and the router or from logits that a
 // launch before has summed in pieces; or the router's kernel.
 enum Route { kAllInOne, kFromLogits, kRouted };
+constexpr int kMostInOne = 64;   // experts of kAllInOne
 
 // ------------------------------------------------------------------------------------------
 // Lines of weights
@@ -77,12 +78,14 @@ struct Held {
     uint32_t byte;
 };
 
-// Line s of the rows n0 .. n0 + 7 (n0 a multiple of 8); zeros outside of the matrix.
+// Line s of the rows n0 .. n0 + 7 (n0 a multiple of 8); zeros outside of the matrix, and where it is not live. Loads that are not
+// wanted are issued too, at an offset past the end: behind a branch the compiler could not count the loads in flight, and would
+// wait for all of them before it uses the oldest.
 template <int Form>
-__device__ __forceinline__ Held load_line(const Matrix<Form> &m, int n0, int s) {
+__device__ __forceinline__ Held load_line(const Matrix<Form> &m, int n0, int s, bool live = true) {
     const int lane = threadIdx.x & 63, r = lane & 7, chunk = 2 * (lane >> 4) + (lane >> 3 & 1);
     const uint32_t at = (uint32_t)s * 128u + (uint32_t)chunk * 16u;
-    const bool in = at < m.pitch && n0 < m.rows;
+    const bool in = live && at < m.pitch && n0 < m.rows;
     Held v;
     v.codes = __builtin_bit_cast(u32x4, buf_load16(m.codes, in ? (uint32_t)(n0 + r) * m.pitch + at : kPast, 0));
     v.byte = 0;
@@ -131,7 +134,15 @@ struct Sums {
         for (int i = 0; i < Tokens<Few>::kN; ++i) v[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[i], v[i], 0, 0, 0);
     }
     __device__ __forceinline__ f32x4 all() const {
-        const f32x4 even = v[0], odd = v[Tokens<Few>::kN - 1];   // values: a choice between their places would put both into memory
+        // The wait states between a matrix instruction and a read of its result. The compiler counts them, but hipcc 7.2 left them out
+        // where the instruction ends a loop and an LDS write of its result follows the loop: the old sums were written.
+        f32x4 even = v[0];
+        if constexpr (Few) {
+            asm volatile("s_nop 15" : "+v"(even));
+            return even;
+        }
+        f32x4 odd = v[Tokens<Few>::kN - 1];   // (a choice between the places of the two would put both into memory)
+        asm volatile("s_nop 15" : "+v"(even), "+v"(odd));
         const bool upper = threadIdx.x & 32;
         return f32x4{upper ? odd[0] : even[0], upper ? odd[1] : even[1], upper ? odd[2] : even[2], upper ? odd[3] : even[3]};
     }
@@ -228,39 +239,51 @@ __device__ __forceinline__ int place_of(const Chosen &c, int e) {   // chosen ex
     return n;
 }
 
-// From c.index.
-__device__ __forceinline__ void choose(const FfnArgs &g, Chosen &c) {
-    const int slots = g.T * g.k, words = (g.E + 31) / 32, i = threadIdx.x;   // slots <= 512 threads
-    if (i < words) c.bits[i] = 0;
-    __syncthreads();
-    const int e = i < slots ? c.index[i] : -1;
-    if (e >= 0) atomicOr(&c.bits[e >> 5], 1u << (e & 31));
-    __syncthreads();
-    int n = 0;
-    for (int w = 0; w < words; ++w) n += __popc(c.bits[w]);
-    if (i == 0) c.count = n;
-    for (int j = i; j < n * (kTok / 4); j += kThreads) reinterpret_cast<uint32_t *>(c.slot)[j] = ~0u;
-    __syncthreads();
+// Before anything is chosen; the caller's next barrier publishes it.
+__device__ __forceinline__ void clear(const FfnArgs &g, Chosen &c) {
+    const int slots = g.T * g.k, i = threadIdx.x;   // slots <= 512 threads
+    if (i < (g.E + 31) / 32) c.bits[i] = 0;
+    if (i < slots) c.index[i] = -1;
+    for (int j = i; j < slots * (kTok / 4); j += kThreads) reinterpret_cast<uint32_t *>(c.slot)[j] = ~0u;
+}
+
+__device__ __forceinline__ void choose(Chosen &c, int i, int e) {
+    c.index[i] = (int16_t)e;
+    atomicOr(&c.bits[e >> 5], 1u << (e & 31));
+}
+
+// After a barrier behind the last choose(): the list; the caller's next barrier publishes it.
+__device__ __forceinline__ void list(const FfnArgs &g, Chosen &c) {
+    const int words = (g.E + 31) / 32, i = threadIdx.x;
+    const int e = i < g.T * g.k ? c.index[i] : -1;
+    if (i == 0) {
+        int n = 0;
+        for (int w = 0; w < words; ++w) n += __popc(c.bits[w]);
+        c.count = n;
+    }
     if (e >= 0) {
         const int a = place_of(c, e);
         c.expert[a] = (uint16_t)e;   // the same value from every slot
         c.slot[a][i / g.k] = (uint8_t)(i % g.k);
     }
-    __syncthreads();
 }
 
-__device__ __forceinline__ void read_index(const FfnArgs &g, Chosen &c) {
-    const int i = threadIdx.x;
-    if (i < g.T * g.k) {
-        const int e = g.index[i];
-        c.index[i] = (unsigned)e < (unsigned)g.E ? (int16_t)e : (int16_t)-1;
-    }
+// Largest of the wave's v.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, true));   // row rotations by 8, 4, 2, 1
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, true));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, true));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, true));
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return max(max(a, b), max(c, d));
 }
 
-// Router in the work-group: logits, ranks of all experts of a token by counting the better ones (ties to the lowest; NaN is
-// better than all; -infinity is never chosen), as bsr_router_fwd. One work-group writes index and weight for the down product.
-constexpr int kMostLogits = 4096;       // T * E of a work-group that routes
-constexpr int kMostRanks = 1 << 17;     // T * E * E: 128 comparisons a thread
+// Router in the work-group: a wave takes a token, lane l its experts l, 64 + l, ...; k rounds of the largest logit, ties to the lowest
+// expert (NaN is larger than all, -infinity is never chosen), as bsr_router_fwd. One work-group writes index and weight for the
+// down product. (Ranks by counting the better experts of each, 64 comparisons a thread at 16 tokens and 64 experts: 4 us more.)
+constexpr int kMostHere = 256;   // experts of a work-group that routes
+constexpr int kRounds = kMostHere / 64;
 
 template <bool Few>
 __device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, float *logit) {
@@ -272,77 +295,112 @@ __device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, f
             __syncthreads();
             store_logits<Few>(g, part, e0, logit);
         }
-    } else {
-        for (int i = threadIdx.x; i < g.T * g.E; i += kThreads) {
-            float s = 0.f;
-            for (int p = 0; p < g.parts; ++p) s += g.logits[(int64_t)p * g.T * g.E + i];
-            logit[i] = s;
-        }
-    }
-    for (int i = threadIdx.x; i < g.T * g.k; i += kThreads) c.index[i] = -1;
-    __syncthreads();
-    for (int i = threadIdx.x; i < g.T * g.E; i += kThreads) {
-        const int t = i / g.E, e = i % g.E;
-        const float *row = logit + t * g.E, l = row[e];
-        const bool nan = l != l;
-        int rank = 0;
-        for (int o = 0; o < g.E; ++o) {
-            const float q = row[o];
-            const bool better = q > l || (q != q && !nan), same = q == l || (q != q && nan);
-            rank += better || (same && o < e) ? 1 : 0;
-        }
-        if (rank < g.k && l != -__builtin_inff()) c.index[t * g.k + rank] = (int16_t)e;
     }
     __syncthreads();
-    if (blockIdx.x == 0 && threadIdx.x < kTok * 16) {
-        const int t = threadIdx.x >> 4, j0 = threadIdx.x & 15;
-        if (t < g.T) {
-            const float *row = logit + t * g.E;
-            const int first = c.index[t * g.k];
-            const float m = first >= 0 ? row[first] : 0.f;
-            float den = 0.f;
-            if (g.renorm) {
-                for (int j = j0; j < g.k; j += 16) {
-                    const int e = c.index[t * g.k + j];
-                    if (e >= 0) den += __expf(row[e] - m);
-                }
-            } else {
-                for (int e = j0; e < g.E; e += 16) den += __expf(row[e] - m);
-            }
+    const int t = wave;   // kTok <= kWaves
+    if (t >= g.T) return;
+    float l[kRounds];
+    uint32_t key[kRounds];
+    int slot[kRounds];
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) den += __shfl_xor(den, d);
-            for (int j = j0; j < g.k; j += 16) {
-                const int e = c.index[t * g.k + j];
-                g.index[t * g.k + j] = e;
-                g.weight[t * g.k + j] = e >= 0 ? __expf(row[e] - m) / den : 0.f;
+    for (int r = 0; r < kRounds; ++r) {
+        const int e = 64 * r + lane;
+        l[r] = -__builtin_inff();
+        if (e < g.E) {
+            if (g.route == kAllInOne) {
+                l[r] = logit[t * g.E + e];
+            } else {
+                l[r] = 0.f;
+                for (int p = 0; p < g.parts; ++p) l[r] += g.logits[((int64_t)p * g.T + t) * g.E + e];
             }
         }
+        const uint32_t bits = __float_as_uint(l[r] + 0.f);   // -0 is 0
+        key[r] = bits ^ ((int)bits < 0 ? 0xFFFFFFFFu : 0x80000000u);   // in the order of the values
+        if (l[r] != l[r]) key[r] = 0xFFFFFFFFu;
+        if (l[r] == -__builtin_inff()) key[r] = 0;
+        slot[r] = -1;
+    }
+    int found = 0;
+    float top = 0.f;
+    for (; found < g.k; ++found) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int r = 1; r < kRounds; ++r) m = max(m, key[r]);
+        m = wave_max(m);
+        if (m == 0) break;
+        bool done = false;
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const uint64_t at = __ballot(key[r] == m);
+            if (!done && at) {
+                done = true;
+                const int who = __builtin_ctzll(at);
+                if (found == 0) top = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(l[r]), who));
+                if (lane == who) key[r] = 0, slot[r] = found;
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+        if (slot[r] >= 0) choose(c, t * g.k + slot[r], 64 * r + lane);
+    if (blockIdx.x != 0) return;
+    float den = 0.f;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        if (64 * r + lane < g.E && (slot[r] >= 0 || !g.renorm)) den += __expf(l[r] - top);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) den += __shfl_xor(den, d);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+        if (slot[r] >= 0) {
+            g.index[t * g.k + slot[r]] = 64 * r + lane;
+            g.weight[t * g.k + slot[r]] = __expf(l[r] - top) / den;
+        }
+    if (lane >= found && lane < g.k) {
+        g.index[t * g.k + lane] = -1;
+        g.weight[t * g.k + lane] = 0.f;
     }
 }
 
 // ------------------------------------------------------------------------------------------
 // h: Q times 8 gate rows and their up rows of one chosen expert a unit; the waves split the columns, Span of them each, and hold
-// their tokens' values there over all units. A unit's weights are loaded before the sums of the last one are joined.
+// their tokens' values there over all units. Weights are loaded D units ahead.
 // Wide: more columns than the waves hold, taken in several spans whose tokens' values are loaded for every unit.
 // ------------------------------------------------------------------------------------------
-template <int Form, bool Few, int Span, int Q, bool Wide>
+template <int Form, bool Few, int Span, int Q, int D, bool Wide>
 __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
     using L = Line<Form>;
     constexpr int LN = Span > L::kValues ? Span / L::kValues : 1, N = Tokens<Few>::kN;   // lines a wave
     __shared__ Chosen chosen;
     __shared__ Part part[2][2 * Q];
-    __shared__ float logit[kMostLogits];
-    if (g.route == kRouted) read_index(g, chosen);
-    else route<Few>(g, chosen, part[0][0], logit);
+    __shared__ float logit[kTok * kMostInOne];
+    clear(g, chosen);
+    if (g.route == kRouted) {
+        __syncthreads();
+        const int i = threadIdx.x, e = i < g.T * g.k ? g.index[i] : -1;
+        if ((unsigned)e < (unsigned)g.E) choose(chosen, i, e);
+        __syncthreads();
+    } else {
+        route<Few>(g, chosen, part[0][0], logit);
+        __syncthreads();
+    }
+    list(g, chosen);
     __syncthreads();
-    choose(g, chosen);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = Tokens<Few>::token();
     const __amdgpu_buffer_rsrc_t x = make_rsrc(g.x, (uint32_t)(g.T * g.dim) * 2u);
     const uint32_t row = token < g.T ? (uint32_t)(token * g.dim) * 2u : kPast;
-    const int tiles = (g.hidden + 8 * Q - 1) / (8 * Q), units = chosen.count * tiles;
+    const int tiles = (g.hidden + 8 * Q - 1) / (8 * Q), units = __builtin_amdgcn_readfirstlane(chosen.count) * tiles;
     const int spans = (g.dim + LN * kWaves * L::kValues - 1) / (LN * kWaves * L::kValues);
     bf16x8 v[LN][L::kP][N];
-    Held w[LN][Q][2];
+    struct Unit {
+        Held w[LN][Q][2];
+        uint32_t bias[Q];   // of the row that this thread joins
+    };
+    // groups 2 j and 2 j + 1, neighbours in a wave, join gate and up
+    const Group<Few> group(threadIdx.x >> 5);
+    const bool gate = !(threadIdx.x & 16), joins = threadIdx.x < 2 * Group<Few>::kCount * 16;
+    const int at = 4 * group.quad + (threadIdx.x & 3);
     // lines of span z: neighbouring ones for neighbouring waves
     auto load_x = [&](int z) __attribute__((always_inline)) {
 #pragma unroll
@@ -352,65 +410,75 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
 #pragma unroll
                 for (int n = 0; n < N; ++n) v[i][p][n] = load_tokens<Form, Few>(x, row, g.dim, (z * LN + i) * kWaves + wave, p, n);
     };
-    auto load_w = [&](int u, int z) __attribute__((always_inline)) {
-        const int a = u / tiles, n0 = u % tiles * 8 * Q;
-        const Matrix<Form> m(g.up, g.up_scales, __builtin_amdgcn_readfirstlane(chosen.expert[a]), 2 * g.hidden, g.dim);
+    auto load_w = [&](Unit &to, int u, int z) __attribute__((always_inline)) {
+        const bool live = u < units;
+        const int a = live ? u / tiles : 0, n0 = live ? u % tiles * 8 * Q : 0, e = __builtin_amdgcn_readfirstlane(chosen.expert[a]);
+        const Matrix<Form> m(g.up, g.up_scales, live ? e : 0, 2 * g.hidden, g.dim);
+        const __amdgpu_buffer_rsrc_t b = make_rsrc(g.up_bias + (int64_t)(live ? e : 0) * 2 * g.hidden, g.up_bias ? (uint32_t)g.hidden * 4u : 0u);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (z == 0) to.bias[q] = __builtin_amdgcn_raw_buffer_load_b16(b, (uint32_t)(n0 + 8 * q + at + (gate ? 0 : g.hidden)) * 2u, 0, 0);
+#pragma unroll
+            for (int i = 0; i < LN; ++i) {   // (a unit's last rows may lie past the gate's: they are not stored)
+                to.w[i][q][0] = load_line<Form>(m, n0 + 8 * q, (z * LN + i) * kWaves + wave, live);
+                to.w[i][q][1] = load_line<Form>(m, g.hidden + n0 + 8 * q, (z * LN + i) * kWaves + wave, live);
+            }
+        }
+    };
+    Sums<Few> acc[Q][2];
+    auto products = [&](const Unit &of) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < LN; ++i)
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {   // (a unit's last rows may lie past the gate's: they are not stored)
-                w[i][q][0] = load_line<Form>(m, n0 + 8 * q, (z * LN + i) * kWaves + wave);
-                w[i][q][1] = load_line<Form>(m, g.hidden + n0 + 8 * q, (z * LN + i) * kWaves + wave);
-            }
+            for (int p = 0; p < L::kP; ++p)
+#pragma unroll
+                for (int q = 0; q < Q; ++q)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) acc[q][c].add(expand<Form>(of.w[i][q][c], p), v[i][p]);
     };
-    if ((int)blockIdx.x >= units) return;
-    load_w(blockIdx.x, 0);
+    int u = blockIdx.x, turn = 0;
+    const int stride = gridDim.x;
+    Unit unit[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_w(unit[d], u + d * stride, 0);
     load_x(0);
-    int turn = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, turn ^= 1) {
-        Sums<Few> acc[Q][2];
+    while (u < units) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) acc[q][0].clear(), acc[q][1].clear();
-        for (int z = 0;;) {
+        for (int d = 0; d < D; ++d) {
+            if (u >= units) break;
 #pragma unroll
-            for (int i = 0; i < LN; ++i)
-#pragma unroll
-                for (int p = 0; p < L::kP; ++p)
-#pragma unroll
-                    for (int q = 0; q < Q; ++q)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) acc[q][c].add(expand<Form>(w[i][q][c], p), v[i][p]);
-            if (!Wide || ++z == spans) break;
-            load_w(u, z);
-            load_x(z);
-        }
-        if (u + (int)gridDim.x < units) {
-            load_w(u + gridDim.x, 0);
-            if (Wide) load_x(0);
-        }
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) part[turn][2 * q + c][wave][lane] = acc[q][c].all();
-        __syncthreads();
-        const int a = u / tiles, e = chosen.expert[a];
-        // groups 2 j and 2 j + 1, neighbours in a wave, join gate and up
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            if (threadIdx.x >= 2 * Group<Few>::kCount * 16) break;
-            const Group<Few> j(threadIdx.x >> 5);
-            const float mine = pick(j.join(part[turn][2 * q + (threadIdx.x >> 4 & 1)])), other = __shfl_xor(mine, 16);
-            const int n = u % tiles * 8 * Q + 8 * q + 4 * j.quad + (threadIdx.x & 3);
-            const int slot = j.token < g.T ? chosen.slot[a][j.token] : kNone;
-            if ((threadIdx.x & 31) < 4 && slot != kNone && n < g.hidden) {
-                float gv = mine, uv = other;
-                if (g.up_bias) {
-                    const uint16_t *b = g.up_bias + (int64_t)e * 2 * g.hidden + n;
-                    gv += from_bf16(b[0]);
-                    uv += from_bf16(b[g.hidden]);
+            for (int q = 0; q < Q; ++q) acc[q][0].clear(), acc[q][1].clear();
+            products(unit[d]);
+            if constexpr (Wide) {
+                for (int z = 1; z < spans; ++z) {
+                    load_w(unit[d], u, z);
+                    load_x(z);
+                    products(unit[d]);
                 }
-                g.h[(int64_t)(j.token * g.k + slot) * g.hidden + n] = to_bf16(gv / (1.f + __expf(-gv)) * uv);
+                load_x(0);
             }
+            uint32_t bias[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) bias[q] = unit[d].bias[q];
+            load_w(unit[d], u + D * stride, 0);
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) part[turn][2 * q + c][wave][lane] = acc[q][c].all();
+            __syncthreads();
+            if (joins) {
+                const int a = u / tiles, slot = group.token < g.T ? chosen.slot[a][group.token] : kNone;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const float mine = pick(group.join(part[turn][2 * q + !gate])) + from_bf16((uint16_t)bias[q]);
+                    const float other = __shfl_xor(mine, 16);
+                    const int n = u % tiles * 8 * Q + 8 * q + at;
+                    if ((threadIdx.x & 31) < 4 && slot != kNone && n < g.hidden)
+                        g.h[(int64_t)(group.token * g.k + slot) * g.hidden + n] = to_bf16(mine / (1.f + __expf(-mine)) * other);
+                }
+            }
+            u += stride;
+            turn ^= 1;
         }
     }
 }
@@ -418,73 +486,83 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
 // ------------------------------------------------------------------------------------------
 // out: 8 RS columns a work-group, over all chosen experts; the waves split the hidden columns, a line of each expert in turn.
 // ------------------------------------------------------------------------------------------
-template <int Form, bool Few, int RS>
+template <int Form, bool Few, int RS, int D>
 __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
     using L = Line<Form>;
     constexpr int N = Tokens<Few>::kN;
     __shared__ Chosen chosen;
     __shared__ Part part[RS];
-    read_index(g, chosen);
+    __shared__ float weight[kTok * kMaxSlots];
+    clear(g, chosen);
     __syncthreads();
-    choose(g, chosen);
+    if ((int)threadIdx.x < g.T * g.k) {
+        const int e = g.index[threadIdx.x];
+        weight[threadIdx.x] = g.weight[threadIdx.x];
+        if ((unsigned)e < (unsigned)g.E) choose(chosen, threadIdx.x, e);
+    }
+    __syncthreads();
+    list(g, chosen);
+    __syncthreads();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = Tokens<Few>::token();
     const __amdgpu_buffer_rsrc_t h = make_rsrc(g.h, (uint32_t)(g.T * g.k) * (uint32_t)g.hidden * 2u);
-    const int n0 = blockIdx.x * 8 * RS, steps = (g.hidden + L::kValues - 1) / L::kValues, count = chosen.count;
+    const int n0 = blockIdx.x * 8 * RS, steps = (g.hidden + L::kValues - 1) / L::kValues, count = __builtin_amdgcn_readfirstlane(chosen.count);
 
     struct Stage {
         Held w[RS];
         bf16x8 v[L::kP][N];
+        int a, slot;    // the expert's place, its slot of this lane's token or kNone
     };
-    auto load = [&](Stage &st, int a, int s) __attribute__((always_inline)) {
-        const Matrix<Form> m(g.down, g.down_scales, __builtin_amdgcn_readfirstlane(chosen.expert[a]), g.dim, g.hidden);
-        const int j = chosen.slot[a][token];
-        const uint32_t row = j != kNone ? (uint32_t)(token * g.k + j) * (uint32_t)g.hidden * 2u : kPast;
+    int a = 0, s = wave;   // of the next stage to load
+    while (s >= steps) s -= steps, ++a;
+    auto load = [&](Stage &st) __attribute__((always_inline)) {
+        st.a = a;
+        const bool live = a < count;
+        const int place = live ? a : 0, e = __builtin_amdgcn_readfirstlane(chosen.expert[place]);
+        const Matrix<Form> m(g.down, g.down_scales, live ? e : 0, g.dim, g.hidden);
+        st.slot = live ? chosen.slot[place][token] : kNone;
+        const int at = st.slot != kNone ? token * g.k + st.slot : 0;
+        const uint32_t row = st.slot != kNone ? (uint32_t)at * (uint32_t)g.hidden * 2u : kPast;
 #pragma unroll
-        for (int i = 0; i < RS; ++i) st.w[i] = load_line<Form>(m, n0 + 8 * i, s);
+        for (int i = 0; i < RS; ++i) st.w[i] = load_line<Form>(m, n0 + 8 * i, s, live);
 #pragma unroll
         for (int p = 0; p < L::kP; ++p)
 #pragma unroll
             for (int n = 0; n < N; ++n) st.v[p][n] = load_tokens<Form, Few>(h, row, g.hidden, s, p, n);
+        s += kWaves;
+        while (s >= steps) s -= steps, ++a;
     };
     f32x4 sum[RS] = {};
     Sums<Few> acc[RS];
 #pragma unroll
     for (int i = 0; i < RS; ++i) acc[i].clear();
-    // expert a's sums, weighted, into the tokens that chose it (others' are dropped: infinite weights times no value)
-    auto close = [&](int a) __attribute__((always_inline)) {
-        const int j = chosen.slot[a][token];
-        const float w = j != kNone ? g.weight[token * g.k + j] : 0.f;
+    Stage st[D];
 #pragma unroll
-        for (int i = 0; i < RS; ++i) {
-            const f32x4 v = acc[i].all();
+    for (int d = 0; d < D; ++d) load(st[d]);
+    for (bool more = true; more;) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) sum[i][q] = j != kNone ? fmaf(w, v[q], sum[i][q]) : sum[i][q];
-            acc[i].clear();
-        }
-    };
-    int a = 0, s = wave;
-    auto norm = [&](int &aa, int &ss) __attribute__((always_inline)) {
-        while (ss >= steps) ss -= steps, ++aa;
-    };
-    norm(a, s);
-    if (a < count) {
-        Stage cur;
-        load(cur, a, s);
-        for (;;) {
-            int an = a, sn = s + kWaves;
-            norm(an, sn);
-            Stage nxt;
-            const bool more = an < count;
-            if (more) load(nxt, an, sn);
+        for (int d = 0; d < D; ++d) {
+            if (st[d].a >= count) {
+                more = false;
+                break;
+            }
 #pragma unroll
             for (int p = 0; p < L::kP; ++p)
 #pragma unroll
-                for (int i = 0; i < RS; ++i) acc[i].add(expand<Form>(cur.w[i], p), cur.v[p]);
-            if (an != a) close(a);
-            if (!more) break;
-            cur = nxt;
-            a = an;
-            s = sn;
+                for (int i = 0; i < RS; ++i) acc[i].add(expand<Form>(st[d].w[i], p), st[d].v[p]);
+            // the expert's last line of this wave: its sums, weighted, go into the tokens that chose it (others' are dropped: infinite
+            // weights times no value)
+            if (st[(d + 1) % D].a != st[d].a || D == 1) {
+                const bool mine = st[d].slot != kNone;
+                const float by = weight[mine ? token * g.k + st[d].slot : 0];
+#pragma unroll
+                for (int i = 0; i < RS; ++i) {
+                    const f32x4 v = acc[i].all();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) sum[i][q] = mine ? fmaf(by, v[q], sum[i][q]) : sum[i][q];
+                    acc[i].clear();
+                }
+            }
+            load(st[d]);
         }
     }
 #pragma unroll
@@ -498,7 +576,7 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
         if (g.down_bias)
             for (int i = 0; i < g.k; ++i) {
                 const int e = chosen.index[t * g.k + i];
-                if (e >= 0) v = fmaf(g.weight[t * g.k + i], from_bf16(g.down_bias[(int64_t)e * g.dim + n]), v);
+                if (e >= 0) v = fmaf(weight[t * g.k + i], from_bf16(g.down_bias[(int64_t)e * g.dim + n]), v);
             }
         g.out[(int64_t)t * g.dim + n] = to_bf16(v);
     }
@@ -513,9 +591,9 @@ int32_t launched(const char *what) {
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 // Who finds the experts of a call.
-Route route_of(int T, int E, int64_t dim) {
-    if ((int64_t)T * E > kMostLogits || (int64_t)T * E * E > kMostRanks) return kRouted;
-    return E * dim <= 32768 ? kAllInOne : kFromLogits;
+Route route_of(int E, int64_t dim) {
+    if (E > kMostHere) return kRouted;
+    return E <= kMostInOne && E * dim <= 32768 ? kAllInOne : kFromLogits;
 }
 
 // Pieces of the logits' sums: 8 lines each, half a line a wave.
@@ -528,13 +606,14 @@ void launch_products(const FfnArgs &g, hipStream_t st) {
         const int64_t units = most * ((g.hidden + columns - 1) / columns);
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(units, kCUs)), dim3(kThreads), 0, st, g);
     };
-    if (g.dim > 256 * kWaves) up(k_ffn_up<Form, Few, 128, 1, true>, 8);
-    else if (g.dim <= 128 * kWaves && most * (g.hidden / 16) >= kCUs) up(k_ffn_up<Form, Few, 128, 2, false>, 16);
-    else up(k_ffn_up<Form, Few, 256, 1, false>, 8);
+    constexpr int UD = Form == BSR_WEIGHTS_BF16 ? 1 : Form == BSR_WEIGHTS_FP8 ? 2 : 3, DD = Few ? 3 : 2;
+    if (g.dim > 256 * kWaves) up(k_ffn_up<Form, Few, 128, 1, 1, true>, 8);
+    else if (g.dim <= 128 * kWaves && most * (g.hidden / 16) >= kCUs) up(k_ffn_up<Form, Few, 128, 2, Form == BSR_WEIGHTS_MX4 && !Few || UD < 2 ? 1 : 2, false>, 16);
+    else up(k_ffn_up<Form, Few, 256, 1, UD, false>, 8);
     if (g.dim >= 16 * kCUs)
-        hipLaunchKernelGGL((k_ffn_down<Form, Few, 2>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kThreads), 0, st, g);
+        hipLaunchKernelGGL((k_ffn_down<Form, Few, 2, DD>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kThreads), 0, st, g);
     else
-        hipLaunchKernelGGL((k_ffn_down<Form, Few, 1>), dim3((unsigned)(g.dim / 8)), dim3(kThreads), 0, st, g);
+        hipLaunchKernelGGL((k_ffn_down<Form, Few, 1, DD>), dim3((unsigned)(g.dim / 8)), dim3(kThreads), 0, st, g);
 }
 
 template <int Form>
@@ -546,14 +625,14 @@ void launch_products(const FfnArgs &g, hipStream_t st) {
 }  // namespace
 
 size_t expert_ffn_workspace_bytes(int T, int dim, int hidden, int E, int k) {
-    return up16((size_t)parts_of(route_of(T, E, dim), dim) * T * E * 4) + 2 * up16((size_t)T * k * 4) + (size_t)T * k * hidden * 2;
+    return up16((size_t)parts_of(route_of(E, dim), dim) * T * E * 4) + 2 * up16((size_t)T * k * 4) + (size_t)T * k * hidden * 2;
 }
 
 int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,
                           int form, const void *up, const uint8_t *up_scales, const void *down, const uint8_t *down_scales,
                           const uint16_t *up_bias, const uint16_t *down_bias, uint16_t *out, void *workspace, void *stream) {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const Route r = route_of(T, E, dim);
+    const Route r = route_of(E, dim);
     FfnArgs g{x, T, dim, hidden, E, k, renorm, r, parts_of(r, dim), router, up, down, up_scales, down_scales, up_bias, down_bias, out,
               nullptr, nullptr, nullptr, nullptr};
     g.logits = reinterpret_cast<float *>(ws);
