@@ -192,13 +192,19 @@ __device__ __forceinline__ f32x4 logit_sums(const FfnArgs &g, int e0, int first,
     const uint32_t row = token < g.T ? (uint32_t)(token * g.dim) * 2u : kPast;
     Sums<Few> acc;
     acc.clear();
-#pragma unroll 4
-    for (int s = first; s < to; s += step) {
-        const Held w = load_line(m, e0, s);
-        bf16x8 v[Tokens<Few>::kN];
+    constexpr int B = 4;   // lines in flight
+    for (int s0 = first; s0 < to; s0 += B * step) {
+        Held w[B];
+        bf16x8 v[B][Tokens<Few>::kN];
 #pragma unroll
-        for (int i = 0; i < Tokens<Few>::kN; ++i) v[i] = load_tokens<BSR_WEIGHTS_BF16, Few>(x, row, g.dim, s, 0, i);
-        acc.add(expand<BSR_WEIGHTS_BF16>(w, 0), v);
+        for (int b = 0; b < B; ++b) {
+            const int s = s0 + b * step;
+            w[b] = load_line(m, e0, s, s < to);
+#pragma unroll
+            for (int i = 0; i < Tokens<Few>::kN; ++i) v[b][i] = load_tokens<BSR_WEIGHTS_BF16, Few>(x, row, g.dim, s, 0, i);
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) acc.add(expand<BSR_WEIGHTS_BF16>(w[b], 0), v[b]);
     }
     return acc.all();
 }
@@ -283,7 +289,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 // expert (NaN is larger than all, -infinity is never chosen), as bsr_router_fwd. One work-group writes index and weight for the
 // down product. (Ranks by counting the better experts of each, 64 comparisons a thread at 16 tokens and 64 experts: 4 us more.)
 constexpr int kMostHere = 256;   // experts of a work-group that routes
-constexpr int kRounds = kMostHere / 64;
+constexpr int kRounds = kMostHere / 64, kMostParts = 8;
 
 template <bool Few>
 __device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, float *logit) {
@@ -299,6 +305,7 @@ __device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, f
     __syncthreads();
     const int t = wave;   // kTok <= kWaves
     if (t >= g.T) return;
+    const __amdgpu_buffer_rsrc_t logits = make_rsrc(g.logits, (uint32_t)(g.parts * g.T * g.E) * 4u);
     float l[kRounds];
     uint32_t key[kRounds];
     int slot[kRounds];
@@ -310,8 +317,14 @@ __device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, f
             if (g.route == kAllInOne) {
                 l[r] = logit[t * g.E + e];
             } else {
+                float piece[kMostParts];   // all of them in flight, 0 where there is none
+#pragma unroll
+                for (int p = 0; p < kMostParts; ++p)
+                    piece[p] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                        logits, p < g.parts ? (uint32_t)((p * g.T + t) * g.E + e) * 4u : kPast, 0, 0));
                 l[r] = 0.f;
-                for (int p = 0; p < g.parts; ++p) l[r] += g.logits[((int64_t)p * g.T + t) * g.E + e];
+#pragma unroll
+                for (int p = 0; p < kMostParts; ++p) l[r] += piece[p];
             }
         }
         const uint32_t bits = __float_as_uint(l[r] + 0.f);   // -0 is 0
@@ -597,7 +610,7 @@ Route route_of(int E, int64_t dim) {
 }
 
 // Pieces of the logits' sums: 8 lines each, half a line a wave.
-int parts_of(Route r, int dim) { return r == kFromLogits ? std::min(8, (dim + 511) / 512) : 1; }
+int parts_of(Route r, int dim) { return r == kFromLogits ? std::min(kMostParts, (dim + 511) / 512) : 1; }
 
 template <int Form, bool Few>
 void launch_products(const FfnArgs &g, hipStream_t st) {
