@@ -56,45 +56,65 @@ struct Line {
     static constexpr int kValues = 8 * kV;                                                        // of a line
 };
 
-// One expert's matrix [rows][cols] of a form.
+// The matrices [rows][cols] of a form, one an expert. Loads that are not wanted (of experts, rows or chunks that do not exist) are
+// issued too, at an offset past the end: behind a branch the compiler could not count the loads in flight, and would wait for all
+// of them before it uses the oldest.
 template <int Form>
 struct Matrix {
-    __amdgpu_buffer_rsrc_t codes, scales;
-    int rows, cols;
-    uint32_t pitch;
-    __device__ __forceinline__ Matrix(const void *p, const uint8_t *s, int e, int rows_, int cols_) : rows(rows_), cols(cols_) {
+    const uint8_t *codes, *scales;
+    uint32_t pitch, bytes, scale_bytes;   // of a row's codes, of a matrix
+    int rows, blocks;                     // blocks: bytes of scales a row of 128 x 128 blocks (fp8)
+    __device__ __forceinline__ Matrix(const void *p, const uint8_t *s, int rows_, int cols)
+        : codes(static_cast<const uint8_t *>(p)), scales(s), rows(rows_), blocks((cols + 127) / 128) {
         pitch = (uint32_t)cols / Line<Form>::kV * 16u;
-        const uint32_t bytes = (uint32_t)rows * pitch;
-        codes = make_rsrc(static_cast<const uint8_t *>(p) + (int64_t)e * bytes, bytes);
-        uint32_t sb = 0;
-        if constexpr (Form == BSR_WEIGHTS_MX4) sb = (uint32_t)((cols + 255) / 256) * (uint32_t)rows * 8u;
-        if constexpr (Form == BSR_WEIGHTS_FP8) sb = (uint32_t)((cols + 127) / 128) * (uint32_t)((rows + 127) / 128);
-        scales = make_rsrc(s + (int64_t)e * sb, sb);
+        bytes = (uint32_t)rows * pitch;
+        scale_bytes = Form == BSR_WEIGHTS_MX4 ? (uint32_t)((cols + 255) / 256) * (uint32_t)rows * 8u
+                                              : Form == BSR_WEIGHTS_FP8 ? (uint32_t)blocks * (uint32_t)((rows + 127) / 128) : 0u;
     }
 };
+
+// One expert of them; not live: nothing is read.
+template <int Form>
+struct Expert {
+    __amdgpu_buffer_rsrc_t codes, scales;
+    __device__ __forceinline__ Expert(const Matrix<Form> &m, int e, bool live)
+        : codes(make_rsrc(m.codes + (int64_t)e * m.bytes, live ? m.bytes : 0u)),
+          scales(make_rsrc(m.scales + (int64_t)e * m.scale_bytes, live ? m.scale_bytes : 0u)) {}
+};
+
+// A line that no row has: its pieces lie from 2^32 - 128 on, past every row.
+constexpr int kNoLine = (1 << 25) - 1;
 
 struct Held {
     u32x4 codes;
     uint32_t byte;
 };
 
-// Line s of the rows n0 .. n0 + 7 (n0 a multiple of 8); zeros outside of the matrix, and where it is not live. Loads that are not
-// wanted are issued too, at an offset past the end: behind a branch the compiler could not count the loads in flight, and would
-// wait for all of them before it uses the oldest.
+// A lane's piece of line s of 8 rows, from the first of them on: what stays the same for all groups of 8 rows. Lane (g = l / 16,
+// r = l % 16) takes chunk 2 g + r / 8 of row r % 8.
 template <int Form>
-__device__ __forceinline__ Held load_line(const Matrix<Form> &m, int n0, int s, bool live = true) {
-    const int lane = threadIdx.x & 63, r = lane & 7, chunk = 2 * (lane >> 4) + (lane >> 3 & 1);
-    const uint32_t at = (uint32_t)s * 128u + (uint32_t)chunk * 16u;
-    const bool in = live && at < m.pitch && n0 < m.rows;
-    Held v;
-    v.codes = __builtin_bit_cast(u32x4, buf_load16(m.codes, in ? (uint32_t)(n0 + r) * m.pitch + at : kPast, 0));
-    v.byte = 0;
-    if constexpr (Form == BSR_WEIGHTS_MX4)
-        v.byte = __builtin_amdgcn_raw_buffer_load_b8(m.scales, in ? ((uint32_t)s * (uint32_t)m.rows + (uint32_t)(n0 + r)) * 8u + chunk : kPast, 0, 0);
-    if constexpr (Form == BSR_WEIGHTS_FP8)
-        v.byte = __builtin_amdgcn_raw_buffer_load_b8(m.scales, in ? (uint32_t)(n0 >> 7) * (uint32_t)((m.cols + 127) / 128) + s : kPast, 0, 0);
-    return v;
-}
+struct Piece8 {
+    uint32_t code, scale;   // offsets
+    bool in;                // the chunk exists
+    __device__ __forceinline__ Piece8(const Matrix<Form> &m, int s) {
+        const int lane = threadIdx.x & 63, r = lane & 7, chunk = 2 * (lane >> 4) + (lane >> 3 & 1);
+        const uint32_t at = (uint32_t)s * 128u + (uint32_t)chunk * 16u;
+        in = at < m.pitch;
+        code = (uint32_t)r * m.pitch + at;
+        scale = Form == BSR_WEIGHTS_MX4 ? ((uint32_t)s * (uint32_t)m.rows + (uint32_t)r) * 8u + chunk : (uint32_t)s;
+    }
+    // Of the 8 rows from n0 (a multiple of 8).
+    __device__ __forceinline__ Held load(const Matrix<Form> &m, const Expert<Form> &e, int n0) const {
+        Held v;
+        v.codes = __builtin_bit_cast(u32x4, buf_load16(e.codes, in ? code + (uint32_t)n0 * m.pitch : kPast, 0));
+        v.byte = 0;
+        if constexpr (Form == BSR_WEIGHTS_MX4)
+            v.byte = __builtin_amdgcn_raw_buffer_load_b8(e.scales, in ? scale + (uint32_t)n0 * 8u : kPast, 0, 0);
+        if constexpr (Form == BSR_WEIGHTS_FP8)
+            v.byte = __builtin_amdgcn_raw_buffer_load_b8(e.scales, in ? scale + (uint32_t)(n0 >> 7) * (uint32_t)m.blocks : kPast, 0, 0);
+        return v;
+    }
+};
 
 template <int Form>
 __device__ __forceinline__ bf16x8 expand(const Held &v, int p) {
@@ -186,7 +206,8 @@ __device__ __forceinline__ float pick(f32x4 v) {
 // Sums of 8 experts' logits over the lines first, first + step, ... below `to` by one wave.
 template <bool Few>
 __device__ __forceinline__ f32x4 logit_sums(const FfnArgs &g, int e0, int first, int step, int to) {
-    const Matrix<BSR_WEIGHTS_BF16> m(g.router, nullptr, 0, g.E, g.dim);
+    const Matrix<BSR_WEIGHTS_BF16> m(g.router, nullptr, g.E, g.dim);
+    const Expert<BSR_WEIGHTS_BF16> router(m, 0, true);
     const __amdgpu_buffer_rsrc_t x = make_rsrc(g.x, (uint32_t)(g.T * g.dim) * 2u);
     const int token = Tokens<Few>::token();
     const uint32_t row = token < g.T ? (uint32_t)(token * g.dim) * 2u : kPast;
@@ -199,7 +220,7 @@ __device__ __forceinline__ f32x4 logit_sums(const FfnArgs &g, int e0, int first,
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             const int s = s0 + b * step;
-            w[b] = load_line(m, e0, s, s < to);
+            w[b] = Piece8<BSR_WEIGHTS_BF16>(m, s < to ? s : kNoLine).load(m, router, e0);   // (of lines from `to` on: none)
 #pragma unroll
             for (int i = 0; i < Tokens<Few>::kN; ++i) v[b][i] = load_tokens<BSR_WEIGHTS_BF16, Few>(x, row, g.dim, s, 0, i);
         }
@@ -403,12 +424,14 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = Tokens<Few>::token();
     const __amdgpu_buffer_rsrc_t x = make_rsrc(g.x, (uint32_t)(g.T * g.dim) * 2u);
     const uint32_t row = token < g.T ? (uint32_t)(token * g.dim) * 2u : kPast;
-    const int tiles = (g.hidden + 8 * Q - 1) / (8 * Q), units = __builtin_amdgcn_readfirstlane(chosen.count) * tiles;
+    const int tiles = (g.hidden + 8 * Q - 1) / (8 * Q), count = __builtin_amdgcn_readfirstlane(chosen.count);
     const int spans = (g.dim + LN * kWaves * L::kValues - 1) / (LN * kWaves * L::kValues);
+    const Matrix<Form> m(g.up, g.up_scales, 2 * g.hidden, g.dim);
     bf16x8 v[LN][L::kP][N];
     struct Unit {
         Held w[LN][Q][2];
         uint32_t bias[Q];   // of the row that this thread joins
+        int a, n0;          // place of its expert (from count on: none), first gate row
     };
     // groups 2 j and 2 j + 1, neighbours in a wave, join gate and up
     const Group<Few> group(threadIdx.x >> 5);
@@ -423,20 +446,33 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
 #pragma unroll
                 for (int n = 0; n < N; ++n) v[i][p][n] = load_tokens<Form, Few>(x, row, g.dim, (z * LN + i) * kWaves + wave, p, n);
     };
-    auto load_w = [&](Unit &to, int u, int z) __attribute__((always_inline)) {
-        const bool live = u < units;
-        const int a = live ? u / tiles : 0, n0 = live ? u % tiles * 8 * Q : 0, e = __builtin_amdgcn_readfirstlane(chosen.expert[a]);
-        const Matrix<Form> m(g.up, g.up_scales, live ? e : 0, 2 * g.hidden, g.dim);
-        const __amdgpu_buffer_rsrc_t b = make_rsrc(g.up_bias + (int64_t)(live ? e : 0) * 2 * g.hidden, g.up_bias ? (uint32_t)g.hidden * 4u : 0u);
+    auto load_w = [&](Unit &to, int z) __attribute__((always_inline)) {
+        const bool live = to.a < count;
+        const int e = live ? __builtin_amdgcn_readfirstlane(chosen.expert[live ? to.a : 0]) : 0;
+        const Expert<Form> w(m, e, live);
+        const __amdgpu_buffer_rsrc_t b = make_rsrc(g.up_bias + (int64_t)e * 2 * g.hidden, g.up_bias ? (uint32_t)g.hidden * 4u : 0u);
+        if (z == 0) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            if (z == 0) to.bias[q] = __builtin_amdgcn_raw_buffer_load_b16(b, (uint32_t)(n0 + 8 * q + at + (gate ? 0 : g.hidden)) * 2u, 0, 0);
+            for (int q = 0; q < Q; ++q)
+                to.bias[q] = __builtin_amdgcn_raw_buffer_load_b16(b, (uint32_t)(to.n0 + 8 * q + at + (gate ? 0 : g.hidden)) * 2u, 0, 0);
+        }
 #pragma unroll
-            for (int i = 0; i < LN; ++i) {   // (a unit's last rows may lie past the gate's: they are not stored)
-                to.w[i][q][0] = load_line<Form>(m, n0 + 8 * q, (z * LN + i) * kWaves + wave, live);
-                to.w[i][q][1] = load_line<Form>(m, g.hidden + n0 + 8 * q, (z * LN + i) * kWaves + wave, live);
+        for (int i = 0; i < LN; ++i) {   // (a unit's last rows may lie past the gate's: they are not stored)
+            const Piece8<Form> piece(m, (z * LN + i) * kWaves + wave);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                to.w[i][q][0] = piece.load(m, w, to.n0 + 8 * q);
+                to.w[i][q][1] = piece.load(m, w, to.n0 + 8 * q + g.hidden);
             }
         }
+    };
+    int na = 0, ntile = blockIdx.x;   // of the next unit to load
+    auto next = [&](Unit &to) __attribute__((always_inline)) {
+        while (ntile >= tiles) ntile -= tiles, ++na;
+        to.a = na;
+        to.n0 = ntile * 8 * Q;
+        load_w(to, 0);
+        ntile += gridDim.x;
     };
     Sums<Few> acc[Q][2];
     auto products = [&](const Unit &of) __attribute__((always_inline)) {
@@ -449,22 +485,25 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) acc[q][c].add(expand<Form>(of.w[i][q][c], p), v[i][p]);
     };
-    int u = blockIdx.x, turn = 0;
-    const int stride = gridDim.x;
+    int turn = 0;
     Unit unit[D];
 #pragma unroll
-    for (int d = 0; d < D; ++d) load_w(unit[d], u + d * stride, 0);
+    for (int d = 0; d < D; ++d) next(unit[d]);
     load_x(0);
-    while (u < units) {
+    for (bool more = true; more;) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            if (u >= units) break;
+            const int a = unit[d].a, n0 = unit[d].n0;
+            if (a >= count) {
+                more = false;
+                break;
+            }
 #pragma unroll
             for (int q = 0; q < Q; ++q) acc[q][0].clear(), acc[q][1].clear();
             products(unit[d]);
             if constexpr (Wide) {
                 for (int z = 1; z < spans; ++z) {
-                    load_w(unit[d], u, z);
+                    load_w(unit[d], z);
                     load_x(z);
                     products(unit[d]);
                 }
@@ -473,31 +512,31 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
             uint32_t bias[Q];
 #pragma unroll
             for (int q = 0; q < Q; ++q) bias[q] = unit[d].bias[q];
-            load_w(unit[d], u + D * stride, 0);
+            next(unit[d]);
 #pragma unroll
             for (int q = 0; q < Q; ++q)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) part[turn][2 * q + c][wave][lane] = acc[q][c].all();
             __syncthreads();
             if (joins) {
-                const int a = u / tiles, slot = group.token < g.T ? chosen.slot[a][group.token] : kNone;
+                const int slot = group.token < g.T ? chosen.slot[a][group.token] : kNone;
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
                     const float mine = pick(group.join(part[turn][2 * q + !gate])) + from_bf16((uint16_t)bias[q]);
                     const float other = __shfl_xor(mine, 16);
-                    const int n = u % tiles * 8 * Q + 8 * q + at;
+                    const int n = n0 + 8 * q + at;
                     if ((threadIdx.x & 31) < 4 && slot != kNone && n < g.hidden)
                         g.h[(int64_t)(group.token * g.k + slot) * g.hidden + n] = to_bf16(mine / (1.f + __expf(-mine)) * other);
                 }
             }
-            u += stride;
             turn ^= 1;
         }
     }
 }
 
 // ------------------------------------------------------------------------------------------
-// out: 8 RS columns a work-group, over all chosen experts; the waves split the hidden columns, a line of each expert in turn.
+// out: 8 RS columns a work-group, over all chosen experts; the waves split the lines of all of them, neighbouring ones a wave, so that
+// a wave seldom changes its expert.
 // ------------------------------------------------------------------------------------------
 template <int Form, bool Few, int RS, int D>
 __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
@@ -519,43 +558,59 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = Tokens<Few>::token();
     const __amdgpu_buffer_rsrc_t h = make_rsrc(g.h, (uint32_t)(g.T * g.k) * (uint32_t)g.hidden * 2u);
     const int n0 = blockIdx.x * 8 * RS, steps = (g.hidden + L::kValues - 1) / L::kValues, count = __builtin_amdgcn_readfirstlane(chosen.count);
+    const Matrix<Form> m(g.down, g.down_scales, g.dim, g.hidden);
 
     struct Stage {
         Held w[RS];
         bf16x8 v[L::kP][N];
-        int a, slot;    // the expert's place, its slot of this lane's token or kNone
+        int slot;           // of this lane's token for the stage's expert, or kNone
+        bool valid, last;   // a line of this wave; its last one of the expert
     };
-    int a = 0, s = wave;   // of the next stage to load
-    while (s >= steps) s -= steps, ++a;
-    auto load = [&](Stage &st) __attribute__((always_inline)) {
-        st.a = a;
+    // this wave's lines: left of them to load, the next one
+    const int total = count * steps, per = total / kWaves, more = total % kWaves;
+    int left = per + (wave < more ? 1 : 0);
+    const int from = wave * per + min(wave, more);
+    int a = from / steps, s = from - a * steps, slot = kNone;
+    Expert<Form> w(m, 0, false);
+    uint32_t row = kPast;
+    auto expert = [&]() __attribute__((always_inline)) {   // a's: where its weights and its tokens' rows of h lie
         const bool live = a < count;
-        const int place = live ? a : 0, e = __builtin_amdgcn_readfirstlane(chosen.expert[place]);
-        const Matrix<Form> m(g.down, g.down_scales, live ? e : 0, g.dim, g.hidden);
-        st.slot = live ? chosen.slot[place][token] : kNone;
-        const int at = st.slot != kNone ? token * g.k + st.slot : 0;
-        const uint32_t row = st.slot != kNone ? (uint32_t)at * (uint32_t)g.hidden * 2u : kPast;
+        w = Expert<Form>(m, live ? __builtin_amdgcn_readfirstlane(chosen.expert[live ? a : 0]) : 0, live);
+        slot = live ? chosen.slot[a][token] : kNone;
+        row = slot != kNone ? (uint32_t)(token * g.k + slot) * (uint32_t)g.hidden * 2u : kPast;
+    };
+    auto load = [&](Stage &st) __attribute__((always_inline)) {
+        if (s == steps) {
+            s = 0;
+            ++a;
+            expert();
+        }
+        st.valid = left > 0;
+        st.last = left == 1 || s + 1 == steps;
+        st.slot = slot;
+        const Piece8<Form> piece(m, left > 0 ? s : kNoLine);
 #pragma unroll
-        for (int i = 0; i < RS; ++i) st.w[i] = load_line<Form>(m, n0 + 8 * i, s, live);
+        for (int i = 0; i < RS; ++i) st.w[i] = piece.load(m, w, n0 + 8 * i);
 #pragma unroll
         for (int p = 0; p < L::kP; ++p)
 #pragma unroll
-            for (int n = 0; n < N; ++n) st.v[p][n] = load_tokens<Form, Few>(h, row, g.hidden, s, p, n);
-        s += kWaves;
-        while (s >= steps) s -= steps, ++a;
+            for (int n = 0; n < N; ++n) st.v[p][n] = load_tokens<Form, Few>(h, left > 0 ? row : kPast, g.hidden, s, p, n);
+        ++s;
+        --left;
     };
     f32x4 sum[RS] = {};
     Sums<Few> acc[RS];
 #pragma unroll
     for (int i = 0; i < RS; ++i) acc[i].clear();
     Stage st[D];
+    expert();
 #pragma unroll
     for (int d = 0; d < D; ++d) load(st[d]);
-    for (bool more = true; more;) {
+    for (bool go = true; go;) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            if (st[d].a >= count) {
-                more = false;
+            if (!st[d].valid) {
+                go = false;
                 break;
             }
 #pragma unroll
@@ -564,7 +619,7 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
                 for (int i = 0; i < RS; ++i) acc[i].add(expand<Form>(st[d].w[i], p), st[d].v[p]);
             // the expert's last line of this wave: its sums, weighted, go into the tokens that chose it (others' are dropped: infinite
             // weights times no value)
-            if (st[(d + 1) % D].a != st[d].a || D == 1) {
+            if (st[d].last) {
                 const bool mine = st[d].slot != kNone;
                 const float by = weight[mine ? token * g.k + st[d].slot : 0];
 #pragma unroll
