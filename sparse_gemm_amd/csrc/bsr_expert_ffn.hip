@@ -668,17 +668,19 @@ Route route_of(int E, int64_t dim) {
 int parts_of(Route r, int dim) { return r == kFromLogits ? std::min(kMostParts, (dim + 511) / 512) : 1; }
 
 template <int Form, bool Few>
-void launch_products(const FfnArgs &g, hipStream_t st) {
+void launch_products(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
     const int64_t most = std::min(g.E, g.T * g.k);
     auto up = [&](auto kernel, int columns) {
         const int64_t units = most * ((g.hidden + columns - 1) / columns);
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(units, kCUs)), dim3(kThreads), 0, st, g);
     };
+    // units loaded ahead: what the registers hold beside the tokens' values
     constexpr int UD = Form == BSR_WEIGHTS_BF16 ? 1 : Form == BSR_WEIGHTS_FP8 ? 2 : 3, DD = Few ? 3 : 2;
-    if (g.dim > 256 * kWaves) up(k_ffn_up<Form, Few, 128, 1, 1, true>, 8);
-    else if (g.dim <= 128 * kWaves && most * (g.hidden / 16) >= kCUs) up(k_ffn_up<Form, Few, 128, 2, Form == BSR_WEIGHTS_MX4 && !Few || UD < 2 ? 1 : 2, false>, 16);
+    constexpr int QD = Form == BSR_WEIGHTS_BF16 || (Form == BSR_WEIGHTS_MX4 && !Few) ? 1 : 2;
+    if (v.wide) up(k_ffn_up<Form, Few, 128, 1, 1, true>, 8);
+    else if (v.q == 2) up(k_ffn_up<Form, Few, 128, 2, QD, false>, 16);
     else up(k_ffn_up<Form, Few, 256, 1, UD, false>, 8);
-    if (g.dim >= 16 * kCUs)
+    if (v.rs == 2)
         hipLaunchKernelGGL((k_ffn_down<Form, Few, 2, DD>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kThreads), 0, st, g);
     else
         hipLaunchKernelGGL((k_ffn_down<Form, Few, 1, DD>), dim3((unsigned)(g.dim / 8)), dim3(kThreads), 0, st, g);
@@ -686,8 +688,9 @@ void launch_products(const FfnArgs &g, hipStream_t st) {
 
 template <int Form>
 void launch_products(const FfnArgs &g, hipStream_t st) {
-    if (g.T <= 8) launch_products<Form, true>(g, st);
-    else launch_products<Form, false>(g, st);
+    const FfnVariant v = ffn_variant(g.T, g.dim, g.hidden, g.E, g.k);
+    if (v.few) launch_products<Form, true>(g, v, st);
+    else launch_products<Form, false>(g, v, st);
 }
 
 }  // namespace

@@ -1,18 +1,19 @@
 // bsr_experts_few.hip -- grouped products for few rows an expert (decode): forward and input gradient on bf16 weights
-// (include/bsr_experts.h), forward on microscaled 4-bit weights (include/bsr_mx4.h).
+// (include/bsr_experts.h), forward on microscaled 4-bit weights (include/bsr_mx4.h) and on 8-bit ones (include/bsr_fp8_blocks.h).
 //
 // The weights' bytes are the least that they need. A work-group owns up to 16 MT rows of one expert and BN output columns, and
-// streams the BN weight rows in steps of 256 columns (512 bytes of bf16 or 128 bytes of codes a row; for the input
+// streams the BN weight rows in steps of 256 columns (512 bytes of bf16, 256 or 128 bytes of codes a row; for the input
 // gradient 2 BN bytes of 256 weight rows: whole cache lines in most cases) through a ring of NS LDS stages by
 // direct-to-LDS loads, NS - 1 steps ahead. Its four waves split each step's contraction, 64 each, for all BN
 // columns of the output (16 x 16 x 32 products, fp32 sums) and add their sums through LDS at the end, in a fixed
 // order: with the contraction split inside the work-group, BN can be small, and a narrow layer still fills the card.
 // Weights not in the caches, bytes of the experts that have rows: 8 of 8, 4096 -> 14336, one row each: in bf16 146 us, 6.4 TB/s,
-// in 4 bits 51 us, 4.9 TB/s; 4 tokens, k = 2 of 8, there (5.5 experts on average) 45 us, 4.4 TB/s. 64 of 64, 4096 -> 1536, in
-// bf16: 128 us, 6.3 TB/s. Nothing is read twice (219 MB counted for 7 experts' 218): the 4-bit tiles have 16 steps each in about three
-// rounds of work-groups, whose starts and ends weigh. One token, k = 2 of 8, 2048 -> 1024 in bf16: 6 us, eight dependent steps.
+// in 8 bits 93 us, 5.0 TB/s, in 4 bits 51 us, 4.9 TB/s; 4 tokens, k = 2 of 8, there (5.5 experts on average) in 4 bits 45 us, 4.4 TB/s, in 8 bits
+// 77 us, 4.2. 64 of 64, 4096 -> 1536, in bf16: 128 us, 6.3 TB/s. Nothing is read twice (219 MB counted for 7 experts' 218): the tiles
+// of codes have 16 steps each in a few rounds of work-groups, whose starts and ends weigh. One token, k = 2 of 8, 2048 -> 1024 in bf16: 6 us, eight dependent steps.
 //   bf16: lane (r = l % 16, g = l / 16) takes the columns 64 w + 32 i + 8 g + 0 .. 7 of wave w's product i
 //   4-bit: the columns 64 w + 16 g + 8 i + 0 .. 7, so that its 16 codes are 8 neighbouring bytes of one group
+//   8-bit: the same columns; the scale of a wave's 64 columns is one byte for all rows of the tile, kept by lane s for step s of 64
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -20,6 +21,7 @@
 
 #include "bsr_experts_internal.hpp"
 #include "bsr_experts_tile.hpp"
+#include "bsr_fp8_device.hpp"
 #include "bsr_mx4_device.hpp"
 
 namespace bsr {
@@ -30,7 +32,7 @@ using namespace dev;
 struct FewArgs {
     const uint16_t *X;
     const void *W;
-    const uint8_t *scales;   // 4-bit weights
+    const uint8_t *scales;   // 4-bit and 8-bit weights
     const uint16_t *bias;
     uint16_t *Y;
     const int32_t *offsets, *gather;
@@ -38,13 +40,13 @@ struct FewArgs {
 };
 
 // Weights of a tile: bf16 with the contraction contiguous (forward), bf16 with the output columns contiguous
-// (input gradient), 4-bit codes with the contraction contiguous.
-enum Weights { kRowsW, kColsW, kMx4W };
+// input gradient), 4-bit or 8-bit codes with the contraction contiguous.
+enum Weights { kRowsW, kColsW, kMx4W, kFp8W };
 
 template <Weights W, int MT, int BN, int NS>
 struct FewLayout {
     static constexpr int kM = 16 * MT;
-    static constexpr int kA = kM * 512, kB = W == kMx4W ? BN * 128 : BN * 512, kS = W == kMx4W ? BN * 8 : 0;
+    static constexpr int kA = kM * 512, kB = BN * (W == kMx4W ? 128 : W == kFp8W ? 256 : 512), kS = W == kMx4W ? BN * 8 : 0;
     static constexpr int kStage = kA + kB + kS, kRed = 4 * kM * (BN + 4) * 4;
     static constexpr int kLds = NS * kStage > kRed ? NS * kStage : kRed;
     static constexpr int kALoads = 2 * MT, kBLoads = kB / 4096, kLoads = kALoads + kBLoads + (W == kMx4W ? 1 : 0);   // a wave and stage
@@ -61,7 +63,7 @@ __device__ __forceinline__ int cswz(int r) {
 template <Weights W, int MT, int BN, int NS>
 __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_expert_few(FewArgs g, int ntiles) {
     using L = FewLayout<W, MT, BN, NS>;
-    constexpr bool MX4 = W == kMx4W, COLS = W == kColsW;
+    constexpr bool MX4 = W == kMx4W, FP8 = W == kFp8W, COLS = W == kColsW;
     static_assert(L::kB % 4096 == 0 && (W == kRowsW || BN == 64 || BN == 32), "whole loads a wave");
     constexpr int NT = BN / 16;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[L::kLds];
@@ -83,13 +85,20 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
         for (int i = 0; i < NT; ++i) acc[m][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if (steps > 0) {
-        const int64_t wrow = MX4 ? g.C / 2 : COLS ? (int64_t)g.N * 2 : (int64_t)g.C * 2;   // bytes of a weight row
+        const int64_t wrow = MX4 ? g.C / 2 : FP8 ? g.C : COLS ? (int64_t)g.N * 2 : (int64_t)g.C * 2;   // bytes of a weight row
         const int64_t wbytes = wrow * (COLS ? g.C : g.N);
         const int xrows = g.gather ? g.T : g.R;
         const __amdgpu_buffer_rsrc_t rx =
             g.gather ? make_rsrc(g.X, (uint32_t)((int64_t)xrows * g.C * 2))
                      : make_rsrc(g.X + (int64_t)t.at * g.C, (uint32_t)((int64_t)t.n * g.C * 2));   // the tile's own rows
         const __amdgpu_buffer_rsrc_t rw = make_rsrc(static_cast<const uint8_t *>(g.W) + e * wbytes, (uint32_t)wbytes);
+        // 8-bit: lane l keeps the byte of step l of 64. The load is waited for by itself: in the loop the compiler, which cannot know
+        // whether it is a step after one, would wait for all loads of every step.
+        const int groups = (g.C + 127) / 128;
+        const uint8_t *ws = g.scales + ((int64_t)e * ((g.N + 127) / 128) + n0 / 128) * groups;
+        auto scale_of = [&](int s) __attribute__((always_inline)) { return ws[min(2 * (s + lane) + (wave >> 1), groups - 1)]; };
+        int held = 0;
+        if constexpr (FP8) held = scale_of(0);
         // Each load: byte offset at step 0 and the number of steps in which its bytes exist.
         uint32_t aoff[L::kALoads], boff[L::kBLoads];
         int alim[L::kALoads], blim[L::kBLoads];
@@ -108,18 +117,20 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
                 boff[j] = (uint32_t)r * (uint32_t)wrow + (uint32_t)(n0 + 8 * q) * 2u;
                 blim[j] = n0 + 8 * q < g.N ? (g.C - r + 255) / 256 : 0;
             } else {
-                const int r = MX4 ? 8 * i + (lane >> 3) : 2 * i + (lane >> 5);
-                const int q = MX4 ? (lane & 7) ^ swz8(r) : (lane & 31) ^ (r & 15);
+                const int r = MX4 ? 8 * i + (lane >> 3) : FP8 ? 4 * i + (lane >> 4) : 2 * i + (lane >> 5);
+                const int q = MX4 ? (lane & 7) ^ swz8(r) : (lane & (FP8 ? 15 : 31)) ^ (r & 15);
                 boff[j] = (uint32_t)(n0 + r) * (uint32_t)wrow + (uint32_t)q * 16u;
-                blim[j] = n0 + r >= g.N ? 0 : MX4 ? (g.C / 2 - 16 * q + 127) / 128 : (g.C * 2 - 16 * q + 511) / 512;
+                blim[j] = n0 + r >= g.N ? 0 : MX4 ? (g.C / 2 - 16 * q + 127) / 128
+                                            : FP8 ? (g.C - 16 * q + 255) / 256 : (g.C * 2 - 16 * q + 511) / 512;
             }
         }
-        const uint32_t bstep = MX4 ? 128u : COLS ? 256u * (uint32_t)wrow : 512u;
+        const uint32_t bstep = MX4 ? 128u : FP8 ? 256u : COLS ? 256u * (uint32_t)wrow : 512u;
         // 4-bit: word h of row 32 w + r (w = wave % (BN / 32): several waves load the same words)
         const int sw = wave % (BN >= 32 ? BN / 32 : 1), kb = (g.C + 255) / 256, srow = n0 + sw * 32 + (lane >> 1);
         const __amdgpu_buffer_rsrc_t rs = MX4 ? make_rsrc(g.scales + (int64_t)e * kb * g.N * 8, (uint32_t)((int64_t)kb * g.N * 8)) : rw;
         const uint32_t soff = (uint32_t)srow * 8u + 4u * (lane & 1);
         const int slim = srow < g.N ? steps : 0;
+        if constexpr (FP8) asm volatile("" : "+v"(held));
         auto issue = [&](int s) __attribute__((always_inline)) {
             const uint32_t to = base + (uint32_t)(s % NS) * L::kStage;
 #pragma unroll
@@ -139,12 +150,13 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
             const unsigned char *ta = smem + (s % NS) * L::kStage, *tb = ta + L::kA;
             bf16x8 fa[MT][2], fb[NT][2];
             uint2 codes[MX4 ? NT : 1];
+            u32x4 codes8[FP8 ? NT : 1];
             uint32_t byte[MX4 ? NT : 1];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int q = MX4 ? wave * 8 + 2 * gq + i : wave * 8 + 4 * i + gq;
+                    const int q = MX4 || FP8 ? wave * 8 + 2 * gq + i : wave * 8 + 4 * i + gq;
                     fa[m][i] = *reinterpret_cast<const bf16x8 *>(ta + (16 * m + r16) * 512 + ((q ^ r16) << 4));
                 }
 #pragma unroll
@@ -153,6 +165,9 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
                     const int r = c * 16 + r16, q = 2 * wave + (gq >> 1);   // the group
                     codes[c] = *reinterpret_cast<const uint2 *>(tb + r * 128 + ((q ^ swz8(r)) << 4) + 8 * (gq & 1));
                     byte[c] = *(ta + L::kA + L::kB + r * 8 + q);
+                } else if constexpr (FP8) {
+                    const int r = c * 16 + r16;
+                    codes8[c] = *reinterpret_cast<const u32x4 *>(tb + r * 256 + (((4 * wave + gq) ^ r16) << 4));
                 } else if constexpr (COLS) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -172,6 +187,7 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
                 }
             }
             issue(s + NS - 1);   // while the reads arrive; into the stage of step s - 1, which every wave has read
+            const float scale8 = FP8 ? mx4_scale_bits(__builtin_amdgcn_readlane(held, s & 63)) : 0.f;
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
                 if constexpr (MX4) {   // bytes past the contraction may hold anything
@@ -179,11 +195,19 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
                     fb[c][0] = mx4_expand8(codes[c].x, scale);
                     fb[c][1] = mx4_expand8(codes[c].y, scale);
                 }
+                if constexpr (FP8) {
+                    fb[c][0] = fp8_expand8(make_uint2(codes8[c][0], codes8[c][1]), scale8);
+                    fb[c][1] = fp8_expand8(make_uint2(codes8[c][2], codes8[c][3]), scale8);
+                }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[c][i], fa[m][i], acc[m][c], 0, 0, 0);
+            }
+            if (FP8 && (s & 63) == 63) {
+                held = scale_of(s + 1);
+                asm volatile("" : "+v"(held));
             }
         }
         wait_vm<0, 0>(0);   // the last loads (of zeros) leave the stages
@@ -247,6 +271,15 @@ int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, int mt, const uint16_t *
     const char *what = "bsr_expert_fwd_mx4";
     if (few_cols_mx4(mt, s.R, s.E, s.N) == 32) return launch<kMx4W, 1, 32, 4>(g, stream, what);
     return mt == 1 ? launch<kMx4W, 1, 64, 4>(g, stream, what) : launch<kMx4W, 2, 64, 3>(g, stream, what);
+}
+
+int32_t launch_expert_fwd_few_fp8(const ExpertShape &s, int mt, const uint16_t *X, const uint8_t *codes,
+                                  const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream) {
+    const FewArgs g{X, codes, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
+    const char *what = "bsr_expert_fwd_fp8";
+    if (few_cols_fp8(mt, s.R, s.E, s.N) == 32) return launch<kFp8W, 1, 32, 5>(g, stream, what);
+    return mt == 1 ? launch<kFp8W, 1, 64, 3>(g, stream, what)
+                   : mt == 2 ? launch<kFp8W, 2, 64, 4>(g, stream, what) : launch<kFp8W, 4, 64, 3>(g, stream, what);
 }
 
 }  // namespace bsr

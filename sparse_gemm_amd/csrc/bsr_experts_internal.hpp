@@ -57,6 +57,9 @@ inline int32_t check_grid(int64_t blocks, int threads, const char *what) {
 //   forward 4096 -> 14336, E = 8    16: 160 | 166   24: 203 | 196   32: 208 | 169
 //   input gradient of 4096 -> 14336, E = 1   16: 38 | 108    128: 43 | 108    384: 114 | 109
 //   4-bit forward 4096 -> 14336, E = 8       16: 58 | 103    24: 65 | 103     48: 100 | 113    64: 107 | 115    96: 159 | 125
+//   8-bit forward 4096 -> 14336, E = 8       16: 101 | 127    32: 123 | 127    48: 135 | 131    64: 143 | 134    96: 204 | 143
+//   8-bit forward 4096 -> 4096, E = 1        16: 9 | 40    64: 11 | 41    128: 14 | 41    256: 17 | 42    384: 31 | 43
+//   8-bit forward 2064 -> 1008, E = 60       16: 32 | 42    20: 40 | 43    32: 42 | 45    48: 48 | 48    64: 53 | 51
 struct TileKind {
     int id, rows, cols, step, slots;
     double alone, shared;
@@ -88,6 +91,8 @@ constexpr TileKind kBwdInputTiles[] = {{1, 16, 64, 256, 256, 0.65, 0.65}, {2, 32
                                        {256, 256, 256, 64, 256, 1.60, 1.60}};
 constexpr TileKind kFwdMx4Tiles[] = {{1, 16, 64, 256, 512, 0.45, 0.75}, {2, 32, 64, 256, 512, 0.60, 0.90},
                                      {128, 128, 128, 64, 512, 0.56, 1.00}};
+constexpr TileKind kFwdFp8Tiles[] = {{1, 16, 64, 256, 512, 0.50, 0.72}, {2, 32, 64, 256, 256, 0.70, 0.57},
+                                     {4, 64, 64, 256, 256, 0.87, 0.80}, {128, 128, 128, 64, 512, 0.61, 0.92}};
 
 // Row tiles that R rows in E groups and the rows past the plan can need.
 inline int64_t max_row_tiles(int64_t R, int64_t E, int64_t bm) { return (R + std::min(E + 1, R) * (bm - 1)) / bm; }
@@ -105,12 +110,27 @@ inline int few_cols_bwd_input(int mt, int64_t R, int64_t E, int64_t cols) {
 inline int few_cols_mx4(int mt, int64_t R, int64_t E, int64_t cols) {
     return mt == 1 && max_row_tiles(R, E, 16) * ((cols + 63) / 64) <= 256 ? 32 : 64;
 }
+// 8-bit weights, the same, while tiles of 64 leave a quarter of the CUs without one: one row, one expert, 4096 -> 4096: 7.6 us
+// against 10.5; where they do not, 64 rows of it (256 tiles) 12.4 against 11.1, one row of 60 experts, 2064 -> 1008: 31 against 29. And
+// 32 where that fills a last round of work-groups, two a CU, that tiles of 64 leave half empty: one row of 8 experts, 4096 -> 14336
+// (7 rounds or 3.5): 94 against 102; 4 tokens, k = 2 of 8, there: 77 against 84.
+inline int few_cols_fp8(int mt, int64_t R, int64_t E, int64_t cols) {
+    if (mt != 1) return 64;
+    const int64_t groups = std::min(E, R), tiles = groups * ((R / groups + 15) / 16) * ((cols + 63) / 64);   // of equal groups
+    const int64_t rounds = (tiles + 511) / 512, halves = (2 * tiles + 511) / 512;
+    return tiles <= 192 || (rounds > 1 && halves * 21 < rounds * 40) ? 32 : 64;
+}
+
+// 8 bits on both sides: 256 x 256 tiles with 8 waves where the groups fill them, else 128 x 128 with 4, two work-groups a CU.
+inline bool wide_fp8(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 + 1) * ((cols + 255) / 256) >= 192; }
 
 int32_t launch_expert_fwd_few(const ExpertShape &s, int mt, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
                               uint16_t *Y, void *stream);
 int32_t launch_expert_bwd_input_few(const ExpertShape &s, int mt, const uint16_t *dY, const uint16_t *W, uint16_t *dX,
                                     void *stream);
 int32_t launch_expert_fwd_few_mx4(const ExpertShape &s, int mt, const uint16_t *X, const uint8_t *codes,
+                                  const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream);
+int32_t launch_expert_fwd_few_fp8(const ExpertShape &s, int mt, const uint16_t *X, const uint8_t *codes,
                                   const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream);
 int32_t launch_expert_bwd_input(const ExpertShape &s, const uint16_t *dY, const uint16_t *W, uint16_t *dX, void *stream);
 int32_t launch_expert_bwd_weight(const ExpertShape &s, const uint16_t *dY, const uint16_t *X, uint16_t *dW,
@@ -138,6 +158,19 @@ int32_t launch_expert_fwd_fp8(const ExpertShape &s, const uint16_t *X, const uin
 int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, const uint8_t *xscales, const uint8_t *codes,
                                   const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream);
 
+// Kernels of the whole layer for few tokens. few: up to 8 tokens share an operand. Of the up product a wave holds `span` of the columns
+// and a unit is 8 q gate rows with their up rows; wide: more columns than the 16 waves hold, in several spans. rs: sets of 8 output
+// columns of a work-group of the down product.
+struct FfnVariant {
+    bool few;
+    int span, q;
+    bool wide;
+    int rs;
+};
+inline FfnVariant ffn_variant(int64_t T, int64_t dim, int64_t hidden, int64_t E, int64_t k) {
+    const bool wide = dim > 16 * 256, many = dim <= 16 * 128 && std::min(E, T * k) * (hidden / 16) >= 256;
+    return {T <= 8, wide || many ? 128 : 256, many ? 2 : 1, wide, dim >= 16 * 256 ? 2 : 1};
+}
 size_t expert_ffn_workspace_bytes(int T, int dim, int hidden, int E, int k);
 int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,
                           int form, const void *up, const uint8_t *up_scales, const void *down, const uint8_t *down_scales,

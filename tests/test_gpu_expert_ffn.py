@@ -81,8 +81,11 @@ def test_layer(form, T, dim, hidden, E, k, renorm, bias):
     assert torch.isnan(room[T:]).all()
 
 
+WIDE_CASES = [(1, 2048, 1024, 8, 2), (4, 4096, 1792, 8, 2), (16, 4128, 288, 16, 4), (3, 8224, 96, 4, 2), (11, 4096, 64, 24, 3)]
+
+
 @pytest.mark.parametrize("form", ["bf16", "mx4", "fp8"])
-@pytest.mark.parametrize("T,dim,hidden,E,k", [(1, 2048, 1024, 8, 2), (4, 4096, 1792, 8, 2), (16, 4128, 288, 16, 4), (3, 8224, 96, 4, 2)])
+@pytest.mark.parametrize("T,dim,hidden,E,k", WIDE_CASES)
 def test_wide_layer(form, T, dim, hidden, E, k):
     say(f"case expert_ffn {form} T={T} dim={dim} hidden={hidden} E={E} k={k}")
     m = Layer(form, T, dim, hidden, E, k, True, False)

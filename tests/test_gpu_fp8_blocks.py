@@ -156,7 +156,7 @@ def near(got, want, S, terms, lost=0.0):
 FP8_PRODUCTS = [(kind, T, k, E, N, max(16, K // 16 * 16)) for kind, T, k, E, N, K in PRODUCTS] + [
     ("ragged", 3, 2, 4, 1024, 2048), ("one", 20, 1, 2, 72, 1040), ("one", 270, 1, 1, 304, 784), ("ragged", 70, 4, 8, 256, 768),
     ("ragged", 10000, 2, 70, 1032, 528), ("ragged", 150, 4, 4, 200, 352),
-    ("one", 530, 1, 1, 16392, 96), ("ragged", 400, 2, 2, 12296, 288), ("dropped", 700, 2, 3, 16400, 528)]
+    ("one", 530, 1, 1, 16392, 96), ("ragged", 400, 2, 2, 12296, 288), ("dropped", 700, 2, 3, 16400, 528), ("ragged", 128, 2, 4, 2056, 784)]
 
 
 @pytest.mark.parametrize("kind,T,k,E,N,K", FP8_PRODUCTS)
