@@ -121,8 +121,21 @@ inline int few_cols_fp8(int mt, int64_t R, int64_t E, int64_t cols) {
     return tiles <= 192 || (rounds > 1 && halves * 21 < rounds * 40) ? 32 : 64;
 }
 
-// 8 bits on both sides: 256 x 256 tiles with 8 waves where the groups fill them, else 128 x 128 with 4, two work-groups a CU.
-inline bool wide_fp8(int64_t R, int64_t E, int64_t cols) { return R >= 192 * E && (R / 256 + 1) * ((cols + 255) / 256) >= 192; }
+// 8 bits on both sides: 256 x 256 tiles with 8 waves, one work-group a CU, or 128 x 128 with 4, two of them. Equal groups again; a last
+// round of 256 x 256 tiles that leaves half of the CUs idle or more is taken in halves, which cost 0.65 of a round. Both sides, us (rows
+// of all experts: 128 x 128 | 256 x 256):
+//   4096 -> 14336, E = 8     128: 109 | 123    512: 112 | 124    1024: 141 | 128    2048: 214 | 180
+//   4096 -> 4096, E = 8      512: 28 | 35    1024: 36 | 36    2048: 58 | 50    4096: 92 | 85    8192: 163 | 142
+//   4096 -> 4096, E = 1      256: 23 | 30    1024: 27 | 32    2048: 38 | 37    4096: 73 | 62
+//   2048 -> 1008, E = 64     1024: 24 | 31    4096: 26 | 31    8192: 43 | 33    16384: 58 | 59
+inline bool wide_fp8(int64_t R, int64_t E, int64_t cols, int64_t C) {
+    const TileKind small = {128, 128, 128, 128, 512, 0.72, 1.25};
+    const double groups = (double)std::min(E, R), each = (double)R / groups;
+    const double tiles = (E == 1 ? std::ceil(each / 256) : groups * std::max(1.0, each / 256 + 0.5)) * std::ceil((double)cols / 256);
+    const double whole = std::floor(tiles / 256), rest = tiles / 256 - whole;
+    const double rounds = whole + (rest == 0 ? 0.0 : rest <= 0.5 ? 0.65 : 1.0);
+    return rounds * (std::ceil((double)C / 128) * 1.6 + 2.0) < tile_time(small, R, E, cols, C);
+}
 
 int32_t launch_expert_fwd_few(const ExpertShape &s, int mt, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
                               uint16_t *Y, void *stream);

@@ -350,7 +350,7 @@ int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, c
     const GemmArgs g{xcodes, codes, xscales, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
     const char *what = "bsr_expert_fwd_fp8_fp8";
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const bool w = wide_fp8(s.R, s.E, s.N);
+    const bool w = wide_fp8(s.R, s.E, s.N, s.K);
     const int64_t bm = w ? 256 : 128, ntiles = (s.N + bm - 1) / bm;
     const int64_t blocks = max_row_tiles(s.R, s.E, bm) * ntiles + (w ? kPieces : 0);
     if (const int32_t bad = check_grid(blocks, 512, what)) return bad;

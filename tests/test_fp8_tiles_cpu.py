@@ -27,7 +27,7 @@ int main() {
             const int id = bsr::best_tile(bsr::kFwdFp8Tiles, a, b, c, d);
             std::printf("%d %d\n", id <= 4 ? 16 * id : id, id <= 4 ? bsr::few_cols_fp8(id, a, b, c) : id);
         } else if (kind == 'f') {
-            const int bm = bsr::wide_fp8(a, b, c) ? 256 : 128;
+            const int bm = bsr::wide_fp8(a, b, c, d) ? 256 : 128;
             std::printf("%d %d\n", bm, bm);
         } else {
             const bsr::FfnVariant v = bsr::ffn_variant(a, b, c, d, e);
