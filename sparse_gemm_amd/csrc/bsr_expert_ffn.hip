@@ -537,47 +537,47 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
 // ------------------------------------------------------------------------------------------
 // out: 8 RS columns a work-group, over all chosen experts; the waves split the lines of all of them, neighbouring ones a wave, so that
 // a wave seldom changes its expert.
+// Of 9 to 16 tokens an expert has up to 8 in most calls: then they share an operand as up to 8 tokens of a call do (Packed), column c
+// being the expert's c-th token, and its sums go to the tokens' lanes at the expert's end.
 // ------------------------------------------------------------------------------------------
-template <int Form, bool Few, int RS, int D>
-__global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
+template <int Form, bool Few, bool Packed, int RS, int D>
+__device__ __forceinline__ void down_sums(const FfnArgs &g, const Chosen &chosen, const float *weight, int n0, f32x4 (&sum)[RS]) {
     using L = Line<Form>;
-    constexpr int N = Tokens<Few>::kN;
-    __shared__ Chosen chosen;
-    __shared__ Part part[RS];
-    __shared__ float weight[kTok * kMaxSlots];
-    clear(g, chosen);
-    __syncthreads();
-    if ((int)threadIdx.x < g.T * g.k) {
-        const int e = g.index[threadIdx.x];
-        weight[threadIdx.x] = g.weight[threadIdx.x];
-        if ((unsigned)e < (unsigned)g.E) choose(chosen, threadIdx.x, e);
-    }
-    __syncthreads();
-    list(g, chosen);
-    __syncthreads();
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = Tokens<Few>::token();
+    constexpr bool Shared = Few || Packed;
+    constexpr int N = Tokens<Shared>::kN;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), column = Tokens<Shared>::token();
     const __amdgpu_buffer_rsrc_t h = make_rsrc(g.h, (uint32_t)(g.T * g.k) * (uint32_t)g.hidden * 2u);
-    const int n0 = blockIdx.x * 8 * RS, steps = (g.hidden + L::kValues - 1) / L::kValues, count = __builtin_amdgcn_readfirstlane(chosen.count);
+    const int steps = (g.hidden + L::kValues - 1) / L::kValues, count = __builtin_amdgcn_readfirstlane(chosen.count);
     const Matrix<Form> m(g.down, g.down_scales, g.dim, g.hidden);
 
     struct Stage {
         Held w[RS];
         bf16x8 v[L::kP][N];
-        int slot;           // of this lane's token for the stage's expert, or kNone
+        int item;           // token k + slot of this lane's column, or -1
+        uint32_t tokens;    // Packed: bit t: token t chose the expert
         bool valid, last;   // a line of this wave; its last one of the expert
     };
     // this wave's lines: left of them to load, the next one
     const int total = count * steps, per = total / kWaves, more = total % kWaves;
     int left = per + (wave < more ? 1 : 0);
     const int from = wave * per + min(wave, more);
-    int a = from / steps, s = from - a * steps, slot = kNone;
+    int a = from / steps, s = from - a * steps, item = -1;
+    uint32_t tokens = 0, row = kPast;
     Expert<Form> w(m, 0, false);
-    uint32_t row = kPast;
     auto expert = [&]() __attribute__((always_inline)) {   // a's: where its weights and its tokens' rows of h lie
         const bool live = a < count;
         w = Expert<Form>(m, live ? __builtin_amdgcn_readfirstlane(chosen.expert[live ? a : 0]) : 0, live);
-        slot = live ? chosen.slot[a][token] : kNone;
-        row = slot != kNone ? (uint32_t)(token * g.k + slot) * (uint32_t)g.hidden * 2u : kPast;
+        int token = column;
+        if constexpr (Packed) {
+            tokens = live ? (uint32_t)__ballot(chosen.slot[a][lane & 15] != kNone) & 0xFFFFu : 0u;
+            uint32_t rest = tokens;
+#pragma unroll
+            for (int i = 0; i < 7; ++i) rest = i < column ? rest & (rest - 1) : rest;
+            token = rest ? __builtin_ctz(rest) : -1;
+        }
+        const int slot = live && token >= 0 ? chosen.slot[a][token] : kNone;
+        item = slot != kNone ? token * g.k + slot : -1;
+        row = item >= 0 ? (uint32_t)item * (uint32_t)g.hidden * 2u : kPast;
     };
     auto load = [&](Stage &st) __attribute__((always_inline)) {
         if (s == steps) {
@@ -587,19 +587,19 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
         }
         st.valid = left > 0;
         st.last = left == 1 || s + 1 == steps;
-        st.slot = slot;
+        st.item = item;
+        st.tokens = tokens;
         const Piece8<Form> piece(m, left > 0 ? s : kNoLine);
 #pragma unroll
         for (int i = 0; i < RS; ++i) st.w[i] = piece.load(m, w, n0 + 8 * i);
 #pragma unroll
         for (int p = 0; p < L::kP; ++p)
 #pragma unroll
-            for (int n = 0; n < N; ++n) st.v[p][n] = load_tokens<Form, Few>(h, left > 0 ? row : kPast, g.hidden, s, p, n);
+            for (int n = 0; n < N; ++n) st.v[p][n] = load_tokens<Form, Shared>(h, left > 0 ? row : kPast, g.hidden, s, p, n);
         ++s;
         --left;
     };
-    f32x4 sum[RS] = {};
-    Sums<Few> acc[RS];
+    Sums<Shared> acc[RS];
 #pragma unroll
     for (int i = 0; i < RS; ++i) acc[i].clear();
     Stage st[D];
@@ -620,18 +620,59 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
             // the expert's last line of this wave: its sums, weighted, go into the tokens that chose it (others' are dropped: infinite
             // weights times no value)
             if (st[d].last) {
-                const bool mine = st[d].slot != kNone;
-                const float by = weight[mine ? token * g.k + st[d].slot : 0];
+                const float by = weight[max(st[d].item, 0)];
+                const int t = lane & 15;
+                const bool mine = Packed ? lane < 32 && (st[d].tokens >> t & 1) : st[d].item >= 0;
+                const int even = 4 * ((lane & 16) + __popc(st[d].tokens & ((1u << t) - 1u))), odd = even + 4 * Tokens<true>::kOdd;
 #pragma unroll
                 for (int i = 0; i < RS; ++i) {
                     const f32x4 v = acc[i].all();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) sum[i][q] = mine ? fmaf(by, v[q], sum[i][q]) : sum[i][q];
+                    for (int q = 0; q < 4; ++q) {
+                        float one = v[q] * by;
+                        if constexpr (Packed)
+                            one = __int_as_float(__builtin_amdgcn_ds_bpermute(even, __float_as_int(one))) +
+                                  __int_as_float(__builtin_amdgcn_ds_bpermute(odd, __float_as_int(one)));
+                        sum[i][q] = mine ? sum[i][q] + one : sum[i][q];
+                    }
                     acc[i].clear();
                 }
             }
             load(st[d]);
         }
+    }
+}
+
+template <int Form, bool Few, int RS>
+__global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
+    __shared__ Chosen chosen;
+    __shared__ Part part[RS];
+    __shared__ float weight[kTok * kMaxSlots];
+    clear(g, chosen);
+    __syncthreads();
+    if ((int)threadIdx.x < g.T * g.k) {
+        const int e = g.index[threadIdx.x];
+        weight[threadIdx.x] = g.weight[threadIdx.x];
+        if ((unsigned)e < (unsigned)g.E) choose(chosen, threadIdx.x, e);
+    }
+    __syncthreads();
+    list(g, chosen);
+    __syncthreads();
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = blockIdx.x * 8 * RS;
+    f32x4 sum[RS] = {};
+    // lines loaded ahead: what the registers hold
+    if constexpr (Few) {
+        down_sums<Form, true, false, RS, 3>(g, chosen, weight, n0, sum);
+    } else {
+        bool many = false;   // an expert with more than 8 tokens
+        for (int a = lane; a < chosen.count; a += 64) {
+            int none = 0;
+#pragma unroll
+            for (int i = 0; i < kTok / 4; ++i) none += __popc(reinterpret_cast<const uint32_t *>(chosen.slot[a])[i] & 0x80808080u);
+            many |= kTok - none > 8;
+        }
+        if (__ballot(many)) down_sums<Form, false, false, RS, 2>(g, chosen, weight, n0, sum);
+        else down_sums<Form, false, true, RS, 3>(g, chosen, weight, n0, sum);
     }
 #pragma unroll
     for (int i = 0; i < RS; ++i) part[i][wave][lane] = sum[i];
@@ -675,15 +716,15 @@ void launch_products(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(units, kCUs)), dim3(kThreads), 0, st, g);
     };
     // units loaded ahead: what the registers hold beside the tokens' values
-    constexpr int UD = Form == BSR_WEIGHTS_BF16 ? 1 : Form == BSR_WEIGHTS_FP8 ? 2 : 3, DD = Few ? 3 : 2;
+    constexpr int UD = Form == BSR_WEIGHTS_BF16 ? 1 : Form == BSR_WEIGHTS_FP8 ? 2 : 3;
     constexpr int QD = Form == BSR_WEIGHTS_BF16 || (Form == BSR_WEIGHTS_MX4 && !Few) ? 1 : 2;
     if (v.wide) up(k_ffn_up<Form, Few, 128, 1, 1, true>, 8);
     else if (v.q == 2) up(k_ffn_up<Form, Few, 128, 2, QD, false>, 16);
     else up(k_ffn_up<Form, Few, 256, 1, UD, false>, 8);
     if (v.rs == 2)
-        hipLaunchKernelGGL((k_ffn_down<Form, Few, 2, DD>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kThreads), 0, st, g);
+        hipLaunchKernelGGL((k_ffn_down<Form, Few, 2>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kThreads), 0, st, g);
     else
-        hipLaunchKernelGGL((k_ffn_down<Form, Few, 1, DD>), dim3((unsigned)(g.dim / 8)), dim3(kThreads), 0, st, g);
+        hipLaunchKernelGGL((k_ffn_down<Form, Few, 1>), dim3((unsigned)(g.dim / 8)), dim3(kThreads), 0, st, g);
 }
 
 template <int Form>

@@ -92,6 +92,22 @@ def test_wide_layer(form, T, dim, hidden, E, k):
     m.check(expert_layer.expert_ffn(**m.args()))
 
 
+@pytest.mark.parametrize("form", ["bf16", "mx4", "fp8"])
+@pytest.mark.parametrize("T,first", [(9, 1), (9, 8), (9, 9), (16, 7), (16, 8), (16, 0), (13, 8), (8, 8)])
+@pytest.mark.parametrize("dim", [1, 128])
+def test_tokens_of_one_expert(form, T, first, dim):
+    """Up to 8 tokens of an expert share an operand: `first` tokens choose one expert, the others the other."""
+    dim *= 32
+    m = Layer(form, T, dim, 96, 3, 1, True, True)
+    m.router = torch.zeros(3, dim).bfloat16()
+    m.router[1, 5], m.router[2, 5] = 4.0, -4.0
+    order = torch.randperm(T, generator=gen(first))
+    m.x[:, 5] = -1.0
+    m.x[order[:first], 5] = 1.0
+    assert m.want()[2].reshape(-1).tolist().count(1) == first
+    m.check(expert_layer.expert_ffn(**m.args()))
+
+
 def test_ties_go_to_the_lowest_expert():
     m = Layer("bf16", 6, 136, 24, 16, 3, True, False)
     m.router = m.router[torch.arange(16) // 2 * 2]   # pairs of equal logits
