@@ -30,6 +30,7 @@ struct FfnArgs {
     const uint16_t *x;
     int T, dim, hidden, E, k;
     int renorm, route, parts;   // route: who finds the experts (Route); parts: pieces of the logits' sums
+    int waves;                  // of a set of the up product (FfnVariant)
     const uint16_t *router;
     const void *up, *down;
     const uint8_t *up_scales, *down_scales;
@@ -169,8 +170,9 @@ struct Sums {
 };
 
 // The waves' sums of one set of 8 rows. A group of 16 lanes joins 4 rows of one token: lane w takes those of wave w, 65 vectors apart
-// so that the 16 take different banks, and four row rotations add them up, in an order that is the same for every lane. With one
+// so that the 16 take different banks, and four exchanges add them up, in an order that is the same for every lane. With one
 // thread a sum, 32 reads each, the join took longer than the weights of a unit.
+// Where the waves are sets of 4 or 8 that hold other rows each, the lanes of a set join its rows.
 typedef f32x4 Part[kWaves][65];
 
 template <bool Few>
@@ -178,17 +180,19 @@ struct Group {
     static constexpr int kCount = Few ? 16 : 32;   // of a set
     int token, quad;                               // rows 4 quad .. 4 quad + 3
     __device__ __forceinline__ explicit Group(int j) : token(j % (kCount / 2)), quad(j / (kCount / 2)) {}
-    __device__ __forceinline__ f32x4 join(const Part &part) const {
+    __device__ __forceinline__ f32x4 join(const Part &part, int waves = kWaves) const {
         const int w = threadIdx.x & 15, at = quad * 16 + token;
         f32x4 v = part[w][at] + part[w][at + Tokens<Few>::kOdd];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), 0x128, 0xf, 0xf, true));
-            v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), 0x124, 0xf, 0xf, true));
-            v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), 0x122, 0xf, 0xf, true));
-            v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), 0x121, 0xf, 0xf, true));
-        }
+        add<0xB1>(v);    // lane ^ 1
+        add<0x4E>(v);    // lane ^ 2
+        if (waves > 4) add<0x141>(v);    // 7 - lane of 8
+        if (waves > 8) add<0x140>(v);    // 15 - lane of 16
         return v;
+    }
+    template <int Dpp>
+    static __device__ __forceinline__ void add(f32x4 &v) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[q]), Dpp, 0xf, 0xf, true));
     }
 };
 
@@ -401,6 +405,8 @@ __device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, f
 // h: Q times 8 gate rows and their up rows of one chosen expert a unit; the waves split the columns, Span of them each, and hold
 // their tokens' values there over all units. Weights are loaded D units ahead.
 // Wide: more columns than the waves hold, taken in several spans whose tokens' values are loaded for every unit.
+// Where fewer waves hold the columns, g.waves of them are a set with its own 8 Q rows of a unit: 16 tokens on 64 4-bit experts,
+// 1024 / 2048: the layer 86 us, without sets 131; 4 tokens on 64 8-bit ones, 1024 / 1024: 37 | 41.
 // ------------------------------------------------------------------------------------------
 template <int Form, bool Few, int Span, int Q, int D, bool Wide>
 __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
@@ -424,8 +430,9 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), token = Tokens<Few>::token();
     const __amdgpu_buffer_rsrc_t x = make_rsrc(g.x, (uint32_t)(g.T * g.dim) * 2u);
     const uint32_t row = token < g.T ? (uint32_t)(token * g.dim) * 2u : kPast;
-    const int tiles = (g.hidden + 8 * Q - 1) / (8 * Q), count = __builtin_amdgcn_readfirstlane(chosen.count);
-    const int spans = (g.dim + LN * kWaves * L::kValues - 1) / (LN * kWaves * L::kValues);
+    const int waves = Wide ? kWaves : g.waves, set = wave / waves, line = wave % waves, rows = 8 * Q * (kWaves / waves);   // of a unit
+    const int tiles = (g.hidden + rows - 1) / rows, count = __builtin_amdgcn_readfirstlane(chosen.count);
+    [[maybe_unused]] const int spans = (g.dim + LN * kWaves * L::kValues - 1) / (LN * kWaves * L::kValues);
     const Matrix<Form> m(g.up, g.up_scales, 2 * g.hidden, g.dim);
     bf16x8 v[LN][L::kP][N];
     struct Unit {
@@ -436,7 +443,7 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
     // groups 2 j and 2 j + 1, neighbours in a wave, join gate and up
     const Group<Few> group(threadIdx.x >> 5);
     const bool gate = !(threadIdx.x & 16), joins = threadIdx.x < 2 * Group<Few>::kCount * 16;
-    const int at = 4 * group.quad + (threadIdx.x & 3);
+    const int at = 8 * Q * ((threadIdx.x & 15) / waves) + 4 * group.quad + (threadIdx.x & 3);
     // lines of span z: neighbouring ones for neighbouring waves
     auto load_x = [&](int z) __attribute__((always_inline)) {
 #pragma unroll
@@ -444,7 +451,7 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
 #pragma unroll
             for (int p = 0; p < L::kP; ++p)
 #pragma unroll
-                for (int n = 0; n < N; ++n) v[i][p][n] = load_tokens<Form, Few>(x, row, g.dim, (z * LN + i) * kWaves + wave, p, n);
+                for (int n = 0; n < N; ++n) v[i][p][n] = load_tokens<Form, Few>(x, row, g.dim, (z * LN + i) * waves + line, p, n);
     };
     auto load_w = [&](Unit &to, int z) __attribute__((always_inline)) {
         const bool live = to.a < count;
@@ -458,11 +465,11 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
         }
 #pragma unroll
         for (int i = 0; i < LN; ++i) {   // (a unit's last rows may lie past the gate's: they are not stored)
-            const Piece8<Form> piece(m, (z * LN + i) * kWaves + wave);
+            const Piece8<Form> piece(m, (z * LN + i) * waves + line);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                to.w[i][q][0] = piece.load(m, w, to.n0 + 8 * q);
-                to.w[i][q][1] = piece.load(m, w, to.n0 + 8 * q + g.hidden);
+                to.w[i][q][0] = piece.load(m, w, to.n0 + 8 * (Q * set + q));
+                to.w[i][q][1] = piece.load(m, w, to.n0 + 8 * (Q * set + q) + g.hidden);
             }
         }
     };
@@ -470,7 +477,7 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
     auto next = [&](Unit &to) __attribute__((always_inline)) {
         while (ntile >= tiles) ntile -= tiles, ++na;
         to.a = na;
-        to.n0 = ntile * 8 * Q;
+        to.n0 = ntile * rows;
         load_w(to, 0);
         ntile += gridDim.x;
     };
@@ -522,10 +529,10 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
                 const int slot = group.token < g.T ? chosen.slot[a][group.token] : kNone;
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
-                    const float mine = pick(group.join(part[turn][2 * q + !gate])) + from_bf16((uint16_t)bias[q]);
+                    const float mine = pick(group.join(part[turn][2 * q + !gate], waves)) + from_bf16((uint16_t)bias[q]);
                     const float other = __shfl_xor(mine, 16);
                     const int n = n0 + 8 * q + at;
-                    if ((threadIdx.x & 31) < 4 && slot != kNone && n < g.hidden)
+                    if (gate && (threadIdx.x & 15) % waves < 4 && slot != kNone && n < g.hidden)
                         g.h[(int64_t)(group.token * g.k + slot) * g.hidden + n] = to_bf16(mine / (1.f + __expf(-mine)) * other);
                 }
             }
@@ -710,17 +717,17 @@ int parts_of(Route r, int dim) { return r == kFromLogits ? std::min(kMostParts, 
 
 template <int Form, bool Few>
 void launch_products(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
-    const int64_t most = std::min(g.E, g.T * g.k);
-    auto up = [&](auto kernel, int columns) {
-        const int64_t units = most * ((g.hidden + columns - 1) / columns);
+    const int rows = 8 * v.q * (kWaves / v.waves);
+    const int64_t units = (int64_t)std::min(g.E, g.T * g.k) * ((g.hidden + rows - 1) / rows);
+    auto up = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(units, kCUs)), dim3(kThreads), 0, st, g);
     };
     // units loaded ahead: what the registers hold beside the tokens' values
     constexpr int UD = Form == BSR_WEIGHTS_BF16 ? 1 : Form == BSR_WEIGHTS_FP8 ? 2 : 3;
     constexpr int QD = Form == BSR_WEIGHTS_BF16 || (Form == BSR_WEIGHTS_MX4 && !Few) ? 1 : 2;
-    if (v.wide) up(k_ffn_up<Form, Few, 128, 1, 1, true>, 8);
-    else if (v.q == 2) up(k_ffn_up<Form, Few, 128, 2, QD, false>, 16);
-    else up(k_ffn_up<Form, Few, 256, 1, UD, false>, 8);
+    if (v.wide) up(k_ffn_up<Form, Few, 128, 1, 1, true>);
+    else if (v.q == 2) up(k_ffn_up<Form, Few, 128, 2, QD, false>);
+    else up(k_ffn_up<Form, Few, 256, 1, UD, false>);
     if (v.rs == 2)
         hipLaunchKernelGGL((k_ffn_down<Form, Few, 2>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kThreads), 0, st, g);
     else
@@ -728,8 +735,9 @@ void launch_products(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
 }
 
 template <int Form>
-void launch_products(const FfnArgs &g, hipStream_t st) {
-    const FfnVariant v = ffn_variant(g.T, g.dim, g.hidden, g.E, g.k);
+void launch_products(FfnArgs g, hipStream_t st) {
+    const FfnVariant v = ffn_variant(Line<Form>::kValues, g.T, g.dim, g.hidden, g.E, g.k);
+    g.waves = v.waves;
     if (v.few) launch_products<Form, true>(g, v, st);
     else launch_products<Form, false>(g, v, st);
 }
@@ -745,7 +753,7 @@ int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, 
                           const uint16_t *up_bias, const uint16_t *down_bias, uint16_t *out, void *workspace, void *stream) {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Route r = route_of(E, dim);
-    FfnArgs g{x, T, dim, hidden, E, k, renorm, r, parts_of(r, dim), router, up, down, up_scales, down_scales, up_bias, down_bias, out,
+    FfnArgs g{x, T, dim, hidden, E, k, renorm, r, parts_of(r, dim), kWaves, router, up, down, up_scales, down_scales, up_bias, down_bias, out,
               nullptr, nullptr, nullptr, nullptr};
     g.logits = reinterpret_cast<float *>(ws);
     ws += up16((size_t)g.parts * T * E * 4);

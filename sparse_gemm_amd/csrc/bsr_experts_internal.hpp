@@ -171,18 +171,22 @@ int32_t launch_expert_fwd_fp8(const ExpertShape &s, const uint16_t *X, const uin
 int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, const uint8_t *xscales, const uint8_t *codes,
                                   const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream);
 
-// Kernels of the whole layer for few tokens. few: up to 8 tokens share an operand. Of the up product a wave holds `span` of the columns
-// and a unit is 8 q gate rows with their up rows; wide: more columns than the 16 waves hold, in several spans. rs: sets of 8 output
-// columns of a work-group of the down product.
+// Kernels of the whole layer for few tokens. few: up to 8 tokens share an operand. Of the up product a wave holds `span` of the columns,
+// whole lines of `values` of them, `waves` of the 16 hold all, and a unit is 8 q gate rows with their up rows for each such set; wide:
+// more columns than the 16 waves hold, in several spans. rs: sets of 8 output columns of a work-group of the down product.
 struct FfnVariant {
     bool few;
-    int span, q;
+    int span, q, waves;
     bool wide;
     int rs;
 };
-inline FfnVariant ffn_variant(int64_t T, int64_t dim, int64_t hidden, int64_t E, int64_t k) {
-    const bool wide = dim > 16 * 256, many = dim <= 16 * 128 && std::min(E, T * k) * (hidden / 16) >= 256;
-    return {T <= 8, wide || many ? 128 : 256, many ? 2 : 1, wide, dim >= 16 * 256 ? 2 : 1};
+inline FfnVariant ffn_variant(int values, int64_t T, int64_t dim, int64_t hidden, int64_t E, int64_t k) {
+    const int64_t most = std::min(E, T * k);
+    const bool wide = dim > 16 * 256, many = dim <= 16 * 128 && most * ((hidden + 15) / 16) >= 256;
+    const int64_t lines = (dim + values - 1) / values, each = std::max(1, 128 / values);
+    int waves = many ? 4 : 16;   // as few as hold the columns and leave every CU a unit
+    while (waves < 16 && (waves * each < lines || most * ((hidden + 256 / waves - 1) / (256 / waves)) < 256)) waves *= 2;
+    return {T <= 8, wide || many ? 128 : 256, many ? 2 : 1, waves, wide, dim >= 16 * 256 ? 2 : 1};
 }
 size_t expert_ffn_workspace_bytes(int T, int dim, int hidden, int E, int k);
 int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,

@@ -13,16 +13,18 @@ from test_gpu_fp8_blocks import FP8_PRODUCTS
 
 BF16_ACT = {(16, 32), (16, 64), (32, 64), (64, 64), (128, 128)}   # rows and columns of a tile
 FP8_ACT = {(128, 128), (256, 256)}
-# few, span, q, wide, rs
-LAYER = {(few, *v) for few in (0, 1) for v in ((128, 1, 1, 2), (128, 2, 0, 1), (256, 1, 0, 1), (256, 1, 0, 2))}
+VALUES = {"bf16": 64, "mx4": 256, "fp8": 128}   # of a line
+# few, span, q, waves, wide, rs
+LAYER = {(few, *v) for few in (0, 1) for v in ((128, 1, 16, 1, 2), (256, 1, 16, 0, 1), (256, 1, 16, 0, 2), (128, 2, 4, 0, 1),
+                                               (128, 2, 8, 0, 1), (128, 2, 16, 0, 1))}
 
 PROGRAM = r"""
 #include <cstdio>
 #include "bsr_experts_internal.hpp"
 int main() {
     char kind;
-    long a, b, c, d, e;
-    while (std::scanf(" %c %ld %ld %ld %ld %ld", &kind, &a, &b, &c, &d, &e) == 6) {
+    long a, b, c, d, e, f;
+    while (std::scanf(" %c %ld %ld %ld %ld %ld %ld", &kind, &a, &b, &c, &d, &e, &f) == 7) {
         if (kind == 'b') {
             const int id = bsr::best_tile(bsr::kFwdFp8Tiles, a, b, c, d);
             std::printf("%d %d\n", id <= 4 ? 16 * id : id, id <= 4 ? bsr::few_cols_fp8(id, a, b, c) : id);
@@ -30,8 +32,8 @@ int main() {
             const int bm = bsr::wide_fp8(a, b, c, d) ? 256 : 128;
             std::printf("%d %d\n", bm, bm);
         } else {
-            const bsr::FfnVariant v = bsr::ffn_variant(a, b, c, d, e);
-            std::printf("%d %d %d %d %d\n", v.few, v.span, v.q, v.wide, v.rs);
+            const bsr::FfnVariant v = bsr::ffn_variant(a, b, c, d, e, f);
+            std::printf("%d %d %d %d %d %d\n", v.few, v.span, v.q, v.waves, v.wide, v.rs);
         }
     }
 }
@@ -50,7 +52,7 @@ def variants(tmp_path_factory):
                     f"-I{os.path.join(ROOT, 'sparse_gemm_amd', 'csrc')}", str(src), "-o", str(exe)], check=True)
 
     def ask(kind, sizes):
-        text = "".join(f"{kind} {' '.join(map(str, (*s, 0)[:5]))}\n" for s in sizes)
+        text = "".join(f"{kind} {' '.join(map(str, (*s, 0, 0)[:6]))}\n" for s in sizes)
         out = subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True).stdout
         return {tuple(map(int, line.split())) for line in out.splitlines()}
 
@@ -66,14 +68,15 @@ def test_every_variant_is_taken(variants):
     products = some(100000, lambda log: (log(22), log(10), 8 * log(13), 16 * log(13)))
     assert variants("b", products) == BF16_ACT
     assert variants("f", products) == FP8_ACT
-    layers = some(100000, lambda log: (log(4), 32 * log(8), 32 * log(9), log(10), log(5)))
-    assert variants("l", [s for s in layers if s[4] <= s[3]]) == LAYER
+    for values in VALUES.values():
+        layers = some(100000, lambda log: (values, log(4), 32 * log(8), 32 * log(9), log(10), log(5)))   # noqa: B023
+        assert variants("l", [s for s in layers if s[5] <= s[4]]) == LAYER
 
 
 def test_every_variant_runs_on_the_gpu(variants):
     products = [(T * k, E, N, K) for _, T, k, E, N, K in FP8_PRODUCTS]
     assert variants("b", products) == BF16_ACT
     assert variants("f", products) == FP8_ACT
-    for step in STEP.values():
+    for form, step in STEP.items():
         layers = [(T, dim * step, hidden * step, E, k) for T, dim, hidden, E, k, _, _ in CASES]
-        assert variants("l", layers + WIDE_CASES) == LAYER
+        assert variants("l", [(VALUES[form], *c) for c in layers + WIDE_CASES]) == LAYER

@@ -63,7 +63,9 @@ STEP = {"bf16": 8, "fp8": 16, "mx4": 32}
 #        T, dim, hidden (in steps of the form), E, k, renormalize, bias
 CASES = [(1, 1, 1, 1, 1, True, False), (1, 8, 4, 8, 2, True, True), (3, 9, 7, 4, 4, False, True), (16, 5, 11, 60, 4, True, False),
          (16, 17, 3, 8, 2, False, True), (7, 33, 13, 64, 8, False, False), (2, 40, 67, 128, 8, True, True), (5, 3, 5, 200, 32, True, False),
-         (16, 4, 2, 1024, 32, False, True), (16, 2, 9, 12, 12, True, True), (9, 130, 21, 16, 1, False, False), (4, 19, 300, 4, 2, True, False)]
+         (16, 4, 2, 1024, 32, False, True), (16, 2, 9, 12, 12, True, True), (9, 130, 21, 16, 1, False, False), (4, 19, 300, 4, 2, True, False),
+         (8, 12, 1, 256, 32, True, True), (8, 40, 1, 256, 32, False, False), (8, 100, 1, 256, 32, True, False), (16, 40, 3, 256, 24, True, True),
+         (12, 100, 1, 256, 24, False, True)] + [(T, 20, hidden, 200, k, T > 8, False) for T, k in ((8, 32), (12, 20)) for hidden in (1, 2, 4)]
 
 
 @pytest.mark.parametrize("T,dim,hidden,E,k,renorm,bias", CASES)
