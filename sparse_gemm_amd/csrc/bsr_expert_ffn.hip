@@ -667,9 +667,11 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = blockIdx.x * 8 * RS;
     f32x4 sum[RS] = {};
-    // lines loaded ahead: what the registers hold
+    // Lines loaded ahead. More than three, which the registers could hold for most, win nothing, and of 4-bit weights the third cannot pay
+    // for its code, fetched cold in every launch: 4 tokens, 4096 / 7168 67 us | 70, 16 tokens on 32 experts, 2048 / 2048 68 | 69.
+    constexpr int D = Form == BSR_WEIGHTS_MX4 ? 2 : 3;
     if constexpr (Few) {
-        down_sums<Form, true, false, RS, 3>(g, chosen, weight, n0, sum);
+        down_sums<Form, true, false, RS, D>(g, chosen, weight, n0, sum);
     } else {
         bool many = false;   // an expert with more than 8 tokens
         for (int a = lane; a < chosen.count; a += 64) {
@@ -679,7 +681,7 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
             many |= kTok - none > 8;
         }
         if (__ballot(many)) down_sums<Form, false, false, RS, 2>(g, chosen, weight, n0, sum);
-        else down_sums<Form, false, true, RS, 3>(g, chosen, weight, n0, sum);
+        else down_sums<Form, false, true, RS, D>(g, chosen, weight, n0, sum);
     }
 #pragma unroll
     for (int i = 0; i < RS; ++i) part[i][wave][lane] = sum[i];
