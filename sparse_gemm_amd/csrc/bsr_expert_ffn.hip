@@ -40,6 +40,9 @@ struct FfnArgs {
     int32_t *index;    // [T][k]
     float *weight;     // [T][k]
     uint16_t *h;       // [T * k][hidden]
+    int splits;        // work-groups that share the lines of a down tile (FfnVariant)
+    float *partial;    // [splits][T][dim]
+    uint32_t *done;    // of each down tile: work-groups that have stored their sums
 };
 
 // Who finds the experts: the work-groups of the up product, each for itself, from x and the router or from logits that a
@@ -406,7 +409,7 @@ __device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, f
 // their tokens' values there over all units. Weights are loaded D units ahead.
 // Wide: more columns than the waves hold, taken in several spans whose tokens' values are loaded for every unit.
 // Where fewer waves hold the columns, g.waves of them are a set with its own 8 Q rows of a unit: 16 tokens on 64 4-bit experts,
-// 1024 / 2048: the layer 86 us, without sets 131; 4 tokens on 64 8-bit ones, 1024 / 1024: 37 | 41.
+// 1024 / 2048: the layer 86 us, without sets 131 (the down product unsplit); 4 tokens on 64 8-bit ones, 1024 / 1024: 37 | 41.
 // ------------------------------------------------------------------------------------------
 template <int Form, bool Few, int Span, int Q, int D, bool Wide>
 __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
@@ -416,6 +419,8 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
     __shared__ Part part[2][2 * Q];
     __shared__ float logit[kTok * kMostInOne];
     clear(g, chosen);
+    if (g.splits > 1 && blockIdx.x == 0)   // (tiles of the down product are fewer than CUs then)
+        for (int i = threadIdx.x; i < (g.dim + 7) / 8; i += kThreads) g.done[i] = 0;
     if (g.route == kRouted) {
         __syncthreads();
         const int i = threadIdx.x, e = i < g.T * g.k ? g.index[i] : -1;
@@ -544,11 +549,14 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
 // ------------------------------------------------------------------------------------------
 // out: 8 RS columns a work-group, over all chosen experts; the waves split the lines of all of them, neighbouring ones a wave, so that
 // a wave seldom changes its expert.
+// Where there are fewer tiles than CUs, g.splits work-groups share the lines of a tile; the last of them to be done adds up the sums of
+// all, in the order of their numbers: 8 tokens on 128 experts in bf16, 256 / 1024: the layer 35 us, with one work-group a tile 55; 16
+// tokens on 64 4-bit ones, 1024 / 2048: 72 | 84.
 // Of 9 to 16 tokens an expert has up to 8 in most calls: then they share an operand as up to 8 tokens of a call do (Packed), column c
 // being the expert's c-th token, and its sums go to the tokens' lanes at the expert's end.
 // ------------------------------------------------------------------------------------------
 template <int Form, bool Few, bool Packed, int RS, int D>
-__device__ __forceinline__ void down_sums(const FfnArgs &g, const Chosen &chosen, const float *weight, int n0, f32x4 (&sum)[RS]) {
+__device__ __forceinline__ void down_sums(const FfnArgs &g, const Chosen &chosen, const float *weight, int n0, int split, f32x4 (&sum)[RS]) {
     using L = Line<Form>;
     constexpr bool Shared = Few || Packed;
     constexpr int N = Tokens<Shared>::kN;
@@ -565,9 +573,9 @@ __device__ __forceinline__ void down_sums(const FfnArgs &g, const Chosen &chosen
         bool valid, last;   // a line of this wave; its last one of the expert
     };
     // this wave's lines: left of them to load, the next one
-    const int total = count * steps, per = total / kWaves, more = total % kWaves;
-    int left = per + (wave < more ? 1 : 0);
-    const int from = wave * per + min(wave, more);
+    const int total = count * steps, waves = kWaves * g.splits, at = split * kWaves + wave, per = total / waves, more = total % waves;
+    int left = per + (at < more ? 1 : 0);
+    const int from = at * per + min(at, more);
     int a = from / steps, s = from - a * steps, item = -1;
     uint32_t tokens = 0, row = kPast;
     Expert<Form> w(m, 0, false);
@@ -665,13 +673,14 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
     __syncthreads();
     list(g, chosen);
     __syncthreads();
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = blockIdx.x * 8 * RS;
+    __shared__ bool last;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = blockIdx.x * 8 * RS, split = blockIdx.y;
     f32x4 sum[RS] = {};
     // Lines loaded ahead. More than three, which the registers could hold for most, win nothing, and of 4-bit weights the third cannot pay
     // for its code, fetched cold in every launch: 4 tokens, 4096 / 7168 67 us | 70, 16 tokens on 32 experts, 2048 / 2048 68 | 69.
     constexpr int D = Form == BSR_WEIGHTS_MX4 ? 2 : 3;
     if constexpr (Few) {
-        down_sums<Form, true, false, RS, D>(g, chosen, weight, n0, sum);
+        down_sums<Form, true, false, RS, D>(g, chosen, weight, n0, split, sum);
     } else {
         bool many = false;   // an expert with more than 8 tokens
         for (int a = lane; a < chosen.count; a += 64) {
@@ -680,17 +689,34 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
             for (int i = 0; i < kTok / 4; ++i) none += __popc(reinterpret_cast<const uint32_t *>(chosen.slot[a])[i] & 0x80808080u);
             many |= kTok - none > 8;
         }
-        if (__ballot(many)) down_sums<Form, false, false, RS, 2>(g, chosen, weight, n0, sum);
-        else down_sums<Form, false, true, RS, D>(g, chosen, weight, n0, sum);
+        if (__ballot(many)) down_sums<Form, false, false, RS, 2>(g, chosen, weight, n0, split, sum);
+        else down_sums<Form, false, true, RS, D>(g, chosen, weight, n0, split, sum);
     }
 #pragma unroll
     for (int i = 0; i < RS; ++i) part[i][wave][lane] = sum[i];
     __syncthreads();
-    if (threadIdx.x >= RS * Group<Few>::kCount * 16) return;
     const Group<Few> j((threadIdx.x >> 4) % Group<Few>::kCount);
     const int set = (threadIdx.x >> 4) / Group<Few>::kCount, t = j.token, n = n0 + 8 * set + 4 * j.quad + (threadIdx.x & 3);
-    float v = pick(j.join(part[set]));
-    if ((threadIdx.x & 15) < 4 && t < g.T && n < g.dim) {
+    const bool mine = threadIdx.x < RS * Group<Few>::kCount * 16 && (threadIdx.x & 15) < 4 && t < g.T && n < g.dim;
+    float v = 0.f;
+    if (threadIdx.x < RS * Group<Few>::kCount * 16) v = pick(j.join(part[set]));
+    if (g.splits > 1) {
+        // Stores and loads that go past the XCDs' own caches, and a wait until the stores have arrived, in place of fences, which write
+        // the caches back: those took 80 us.
+        float *at = g.partial + (int64_t)t * g.dim + n;
+        const int64_t next = (int64_t)g.T * g.dim;
+        if (mine) __hip_atomic_store(at + split * next, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = __hip_atomic_fetch_add(&g.done[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)g.splits - 1;
+        __syncthreads();
+        if (!last) return;
+        v = 0.f;
+        if (mine)
+            for (int i = 0; i < g.splits; ++i) v += __hip_atomic_load(at + i * next, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (mine) {
         if (g.down_bias)
             for (int i = 0; i < g.k; ++i) {
                 const int e = chosen.index[t * g.k + i];
@@ -731,15 +757,16 @@ void launch_products(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
     else if (v.q == 2) up(k_ffn_up<Form, Few, 128, 2, QD, false>);
     else up(k_ffn_up<Form, Few, 256, 1, UD, false>);
     if (v.rs == 2)
-        hipLaunchKernelGGL((k_ffn_down<Form, Few, 2>), dim3((unsigned)((g.dim + 15) / 16)), dim3(kThreads), 0, st, g);
+        hipLaunchKernelGGL((k_ffn_down<Form, Few, 2>), dim3((unsigned)((g.dim + 15) / 16), (unsigned)g.splits), dim3(kThreads), 0, st, g);
     else
-        hipLaunchKernelGGL((k_ffn_down<Form, Few, 1>), dim3((unsigned)(g.dim / 8)), dim3(kThreads), 0, st, g);
+        hipLaunchKernelGGL((k_ffn_down<Form, Few, 1>), dim3((unsigned)(g.dim / 8), (unsigned)g.splits), dim3(kThreads), 0, st, g);
 }
 
 template <int Form>
 void launch_products(FfnArgs g, hipStream_t st) {
     const FfnVariant v = ffn_variant(Line<Form>::kValues, g.T, g.dim, g.hidden, g.E, g.k);
     g.waves = v.waves;
+    g.splits = v.splits;
     if (v.few) launch_products<Form, true>(g, v, st);
     else launch_products<Form, false>(g, v, st);
 }
@@ -747,7 +774,9 @@ void launch_products(FfnArgs g, hipStream_t st) {
 }  // namespace
 
 size_t expert_ffn_workspace_bytes(int T, int dim, int hidden, int E, int k) {
-    return up16((size_t)parts_of(route_of(E, dim), dim) * T * E * 4) + 2 * up16((size_t)T * k * 4) + (size_t)T * k * hidden * 2;
+    const size_t splits = ffn_variant(Line<BSR_WEIGHTS_BF16>::kValues, T, dim, hidden, E, k).splits;   // the most of all forms
+    return up16((size_t)parts_of(route_of(E, dim), dim) * T * E * 4) + 2 * up16((size_t)T * k * 4) + up16((size_t)T * k * hidden * 2) +
+           (splits > 1 ? up16((size_t)dim / 8 * 4) + splits * T * dim * 4 : 0);
 }
 
 int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,
@@ -756,7 +785,7 @@ int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Route r = route_of(E, dim);
     FfnArgs g{x, T, dim, hidden, E, k, renorm, r, parts_of(r, dim), kWaves, router, up, down, up_scales, down_scales, up_bias, down_bias, out,
-              nullptr, nullptr, nullptr, nullptr};
+              nullptr, nullptr, nullptr, nullptr, 1, nullptr, nullptr};
     g.logits = reinterpret_cast<float *>(ws);
     ws += up16((size_t)g.parts * T * E * 4);
     g.index = reinterpret_cast<int32_t *>(ws);
@@ -764,6 +793,9 @@ int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, 
     g.weight = reinterpret_cast<float *>(ws);
     ws += up16((size_t)T * k * 4);
     g.h = reinterpret_cast<uint16_t *>(ws);
+    ws += up16((size_t)T * k * hidden * 2);
+    g.done = reinterpret_cast<uint32_t *>(ws);
+    g.partial = reinterpret_cast<float *>(ws + up16((size_t)dim / 8 * 4));
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (r != kAllInOne) {
         const dim3 grid((unsigned)((E + 7) / 8), (unsigned)g.parts);

@@ -173,12 +173,13 @@ int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, c
 
 // Kernels of the whole layer for few tokens. few: up to 8 tokens share an operand. Of the up product a wave holds `span` of the columns,
 // whole lines of `values` of them, `waves` of the 16 hold all, and a unit is 8 q gate rows with their up rows for each such set; wide:
-// more columns than the 16 waves hold, in several spans. rs: sets of 8 output columns of a work-group of the down product.
+// more columns than the 16 waves hold, in several spans. rs: sets of 8 output columns of a work-group of the down product; splits: work-groups that share such columns, where there are fewer sets than CUs and
+// each wave of the work-groups has a line.
 struct FfnVariant {
     bool few;
     int span, q, waves;
     bool wide;
-    int rs;
+    int rs, splits;
 };
 inline FfnVariant ffn_variant(int values, int64_t T, int64_t dim, int64_t hidden, int64_t E, int64_t k) {
     const int64_t most = std::min(E, T * k);
@@ -186,7 +187,9 @@ inline FfnVariant ffn_variant(int values, int64_t T, int64_t dim, int64_t hidden
     const int64_t lines = (dim + values - 1) / values, each = std::max(1, 128 / values);
     int waves = many ? 4 : 16;   // as few as hold the columns and leave every CU a unit
     while (waves < 16 && (waves * each < lines || most * ((hidden + 256 / waves - 1) / (256 / waves)) < 256)) waves *= 2;
-    return {T <= 8, wide || many ? 128 : 256, many ? 2 : 1, waves, wide, dim >= 16 * 256 ? 2 : 1};
+    const int64_t tiles = (dim + 7) / 8, down_lines = most * ((hidden + values - 1) / values);
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({256 / tiles, down_lines / 16, 16}));
+    return {T <= 8, wide || many ? 128 : 256, many ? 2 : 1, waves, wide, dim >= 16 * 256 ? 2 : 1, (int)splits};
 }
 size_t expert_ffn_workspace_bytes(int T, int dim, int hidden, int E, int k);
 int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,

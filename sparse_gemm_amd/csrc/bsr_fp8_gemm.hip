@@ -143,6 +143,7 @@ __global__ __launch_bounds__(256, 2) void k_fp8_rows(GemmArgs g, int ntiles) {
 // 16384 x 4096 -> 4096: 223 us, 2.47 PFLOP/s; 32768 rows of 8 experts, 4096 -> 11008: 1351 us, 2.19. Copies of the former that skip
 // work, of 227: no loads 190, no LDS reads either 169, all steps' loads from the same lines 215. Fragments of a whole half step ahead,
 // which leave the compiler no registers: 239. Four waves of 128 x 128 each, which read a third less from LDS but wait for it alone: 260.
+// Weights straight from memory into registers, in 128 x 128 tiles (16 rows a load): twice the time of such tiles.
 // ------------------------------------------------------------------------------------------
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));

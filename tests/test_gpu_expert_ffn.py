@@ -144,6 +144,29 @@ def test_values_that_are_not_finite_stay_where_they_are(form):
     assert unused and torch.isnan(got[hit]).all() and torch.equal(got[~hit], clean[~hit])
 
 
+@pytest.mark.parametrize("form", ["bf16", "mx4", "fp8"])
+@pytest.mark.parametrize("T", [3, 12])
+@pytest.mark.parametrize("E", [6, 70, 300])
+def test_experts_out_of_reach(form, T, E):
+    """A logit of -infinity: its expert is not chosen, and a token without any has a result of zeros."""
+    m = Layer(form, T, 96, 64, E, 3, True, True)
+    a = m.args()
+    near = [1, E - 2]
+    a["x"][:, 7] = 1.0
+    a["router"][:, 7] = -math.inf
+    assert not expert_layer.expert_ffn(**a).any()
+    a["router"][near, 7] = 0.5
+    got = expert_layer.expert_ffn(**a).double()
+    pick = (lambda W: W[near]) if form == "bf16" else (lambda W: type(W)(W.codes[near].contiguous(), W.scales[near].contiguous()))
+    want = expert_layer.expert_ffn(a["x"], a["router"][near].contiguous(), pick(a["up"]), pick(a["down"]), 2, True,
+                                   a["up_bias"][near].contiguous(), a["down_bias"][near].contiguous()).double()
+    # sums in another order: h and the result may each round to a neighbour, 2 * 2^-8 of a value
+    assert float((got - want).norm()) <= 4 * 2.0 ** -8 * float(want.norm())
+    far = a["x"].clone()
+    far[0, 7] = -1.0   # the signs of token 0 turn: all but two are +infinity, NaN weights
+    assert torch.equal(expert_layer.expert_ffn(**{**a, "x": far})[1:].double(), got[1:])
+
+
 def test_no_tokens():
     m = Layer("bf16", 1, 64, 32, 4, 2, True, False)
     a = m.args()
