@@ -41,7 +41,8 @@ size_t bsr_expert_ffn_workspace(int32_t T, int32_t dim, int32_t hidden, int32_t 
  *   form      bsr_weight_form, of both weights
  *   up        rows 2 * hidden (gate, then up), columns dim; up_bias bf16 [E][2 * hidden] or NULL
  *   down      rows dim, columns hidden; down_bias bf16 [E][dim] or NULL
- *   dim and hidden: positive multiples of 8 (bf16), 16 (fp8) or 32 (mx4) below 2^20; one expert's weight at most 0xF0000000 bytes
+ *   dim and hidden: positive multiples of 8 (bf16), 16 (fp8) or 32 (mx4), below 2^20 and 2^19; one expert's weight at most 0xF0000000
+ *             bytes
  *   workspace device, 16-byte aligned, at least bsr_expert_ffn_workspace bytes; two calls that may run at the same time
  *             need one each. */
 int32_t bsr_expert_ffn(const bsr_bf16 *x, int32_t T, int32_t dim, int32_t hidden, int32_t E, int32_t k,

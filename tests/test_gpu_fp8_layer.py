@@ -152,3 +152,13 @@ def test_frozen_parts_get_no_gradient():
     a, = torch.autograd.grad(expert_layer.expert_linear_fp8(p, leaves[0], W, b), [leaves[0]], expanded)
     c, = torch.autograd.grad(expert_layer.expert_linear_fp8(p, leaves[0], W, b), [leaves[0]], expanded.contiguous())
     assert torch.equal(a, c)
+
+
+def test_the_example_in_8_bits():
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import expert_ffn
+    got = expert_ffn.main(3, "fp8")
+    # of x, W, h and the second W each value is rounded to E4M3, 2^-4 of it at most, and the activation passes its factors' on twice
+    assert len(got["losses"]) == 3 and got["prompt"] < 6 * 2.0 ** -4 and got["token"] < 6 * 2.0 ** -4
