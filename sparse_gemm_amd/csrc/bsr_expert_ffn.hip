@@ -107,10 +107,12 @@ struct Piece8 {
         code = (uint32_t)r * m.pitch + at;
         scale = Form == BSR_WEIGHTS_MX4 ? ((uint32_t)s * (uint32_t)m.rows + (uint32_t)r) * 8u + chunk : (uint32_t)s;
     }
-    // Of the 8 rows from n0 (a multiple of 8).
+    // Of the 8 rows from n0 (a multiple of 8). Stream: marked as not used again (nt).
+    template <bool Stream = false>
     __device__ __forceinline__ Held load(const Matrix<Form> &m, const Expert<Form> &e, int n0) const {
         Held v;
-        v.codes = __builtin_bit_cast(u32x4, buf_load16(e.codes, in ? code + (uint32_t)n0 * m.pitch : kPast, 0));
+        v.codes = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(e.codes, in ? code + (uint32_t)n0 * m.pitch : kPast, 0,
+                                                                                  Stream ? 2 : 0));
         v.byte = 0;
         if constexpr (Form == BSR_WEIGHTS_MX4)
             v.byte = __builtin_amdgcn_raw_buffer_load_b8(e.scales, in ? scale + (uint32_t)n0 * 8u : kPast, 0, 0);
@@ -411,7 +413,7 @@ __device__ __forceinline__ void route(const FfnArgs &g, Chosen &c, Part &part, f
 // Where fewer waves hold the columns, g.waves of them are a set with its own 8 Q rows of a unit: 16 tokens on 64 4-bit experts,
 // 1024 / 2048: the layer 86 us, without sets 131 (the down product unsplit); 4 tokens on 64 8-bit ones, 1024 / 1024: 37 | 41.
 // ------------------------------------------------------------------------------------------
-template <int Form, bool Few, int Span, int Q, int D, bool Wide>
+template <int Form, bool Few, bool Stream, int Span, int Q, int D, bool Wide>
 __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
     using L = Line<Form>;
     constexpr int LN = Span > L::kValues ? Span / L::kValues : 1, N = Tokens<Few>::kN;   // lines a wave
@@ -473,8 +475,8 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
             const Piece8<Form> piece(m, (z * LN + i) * waves + line);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                to.w[i][q][0] = piece.load(m, w, to.n0 + 8 * (Q * set + q));
-                to.w[i][q][1] = piece.load(m, w, to.n0 + 8 * (Q * set + q) + g.hidden);
+                to.w[i][q][0] = piece.template load<Stream>(m, w, to.n0 + 8 * (Q * set + q));
+                to.w[i][q][1] = piece.template load<Stream>(m, w, to.n0 + 8 * (Q * set + q) + g.hidden);
             }
         }
     };
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(kThreads) void k_ffn_up(FfnArgs g) {
 // Of 9 to 16 tokens an expert has up to 8 in most calls: then they share an operand as up to 8 tokens of a call do (Packed), column c
 // being the expert's c-th token, and its sums go to the tokens' lanes at the expert's end.
 // ------------------------------------------------------------------------------------------
-template <int Form, bool Few, bool Packed, int RS, int D>
+template <int Form, bool Few, bool Packed, bool Stream, int RS, int D>
 __device__ __forceinline__ void down_sums(const FfnArgs &g, const Chosen &chosen, const float *weight, int n0, int split, f32x4 (&sum)[RS]) {
     using L = Line<Form>;
     constexpr bool Shared = Few || Packed;
@@ -606,7 +608,7 @@ __device__ __forceinline__ void down_sums(const FfnArgs &g, const Chosen &chosen
         st.tokens = tokens;
         const Piece8<Form> piece(m, left > 0 ? s : kNoLine);
 #pragma unroll
-        for (int i = 0; i < RS; ++i) st.w[i] = piece.load(m, w, n0 + 8 * i);
+        for (int i = 0; i < RS; ++i) st.w[i] = piece.template load<Stream>(m, w, n0 + 8 * i);
 #pragma unroll
         for (int p = 0; p < L::kP; ++p)
 #pragma unroll
@@ -658,7 +660,7 @@ __device__ __forceinline__ void down_sums(const FfnArgs &g, const Chosen &chosen
     }
 }
 
-template <int Form, bool Few, int RS>
+template <int Form, bool Few, bool Stream, int RS>
 __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
     __shared__ Chosen chosen;
     __shared__ Part part[RS];
@@ -680,7 +682,7 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
     // for its code, fetched cold in every launch: 4 tokens, 4096 / 7168 67 us | 70, 16 tokens on 32 experts, 2048 / 2048 68 | 69.
     constexpr int D = Form == BSR_WEIGHTS_MX4 ? 2 : 3;
     if constexpr (Few) {
-        down_sums<Form, true, false, RS, D>(g, chosen, weight, n0, split, sum);
+        down_sums<Form, true, false, Stream, RS, D>(g, chosen, weight, n0, split, sum);
     } else {
         bool many = false;   // an expert with more than 8 tokens
         for (int a = lane; a < chosen.count; a += 64) {
@@ -689,8 +691,8 @@ __global__ __launch_bounds__(kThreads) void k_ffn_down(FfnArgs g) {
             for (int i = 0; i < kTok / 4; ++i) none += __popc(reinterpret_cast<const uint32_t *>(chosen.slot[a])[i] & 0x80808080u);
             many |= kTok - none > 8;
         }
-        if (__ballot(many)) down_sums<Form, false, false, RS, 2>(g, chosen, weight, n0, split, sum);
-        else down_sums<Form, false, true, RS, D>(g, chosen, weight, n0, split, sum);
+        if (__ballot(many)) down_sums<Form, false, false, Stream, RS, 2>(g, chosen, weight, n0, split, sum);
+        else down_sums<Form, false, true, Stream, RS, D>(g, chosen, weight, n0, split, sum);
     }
 #pragma unroll
     for (int i = 0; i < RS; ++i) part[i][wave][lane] = sum[i];
@@ -743,8 +745,8 @@ Route route_of(int E, int64_t dim) {
 // Pieces of the logits' sums: 8 lines each, half a line a wave.
 int parts_of(Route r, int dim) { return r == kFromLogits ? std::min(kMostParts, (dim + 511) / 512) : 1; }
 
-template <int Form, bool Few>
-void launch_products(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
+template <int Form, bool Few, bool Stream>
+void launch_up(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
     const int rows = 8 * v.q * (kWaves / v.waves);
     const int64_t units = (int64_t)std::min(g.E, g.T * g.k) * ((g.hidden + rows - 1) / rows);
     auto up = [&](auto kernel) {
@@ -753,13 +755,24 @@ void launch_products(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
     // units loaded ahead: what the registers hold beside the tokens' values
     constexpr int UD = Form == BSR_WEIGHTS_BF16 ? 1 : Form == BSR_WEIGHTS_FP8 ? 2 : 3;
     constexpr int QD = Form == BSR_WEIGHTS_BF16 || (Form == BSR_WEIGHTS_MX4 && !Few) ? 1 : 2;
-    if (v.wide) up(k_ffn_up<Form, Few, 128, 1, 1, true>);
-    else if (v.q == 2) up(k_ffn_up<Form, Few, 128, 2, QD, false>);
-    else up(k_ffn_up<Form, Few, 256, 1, UD, false>);
-    if (v.rs == 2)
-        hipLaunchKernelGGL((k_ffn_down<Form, Few, 2>), dim3((unsigned)((g.dim + 15) / 16), (unsigned)g.splits), dim3(kThreads), 0, st, g);
-    else
-        hipLaunchKernelGGL((k_ffn_down<Form, Few, 1>), dim3((unsigned)(g.dim / 8), (unsigned)g.splits), dim3(kThreads), 0, st, g);
+    if (v.wide) up(k_ffn_up<Form, Few, Stream, 128, 1, 1, true>);
+    else if (v.q == 2) up(k_ffn_up<Form, Few, Stream, 128, 2, QD, false>);
+    else up(k_ffn_up<Form, Few, Stream, 256, 1, UD, false>);
+}
+
+template <int Form, bool Few, bool Stream>
+void launch_down(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
+    const dim3 grid((unsigned)((g.dim + 8 * v.rs - 1) / (8 * v.rs)), (unsigned)v.splits);
+    if (v.rs == 2) hipLaunchKernelGGL((k_ffn_down<Form, Few, Stream, 2>), grid, dim3(kThreads), 0, st, g);
+    else hipLaunchKernelGGL((k_ffn_down<Form, Few, Stream, 1>), grid, dim3(kThreads), 0, st, g);
+}
+
+template <int Form, bool Few>
+void launch_products(const FfnArgs &g, const FfnVariant &v, hipStream_t st) {
+    if (v.stream_up) launch_up<Form, Few, true>(g, v, st);
+    else launch_up<Form, Few, false>(g, v, st);
+    if (v.stream_down) launch_down<Form, Few, true>(g, v, st);
+    else launch_down<Form, Few, false>(g, v, st);
 }
 
 template <int Form>

@@ -60,7 +60,8 @@ __device__ __forceinline__ int cswz(int r) {
     return BN == 64 ? (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2) : ((r >> 3) & 1) << 1;
 }
 
-template <Weights W, int MT, int BN, int NS>
+// Stream: see streams().
+template <Weights W, int MT, int BN, int NS, bool Stream>
 __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_expert_few(FewArgs g, int ntiles) {
     using L = FewLayout<W, MT, BN, NS>;
     constexpr bool MX4 = W == kMx4W, FP8 = W == kFp8W, COLS = W == kColsW;
@@ -137,8 +138,11 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
             for (int j = 0; j < L::kALoads; ++j)
                 dma16(rx, to + (uint32_t)(wave + 4 * j) * 1024u, s < alim[j] ? aoff[j] + (uint32_t)s * 512u : kPast, 0);
 #pragma unroll
-            for (int j = 0; j < L::kBLoads; ++j)
-                dma16(rw, to + L::kA + (uint32_t)(wave + 4 * j) * 1024u, s < blim[j] ? boff[j] + (uint32_t)s * bstep : kPast, 0);
+            for (int j = 0; j < L::kBLoads; ++j) {
+                const uint32_t at = to + L::kA + (uint32_t)(wave + 4 * j) * 1024u, from = s < blim[j] ? boff[j] + (uint32_t)s * bstep : kPast;
+                if constexpr (Stream) dma16_stream(rw, at, from);
+                else dma16(rw, at, from, 0);
+            }
             if constexpr (MX4)
                 dma4(rs, to + L::kA + L::kB + (uint32_t)sw * 256u, s < slim ? soff + (uint32_t)s * (uint32_t)g.N * 8u : kPast);
         };
@@ -235,11 +239,11 @@ __global__ __launch_bounds__(256, (FewLayout<W, MT, BN, NS>::kGroups)) void k_ex
     }
 }
 
-template <Weights W, int MT, int BN, int NS>
+template <Weights W, int MT, int BN, int NS, bool Stream = false>
 int32_t launch(const FewArgs &g, void *stream, const char *what) {
     const int64_t ntiles = (g.N + BN - 1) / BN, blocks = max_row_tiles(g.R, g.E, 16 * MT) * ntiles;
     if (const int32_t bad = check_grid(blocks, 256, what)) return bad;
-    hipLaunchKernelGGL((k_expert_few<W, MT, BN, NS>), dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
+    hipLaunchKernelGGL((k_expert_few<W, MT, BN, NS, Stream>), dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
                        g, (int)ntiles);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return fail(BSR_ERR_HIP, std::string(what) + ": " + hipGetErrorString(err));
@@ -277,9 +281,11 @@ int32_t launch_expert_fwd_few_fp8(const ExpertShape &s, int mt, const uint16_t *
                                   const uint8_t *scales, const uint16_t *bias, uint16_t *Y, void *stream) {
     const FewArgs g{X, codes, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
     const char *what = "bsr_expert_fwd_fp8";
-    if (few_cols_fp8(mt, s.R, s.E, s.N) == 32) return launch<kFp8W, 1, 32, 5>(g, stream, what);
-    return mt == 1 ? launch<kFp8W, 1, 64, 3>(g, stream, what)
-                   : mt == 2 ? launch<kFp8W, 2, 64, 4>(g, stream, what) : launch<kFp8W, 4, 64, 3>(g, stream, what);
+    const bool once = stream_fp8(mt, s.R, s.E, s.N, s.K);
+    if (few_cols_fp8(mt, s.R, s.E, s.N) == 32)
+        return once ? launch<kFp8W, 1, 32, 5, true>(g, stream, what) : launch<kFp8W, 1, 32, 5>(g, stream, what);
+    if (mt == 1) return once ? launch<kFp8W, 1, 64, 3, true>(g, stream, what) : launch<kFp8W, 1, 64, 3>(g, stream, what);
+    return mt == 2 ? launch<kFp8W, 2, 64, 4>(g, stream, what) : launch<kFp8W, 4, 64, 3>(g, stream, what);
 }
 
 }  // namespace bsr

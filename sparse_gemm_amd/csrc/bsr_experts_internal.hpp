@@ -121,6 +121,20 @@ inline int few_cols_fp8(int mt, int64_t R, int64_t E, int64_t cols) {
     return tiles <= 192 || (rounds > 1 && halves * 21 < rounds * 40) ? 32 : 64;
 }
 
+// Whether weights that a decode step reads once are read as data that is not used again (nt): so many bytes of the experts that may have
+// rows, rows of whole lines or not. What else a call reads stays in the caches then: 7 tokens in bf16, 4096 / 11008, the whole layer 303 us
+// | 335 without; one token on 128 8-bit experts, k = 8, 4096 / 1536: 40.6 | 42.2; 8-bit product of one row of 8 experts, 4096 -> 14336:
+// 83 | 93. But a smaller layer may find its weights in the memory-side cache (256 MB) when it is called again (one token in bf16, k = 2,
+// 2048 / 1024, four such layers in turn: 16.8 | 15.4), and a line that two rows or two steps share is fetched twice (20 rows of 60 experts,
+// 2064 -> 1008: 49 | 43).
+inline bool streams(int64_t bytes, bool whole_lines) { return whole_lines && bytes >= INT64_C(1) << 27; }
+
+// 8-bit weights, tiles of up to 16 mt rows: where an expert has one of them.
+inline bool stream_fp8(int mt, int64_t R, int64_t E, int64_t N, int64_t K) {
+    const int64_t groups = std::min(E, R);
+    return mt == 1 && R <= 16 * groups && streams(groups * N * K, K % 128 == 0);
+}
+
 // 8 bits on both sides: 256 x 256 tiles with 8 waves, one work-group a CU, or 128 x 128 with 4, two of them. Equal groups again; a last
 // round of 256 x 256 tiles that leaves half of the CUs idle or more is taken in halves, which cost 0.65 of a round. Both sides, us (rows
 // of all experts: 128 x 128 | 256 x 256):
@@ -174,12 +188,13 @@ int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, c
 // Kernels of the whole layer for few tokens. few: up to 8 tokens share an operand. Of the up product a wave holds `span` of the columns,
 // whole lines of `values` of them, `waves` of the 16 hold all, and a unit is 8 q gate rows with their up rows for each such set; wide:
 // more columns than the 16 waves hold, in several spans. rs: sets of 8 output columns of a work-group of the down product; splits: work-groups that share such columns, where there are fewer sets than CUs and
-// each wave of the work-groups has a line.
+// each wave of the work-groups has a line. stream_up, stream_down: see streams().
 struct FfnVariant {
     bool few;
     int span, q, waves;
     bool wide;
     int rs, splits;
+    bool stream_up, stream_down;
 };
 inline FfnVariant ffn_variant(int values, int64_t T, int64_t dim, int64_t hidden, int64_t E, int64_t k) {
     const int64_t most = std::min(E, T * k);
@@ -189,7 +204,8 @@ inline FfnVariant ffn_variant(int values, int64_t T, int64_t dim, int64_t hidden
     while (waves < 16 && (waves * each < lines || most * ((hidden + 256 / waves - 1) / (256 / waves)) < 256)) waves *= 2;
     const int64_t tiles = (dim + 7) / 8, down_lines = most * ((hidden + values - 1) / values);
     const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({256 / tiles, down_lines / 16, 16}));
-    return {T <= 8, wide || many ? 128 : 256, many ? 2 : 1, waves, wide, dim >= 16 * 256 ? 2 : 1, (int)splits};
+    return {T <= 8, wide || many ? 128 : 256, many ? 2 : 1, waves, wide, dim >= 16 * 256 ? 2 : 1, (int)splits,
+            streams(most * 3 * dim * hidden * 128 / values, dim % values == 0), streams(most * 3 * dim * hidden * 128 / values, hidden % values == 0)};
 }
 size_t expert_ffn_workspace_bytes(int T, int dim, int hidden, int E, int k);
 int32_t launch_expert_ffn(const uint16_t *x, int T, int dim, int hidden, int E, int k, bool renorm, const uint16_t *router,

@@ -34,6 +34,11 @@ __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t m0, uint
                  : "memory", "m0");
 }
 
+// dma16 of data that is not used again.
+__device__ __forceinline__ void dma16_stream(__amdgpu_buffer_rsrc_t r, uint32_t m0, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(m0), "v"(voff), "s"(r) : "memory", "m0");
+}
+
 // p[i] for a uniform i by a scalar load: a vector load would share the counter of the direct-to-LDS loads
 // and its wait would wait for those too.
 __device__ __forceinline__ int scalar_load(const int32_t *p, int i) {

@@ -65,7 +65,7 @@ CASES = [(1, 1, 1, 1, 1, True, False), (1, 8, 4, 8, 2, True, True), (3, 9, 7, 4,
          (16, 17, 3, 8, 2, False, True), (7, 33, 13, 64, 8, False, False), (2, 40, 67, 128, 8, True, True), (5, 3, 5, 200, 32, True, False),
          (16, 4, 2, 1024, 32, False, True), (16, 2, 9, 12, 12, True, True), (9, 130, 21, 16, 1, False, False), (4, 19, 300, 4, 2, True, False),
          (8, 12, 1, 256, 32, True, True), (8, 40, 1, 256, 32, False, False), (8, 100, 1, 256, 32, True, False), (16, 40, 3, 256, 24, True, True),
-         (12, 100, 1, 256, 24, False, True)] + [(T, 20, hidden, 200, k, T > 8, False) for T, k in ((8, 32), (12, 20)) for hidden in (1, 2, 4)]
+         (12, 100, 1, 256, 24, False, True), (8, 5, 1, 64, 8, True, True), (16, 5, 1, 64, 4, False, True)] + [(T, 20, hidden, 200, k, T > 8, False) for T, k in ((8, 32), (12, 20)) for hidden in (1, 2, 4)]
 
 
 @pytest.mark.parametrize("T,dim,hidden,E,k,renorm,bias", CASES)
@@ -83,7 +83,12 @@ def test_layer(form, T, dim, hidden, E, k, renorm, bias):
     assert torch.isnan(room[T:]).all()
 
 
-WIDE_CASES = [(1, 2048, 1024, 8, 2), (4, 4096, 1792, 8, 2), (16, 4128, 288, 16, 4), (3, 8224, 96, 4, 2), (11, 4096, 64, 24, 3)]
+WIDE_CASES = [(1, 2048, 1024, 8, 2), (4, 4096, 1792, 8, 2), (16, 4128, 288, 16, 4), (3, 8224, 96, 4, 2), (11, 4096, 64, 24, 3), (2, 4096, 256, 4, 1), (16, 2048, 96, 64, 8), (2, 1536, 640, 8, 4)]
+
+# weights of 128 MB and more, rows of whole lines
+STREAMED = [("bf16", T, *c) for T in (5, 9) for c in ((4096, 2752, 2, 2), (8192, 1408, 2, 2), (2560, 2240, 4, 2), (1536, 1856, 8, 4), (1024, 2752, 8, 4))]
+STREAMED += [(form, 8 if form == "fp8" else 10, 1024, hidden, 8, 4) for form, hidden in (("fp8", 5504), ("mx4", 11008))]
+STREAMED += [(form, 3 if form == "mx4" else 12, 4864, hidden, 2, 2) for form, hidden in (("fp8", 4736), ("mx4", 9728))]
 
 
 @pytest.mark.parametrize("form", ["bf16", "mx4", "fp8"])
@@ -91,6 +96,13 @@ WIDE_CASES = [(1, 2048, 1024, 8, 2), (4, 4096, 1792, 8, 2), (16, 4128, 288, 16, 
 def test_wide_layer(form, T, dim, hidden, E, k):
     say(f"case expert_ffn {form} T={T} dim={dim} hidden={hidden} E={E} k={k}")
     m = Layer(form, T, dim, hidden, E, k, True, False)
+    m.check(expert_layer.expert_ffn(**m.args()))
+
+
+@pytest.mark.parametrize("form,T,dim,hidden,E,k", STREAMED)
+def test_large_layer(form, T, dim, hidden, E, k):
+    say(f"case expert_ffn {form} T={T} dim={dim} hidden={hidden} E={E} k={k}")
+    m = Layer(form, T, dim, hidden, E, k, True, True)
     m.check(expert_layer.expert_ffn(**m.args()))
 
 

@@ -162,3 +162,13 @@ def test_the_example_in_8_bits():
     got = expert_ffn.main(3, "fp8")
     # of x, W, h and the second W each value is rounded to E4M3, 2^-4 of it at most, and the activation passes its factors' on twice
     assert len(got["losses"]) == 3 and got["prompt"] < 6 * 2.0 ** -4 and got["token"] < 6 * 2.0 ** -4
+
+
+def test_an_empty_batch():
+    m = layer(fp8=True, decode_tokens=4)
+    x = torch.zeros(0, 256, dtype=torch.bfloat16, device=dev(), requires_grad=True)
+    got = step(m, x, torch.zeros(0, 256, device=dev()))
+    for a, q in zip(got, [x, *m.parameters()]):
+        assert a.shape == q.shape and not a.any()
+    with torch.no_grad():
+        assert m(x).shape == (0, 256) and m.quantize_("fp8")(x).shape == (0, 256)

@@ -74,6 +74,22 @@ def test_blocks_past_4_gib():
                 near(y[a:b], value[a:b], fp8.dequantize(Fp8Blocks(q.codes[e:e + 1], q.scales[e:e + 1]))[0], eight)
 
 
+STREAMED = [(8, 8, 4096, 4096), (7, 8, 14336, 4096), (64, 5, 2056, 13184)]   # R, E, N, K: weights read as not used again
+
+
+@pytest.mark.parametrize("R,E,N,K", STREAMED)
+def test_few_rows_of_large_weights(R, E, N, K):
+    say(f"case few rows R={R} E={E} N={N} K={K}")
+    p, offsets, token = a_plan(R, E, 2)
+    x = randn(R, K, seed=14)
+    q = fp8.quantize_blocks(randn(E, N, K, seed=15))
+    y = fp8.expert_fwd(p, x, q)
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        near(y[a:b], x[token[a:b]], fp8.dequantize(Fp8Blocks(q.codes[e:e + 1], q.scales[e:e + 1].clone()))[0], False)
+    assert not y[offsets[-1]:].any()
+
+
 @pytest.mark.parametrize("R", [3, 200])
 def test_one_expert_of_the_most_bytes(R):
     N, K = 245760, 16384
