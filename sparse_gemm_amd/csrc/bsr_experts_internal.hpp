@@ -121,8 +121,8 @@ inline int few_cols_fp8(int mt, int64_t R, int64_t E, int64_t cols) {
     return tiles <= 192 || (rounds > 1 && halves * 21 < rounds * 40) ? 32 : 64;
 }
 
-// Whether weights that a decode step reads once are read as data that is not used again (nt): so many bytes of the experts that may have
-// rows, rows of whole lines or not. What else a call reads stays in the caches then: 7 tokens in bf16, 4096 / 11008, the whole layer 303 us
+// Whether weights that a decode step reads once, and matrices to quantise or expand, are read (expanded ones stored) as data that is not
+// used again (nt): so many bytes (of the experts that may have rows), rows of whole lines or not. What else a call reads stays in the caches then: 7 tokens in bf16, 4096 / 11008, the whole layer 303 us
 // | 335 without; one token on 128 8-bit experts, k = 8, 4096 / 1536: 40.6 | 42.2; 8-bit product of one row of 8 experts, 4096 -> 14336:
 // 83 | 93. But a smaller layer may find its weights in the memory-side cache (256 MB) when it is called again (one token in bf16, k = 2,
 // 2048 / 1024, four such layers in turn: 16.8 | 15.4), and a line that two rows or two steps share is fetched twice (20 rows of 60 experts,

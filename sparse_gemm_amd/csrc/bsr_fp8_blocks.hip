@@ -12,35 +12,52 @@ namespace {
 
 using namespace dev;
 
-// 8 elements a thread, 16 threads a group, a wave the 512 columns of a row whose scale bytes lie side by side.
-// Threads past K only write the zero bytes of their groups. 16384 x 4096: 44 us, 4.6 TB/s.
+// 16 bytes; Stream: as data that is not used again (see streams()).
+template <bool Stream>
+__device__ __forceinline__ u32x4 load16(const void *p) {
+    const u32x4 *v = static_cast<const u32x4 *>(p);
+    return Stream ? __builtin_nontemporal_load(v) : *v;
+}
+
+// 8 elements a thread and row, 16 threads a group, a wave the 512 columns of `Rows` rows whose scale bytes lie side by side.
+// Threads past K only write the zero bytes of their groups. 16384 x 4096: 39 us, 5.2 TB/s; with one row a wave 46.
+template <int Rows>
 __global__ __launch_bounds__(256) void k_fp8_rows_quantize(const uint16_t *__restrict__ X, int64_t rows, int K, int chunks,
                                                            uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                            uint16_t *__restrict__ values) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // chunk, row by row
-    if (i >= rows * chunks) return;
-    const int64_t row = i / chunks;
+    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), row = i / chunks * Rows;   // chunk, row by row
+    if (row >= rows) return;
     const int cb = (int)(i % chunks), part = threadIdx.x & 63, col = cb * 512 + part * 8;
-    u32x4 x = {0, 0, 0, 0};
-    if (col < K) x = *reinterpret_cast<const u32x4 *>(X + row * K + col);
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top = fp8_top(top, x[j]);
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
     const bool real = col - (part & 15) * 8 < K;   // a group that exists
-    const int byte = real ? fp8_scale_byte(top) : 0;
-    if ((part & 15) == 0) scales[((int64_t)cb * rows + row) * 4 + (part >> 4)] = (uint8_t)byte;
-    if (col < K) {
-        const float scale = mx4_scale_bits((uint32_t)byte);
-        const uint2 c = make_uint2(fp8_quantize4(x[0], x[1], scale), fp8_quantize4(x[2], x[3], scale));
-        *reinterpret_cast<uint2 *>(codes + row * K + col) = c;
-        if (values) *reinterpret_cast<bf16x8 *>(values + row * K + col) = fp8_expand8(c, scale);
+    u32x4 x[Rows];
+#pragma unroll
+    for (int r = 0; r < Rows; ++r) {
+        x[r] = u32x4{0, 0, 0, 0};
+        if (col < K && row + r < rows) x[r] = *reinterpret_cast<const u32x4 *>(X + (row + r) * K + col);
+    }
+#pragma unroll
+    for (int r = 0; r < Rows; ++r) {
+        if (row + r >= rows) return;
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fp8_top(top, x[r][j]);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+        const int byte = real ? fp8_scale_byte(top) : 0;
+        if ((part & 15) == 0) scales[((int64_t)cb * rows + row + r) * 4 + (part >> 4)] = (uint8_t)byte;
+        if (col < K) {
+            const float scale = mx4_scale_bits((uint32_t)byte);
+            const uint2 c = make_uint2(fp8_quantize4(x[r][0], x[r][1], scale), fp8_quantize4(x[r][2], x[r][3], scale));
+            *reinterpret_cast<uint2 *>(codes + (row + r) * K + col) = c;
+            if (values) *reinterpret_cast<bf16x8 *>(values + (row + r) * K + col) = fp8_expand8(c, scale);
+        }
     }
 }
 
 // One 128 x 128 block a work-group: thread t holds rows 8 (t / 16) + 0 .. 7 of the 8 columns from 8 (t % 16), so that a
-// transposed row's 8 codes come from its own registers. 8 x 4096 x 4096 with transposed codes: 100 to 115 us, 4.7 to 5.4 TB/s (as a copy).
+// transposed row's 8 codes come from its own registers. 8 x 4096 x 4096 with transposed codes: 98 us, 5.5 TB/s; with W left in the caches
+// 112, with codes stored as not used again either 101.
+template <bool Stream>
 __global__ __launch_bounds__(256) void k_fp8_blocks_quantize(const uint16_t *__restrict__ W, int N, int K, int nb, int kb,
                                                              uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                              uint8_t *__restrict__ codes_t, uint8_t *__restrict__ scales_t) {
@@ -54,7 +71,7 @@ __global__ __launch_bounds__(256) void k_fp8_blocks_quantize(const uint16_t *__r
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         x[i] = u32x4{0, 0, 0, 0};
-        if (in) x[i] = *reinterpret_cast<const u32x4 *>(W + at + (int64_t)(r0 + i) * K + c0);
+        if (in) x[i] = load16<Stream>(W + at + (int64_t)(r0 + i) * K + c0);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -93,8 +110,8 @@ __global__ __launch_bounds__(256) void k_fp8_blocks_quantize(const uint16_t *__r
 }
 
 // 8 codes a thread. rowwise: scales of bsr_fp8_dequantize_rows, else of one expert's blocks after the other. 8 x 4096 x 4096: 70 us,
-// 5.8 TB/s.
-template <bool Rowwise>
+// 5.8 TB/s; right behind their quantisation, which leaves the codes in the caches, 58, without Stream 71.
+template <bool Rowwise, bool Stream>
 __global__ __launch_bounds__(256) void k_fp8_dequantize(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                         int64_t rows, int N, int K, uint16_t *__restrict__ values) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / (K / 8);   // K / 8 pieces a row
@@ -107,8 +124,13 @@ __global__ __launch_bounds__(256) void k_fp8_dequantize(const uint8_t *__restric
         const int64_t e = row / N;
         s = (e * ((N + 127) / 128) + ((int)(row % N) >> 7)) * ((K + 127) / 128) + g;
     }
-    const uint2 c = *reinterpret_cast<const uint2 *>(codes + i * 8);
-    *reinterpret_cast<bf16x8 *>(values + i * 8) = fp8_expand8(c, mx4_scale_bits(scales[s]));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 *from = reinterpret_cast<const u32x2 *>(codes + i * 8);
+    u32x4 *to = reinterpret_cast<u32x4 *>(values + i * 8);
+    const u32x2 c = Stream ? __builtin_nontemporal_load(from) : *from;
+    const u32x4 v = __builtin_bit_cast(u32x4, fp8_expand8(make_uint2(c[0], c[1]), mx4_scale_bits(scales[s])));
+    if constexpr (Stream) __builtin_nontemporal_store(v, to);
+    else *to = v;
 }
 
 int32_t launched(const char *what) {
@@ -122,8 +144,8 @@ int32_t dequantize(const char *what, const uint8_t *codes, const uint8_t *scales
                    void *stream) {
     const int64_t blocks = (rows * (K / 8) + 255) / 256;
     if (const int32_t bad = check_grid(blocks, 256, what)) return bad;
-    hipLaunchKernelGGL((k_fp8_dequantize<Rowwise>), dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
-                       codes, scales, rows, N, K, values);
+    hipLaunchKernelGGL((streams(rows * K * 2, true) ? k_fp8_dequantize<Rowwise, true> : k_fp8_dequantize<Rowwise, false>),
+                       dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), codes, scales, rows, N, K, values);
     return launched(what);
 }
 
@@ -133,10 +155,12 @@ int32_t launch_fp8_quantize_rows(const uint16_t *X, int64_t rows, int K, uint8_t
                                  void *stream) {
     const char *what = "bsr_fp8_quantize_rows";
     const int chunks = (K + 511) / 512;
-    const int64_t blocks = (rows * chunks + 3) / 4;
+    // four rows a wave where that leaves every CU eight waves
+    const int each = rows * chunks >= 32 * kCUs ? 4 : 1;
+    const int64_t blocks = ((rows + each - 1) / each * chunks + 3) / 4;
     if (const int32_t bad = check_grid(blocks, 256, what)) return bad;
-    hipLaunchKernelGGL(k_fp8_rows_quantize, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), X, rows,
-                       K, chunks, codes, scales, values);
+    hipLaunchKernelGGL((each == 4 ? k_fp8_rows_quantize<4> : k_fp8_rows_quantize<1>), dim3((unsigned)blocks), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), X, rows, K, chunks, codes, scales, values);
     return launched(what);
 }
 
@@ -146,8 +170,9 @@ int32_t launch_fp8_quantize_blocks(const uint16_t *W, int E, int N, int K, uint8
     const int nb = (N + 127) / 128, kb = (K + 127) / 128;
     const int64_t blocks = (int64_t)E * nb * kb;
     if (const int32_t bad = check_grid(blocks, 256, what)) return bad;
-    hipLaunchKernelGGL(k_fp8_blocks_quantize, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), W, N, K,
-                       nb, kb, codes, scales, codes_t, scales_t);
+    hipLaunchKernelGGL((streams((int64_t)E * N * K * 2, K % 64 == 0) ? k_fp8_blocks_quantize<true> : k_fp8_blocks_quantize<false>),
+                       dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), W, N, K, nb, kb, codes, scales, codes_t,
+                       scales_t);
     return launched(what);
 }
 

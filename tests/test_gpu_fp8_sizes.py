@@ -47,6 +47,34 @@ def test_rows_past_4_gib():
         assert torch.equal(back[part], fp8.dequantize(one))
 
 
+def test_large_blocks_and_their_expansion():
+    """Matrices that are read, and expansions that are stored, as data not used again."""
+    E, N, K = 3, 4112, 8192
+    say(f"case large blocks E={E} N={N} K={K}")
+    W = randn(E, N, K, seed=16)
+    q, t = fp8.quantize_blocks(W, transposed=True)
+    back, turned = fp8.dequantize(q), fp8.dequantize(t)
+    for e in range(E):
+        one, two = fp8.quantize_blocks(W[e, :2048].contiguous(), transposed=True)
+        assert torch.equal(q.codes[e, :2048], one.codes) and torch.equal(q.scales[e, :16], one.scales)
+        assert torch.equal(t.codes[e, :, :2048], two.codes) and torch.equal(t.scales[e, :, :16], two.scales)
+        one = fp8.quantize_blocks(W[e, 2048:].contiguous())
+        assert torch.equal(q.codes[e, 2048:], one.codes) and torch.equal(q.scales[e, 16:], one.scales)
+        assert torch.equal(back[e, 2048:], fp8.dequantize(one)) and torch.equal(turned[e], back[e].t())
+
+
+def test_many_rows_in_every_rest():
+    """Four rows a wave, and what is left of them."""
+    for rows in (8192, 8193, 8194, 8195):
+        for K in (512, 1040):
+            say(f"case rows={rows} K={K}")
+            X = randn(rows, K, seed=17)
+            q, values = fp8.quantize_rows(X, want_values=True)
+            for a, b in ((0, 5), (4000, 4011), (rows - 9, rows)):
+                one, v = fp8.quantize_rows(X[a:b].contiguous(), want_values=True)
+                assert torch.equal(q.codes[a:b], one.codes) and torch.equal(q.scales[:, a:b], one.scales) and torch.equal(values[a:b], v)
+
+
 def test_blocks_past_4_gib():
     E, N, K = 33, 8192, 16400
     say(f"case blocks E={E} N={N} K={K}")
