@@ -113,7 +113,7 @@ inline int few_cols_mx4(int mt, int64_t R, int64_t E, int64_t cols) {
 // 8-bit weights, the same, while tiles of 64 leave a quarter of the CUs without one: one row, one expert, 4096 -> 4096: 7.6 us
 // against 10.5; where they do not, 64 rows of it (256 tiles) 12.4 against 11.1, one row of 60 experts, 2064 -> 1008: 31 against 29. And
 // 32 where that fills a last round of work-groups, two a CU, that tiles of 64 leave half empty: one row of 8 experts, 4096 -> 14336
-// (7 rounds or 3.5): 94 against 102; 4 tokens, k = 2 of 8, there: 77 against 84.
+// (7 rounds or 3.5): 94 against 102; 4 tokens, k = 2 of 8, there: 77 against 84 (both before streams()).
 inline int few_cols_fp8(int mt, int64_t R, int64_t E, int64_t cols) {
     if (mt != 1) return 64;
     const int64_t groups = std::min(E, R), tiles = groups * ((R / groups + 15) / 16) * ((cols + 63) / 64);   // of equal groups
@@ -121,18 +121,19 @@ inline int few_cols_fp8(int mt, int64_t R, int64_t E, int64_t cols) {
     return tiles <= 192 || (rounds > 1 && halves * 21 < rounds * 40) ? 32 : 64;
 }
 
-// Whether weights that a decode step reads once, and matrices to quantise or expand, are read (expanded ones stored) as data that is not
-// used again (nt): so many bytes (of the experts that may have rows), rows of whole lines or not. What else a call reads stays in the caches then: 7 tokens in bf16, 4096 / 11008, the whole layer 303 us
-// | 335 without; one token on 128 8-bit experts, k = 8, 4096 / 1536: 40.6 | 42.2; 8-bit product of one row of 8 experts, 4096 -> 14336:
-// 83 | 93. But a smaller layer may find its weights in the memory-side cache (256 MB) when it is called again (one token in bf16, k = 2,
-// 2048 / 1024, four such layers in turn: 16.8 | 15.4), and a line that two rows or two steps share is fetched twice (20 rows of 60 experts,
-// 2064 -> 1008: 49 | 43).
-inline bool streams(int64_t bytes, bool whole_lines) { return whole_lines && bytes >= INT64_C(1) << 27; }
+// Whether weights that are read once, and matrices to quantise or expand, are read (expanded ones stored) as data that is not used again
+// (nt): where they (of the experts that may have rows) are as large as the memory-side cache, and rows are whole lines. What else a call
+// reads stays in the caches then: 7 tokens in bf16, 4096 / 11008, the whole layer 303 us | 335 without, 16 tokens there with 3584 instead
+// of 11008 136 | 145; 8-bit product of one row of 8 experts, 4096 -> 14336, 83 | 93, of 256 rows in 8 bits 104 | 110. But a smaller
+// matrix may be found in that cache by the next call (256 rows of 8 experts, 4096 -> 4096, again and again 36 | 28; one token in bf16,
+// k = 2, 2048 / 1024, four such layers in turn: 16.8 | 15.4), and a line that two rows or two steps share is fetched twice (20 rows of 60
+// experts, 2064 -> 1008: 49 | 43).
+inline bool streams(int64_t bytes, bool whole_lines) { return whole_lines && bytes >= INT64_C(1) << 28; }
 
-// 8-bit weights, tiles of up to 16 mt rows: where an expert has one of them.
+// 8-bit weights: where an expert has one row tile of up to 16 mt rows, mostly.
 inline bool stream_fp8(int mt, int64_t R, int64_t E, int64_t N, int64_t K) {
     const int64_t groups = std::min(E, R);
-    return mt == 1 && R <= 16 * groups && streams(groups * N * K, K % 128 == 0);
+    return R <= 16 * mt * groups && streams(groups * N * K, K % 128 == 0);
 }
 
 // 8 bits on both sides: 256 x 256 tiles with 8 waves, one work-group a CU, or 128 x 128 with 4, two of them. Equal groups again; a last

@@ -159,8 +159,8 @@ struct Fp8Layout {
     static constexpr int kLds = kStages > kOut ? kStages : kOut;
 };
 
-// The tile of t's rows and the columns from col.
-template <int BM, int BN, int WM, int WN>
+// The tile of t's rows and the columns from col. Stream: the weights' loads, see streams().
+template <int BM, int BN, int WM, int WN, bool Stream>
 __device__ __forceinline__ void fp8_tile(const GemmArgs &g, const Rows &t, int col, unsigned char *smem) {
     constexpr int NW = WM * WN, RT = BM / WM / 16, CT = BN / WN / 16;
     static_assert(CT == 4 && RT % 2 == 0 && BM % 64 == 0, "the schedule below");
@@ -208,8 +208,10 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs &g, const Rows &t, int c
             }
         };
         auto issue_b = [&](int s, int j) __attribute__((always_inline)) {
-            dma16(rb, base + L::kB + (uint32_t)(s & 1) * (BN * 128) + (uint32_t)(wave + NW * j) * 1024u,
-                  s < left ? boff + (uint32_t)j * bstep + (uint32_t)s * 128u : kPast, 0);
+            const uint32_t to = base + L::kB + (uint32_t)(s & 1) * (BN * 128) + (uint32_t)(wave + NW * j) * 1024u;
+            const uint32_t from = s < left ? boff + (uint32_t)j * bstep + (uint32_t)s * 128u : kPast;
+            if constexpr (Stream) dma16_stream(rb, to, from);
+            else dma16(rb, to, from, 0);
         };
         // rows' scale bytes of 4 steps: a word a lane, 64 rows a load (waves past BM / 64 load the same words again)
         const int arows = g.gather ? g.T : g.R, sw = wave % U, ar = sw * 64 + lane;
@@ -310,7 +312,7 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs &g, const Rows &t, int c
                                g.out + (int64_t)t.at * g.Nout + col, g.Nout, t.n, g.Nout - col, smem);
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, bool Stream>
 __global__ __launch_bounds__(WM *WN * 64, 1) void k_fp8_fp8(GemmArgs g, int ntiles) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[Fp8Layout<BM, BN>::kLds];
     const RowTiles<BM> tiles(g.offsets, g.E, g.R);
@@ -322,9 +324,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void k_fp8_fp8(GemmArgs g, int ntil
     const int col = o.col * BN + (piece.half > 0 ? BN / 2 : 0);
     if (t.n <= 0 || col >= g.Nout) return;
     if constexpr (BN == 256) {
-        if (piece.half >= 0) return fp8_tile<BM, BN / 2, 4, 2>(g, t, col, smem);
+        if (piece.half >= 0) return fp8_tile<BM, BN / 2, 4, 2, Stream>(g, t, col, smem);
     }
-    fp8_tile<BM, BN, WM, WN>(g, t, col, smem);
+    fp8_tile<BM, BN, WM, WN, Stream>(g, t, col, smem);
 }
 
 int32_t launched(const char *what) {
@@ -356,9 +358,9 @@ int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, c
     const int64_t blocks = max_row_tiles(s.R, s.E, bm) * ntiles + (w ? kPieces : 0);
     if (const int32_t bad = check_grid(blocks, 512, what)) return bad;
     if (w)
-        hipLaunchKernelGGL((k_fp8_fp8<256, 256, 2, 4>), dim3((unsigned)blocks), dim3(512), 0, st, g, (int)ntiles);
+        hipLaunchKernelGGL((k_fp8_fp8<256, 256, 2, 4, false>), dim3((unsigned)blocks), dim3(512), 0, st, g, (int)ntiles);
     else
-        hipLaunchKernelGGL((k_fp8_fp8<128, 128, 2, 2>), dim3((unsigned)blocks), dim3(256), 0, st, g, (int)ntiles);
+        hipLaunchKernelGGL((stream_fp8(4, s.R, s.E, s.N, s.K) ? k_fp8_fp8<128, 128, 2, 2, true> : k_fp8_fp8<128, 128, 2, 2, false>), dim3((unsigned)blocks), dim3(256), 0, st, g, (int)ntiles);
     return launched(what);
 }
 

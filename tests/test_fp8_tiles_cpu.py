@@ -14,7 +14,7 @@ from test_gpu_fp8_sizes import STREAMED as LARGE_PRODUCTS
 
 # rows and columns of a tile, weights streamed
 BF16_ACT = {(16, 32, 0), (16, 32, 1), (16, 64, 0), (16, 64, 1), (32, 64, 0), (64, 64, 0), (128, 128, 0)}
-FP8_ACT = {(128, 128), (256, 256)}
+FP8_ACT = {(128, 128, 0), (128, 128, 1), (256, 256, 0)}
 VALUES = {"bf16": 64, "mx4": 256, "fp8": 128}   # of a line
 # few, span, q, waves, wide, rs
 LAYER = {(few, *v) for few in (0, 1) for v in ((128, 1, 16, 1, 2), (256, 1, 16, 0, 1), (256, 1, 16, 0, 2), (128, 2, 4, 0, 1),
@@ -41,10 +41,10 @@ int main() {
     while (std::scanf(" %c %ld %ld %ld %ld %ld %ld", &kind, &a, &b, &c, &d, &e, &f) == 7) {
         if (kind == 'b') {
             const int id = bsr::best_tile(bsr::kFwdFp8Tiles, a, b, c, d);
-            std::printf("%d %d %d\n", id <= 4 ? 16 * id : id, id <= 4 ? bsr::few_cols_fp8(id, a, b, c) : id, bsr::stream_fp8(id, a, b, c, d));
+            std::printf("%d %d %d\n", id <= 4 ? 16 * id : id, id <= 4 ? bsr::few_cols_fp8(id, a, b, c) : id, id == 1 && bsr::stream_fp8(1, a, b, c, d));
         } else if (kind == 'f') {
             const int bm = bsr::wide_fp8(a, b, c, d) ? 256 : 128;
-            std::printf("%d %d\n", bm, bm);
+            std::printf("%d %d %d\n", bm, bm, bm == 128 && bsr::stream_fp8(4, a, b, c, d));
         } else {
             const bsr::FfnVariant v = bsr::ffn_variant(a, b, c, d, e, f);
             std::printf("%d %d %d %d %d %d %d %d %d\n", v.few, v.span, v.q, v.waves, v.wide, v.rs, v.splits > 1, v.stream_up, v.stream_down);
@@ -91,7 +91,7 @@ def test_every_variant_is_taken(variants):
 def test_every_variant_runs_on_the_gpu(variants):
     products = [(T * k, E, N, K) for _, T, k, E, N, K in FP8_PRODUCTS]
     assert variants("b", products + LARGE_PRODUCTS) == BF16_ACT
-    assert variants("f", products) == FP8_ACT
+    assert variants("f", products + LARGE_PRODUCTS) == FP8_ACT
     for form, step in STEP.items():
         layers = [(T, dim * step, hidden * step, E, k) for T, dim, hidden, E, k, _, _ in CASES]
         got = variants("l", [(VALUES[form], *c) for c in layers + WIDE_CASES])

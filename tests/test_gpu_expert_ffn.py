@@ -85,10 +85,10 @@ def test_layer(form, T, dim, hidden, E, k, renorm, bias):
 
 WIDE_CASES = [(1, 2048, 1024, 8, 2), (4, 4096, 1792, 8, 2), (16, 4128, 288, 16, 4), (3, 8224, 96, 4, 2), (11, 4096, 64, 24, 3), (2, 4096, 256, 4, 1), (16, 2048, 96, 64, 8), (2, 1536, 640, 8, 4)]
 
-# weights of 128 MB and more, rows of whole lines
-STREAMED = [("bf16", T, *c) for T in (5, 9) for c in ((4096, 2752, 2, 2), (8192, 1408, 2, 2), (2560, 2240, 4, 2), (1536, 1856, 8, 4), (1024, 2752, 8, 4))]
-STREAMED += [(form, 8 if form == "fp8" else 10, 1024, hidden, 8, 4) for form, hidden in (("fp8", 5504), ("mx4", 11008))]
-STREAMED += [(form, 3 if form == "mx4" else 12, 4864, hidden, 2, 2) for form, hidden in (("fp8", 4736), ("mx4", 9728))]
+# weights of 256 MB and more, rows of whole lines
+STREAMED = [("bf16", T, *c) for T in (5, 9) for c in ((4096, 5504, 2, 2), (8192, 2752, 2, 2), (2560, 4416, 4, 2), (1536, 3648, 8, 4), (1024, 5504, 8, 4))]
+STREAMED += [(form, 8 if form == "fp8" else 10, 1024, hidden, 8, 4) for form, hidden in (("fp8", 11008), ("mx4", 22016))]
+STREAMED += [(form, 3 if form == "mx4" else 12, 4864, hidden, 2, 2) for form, hidden in (("fp8", 9344), ("mx4", 18688))]
 
 
 @pytest.mark.parametrize("form", ["bf16", "mx4", "fp8"])

@@ -49,7 +49,7 @@ def test_rows_past_4_gib():
 
 def test_large_blocks_and_their_expansion():
     """Matrices that are read, and expansions that are stored, as data not used again."""
-    E, N, K = 3, 4112, 8192
+    E, N, K = 4, 4112, 8192
     say(f"case large blocks E={E} N={N} K={K}")
     W = randn(E, N, K, seed=16)
     q, t = fp8.quantize_blocks(W, transposed=True)
@@ -102,7 +102,7 @@ def test_blocks_past_4_gib():
                 near(y[a:b], value[a:b], fp8.dequantize(Fp8Blocks(q.codes[e:e + 1], q.scales[e:e + 1]))[0], eight)
 
 
-STREAMED = [(8, 8, 4096, 4096), (7, 8, 14336, 4096), (64, 5, 2056, 13184)]   # R, E, N, K: weights read as not used again
+STREAMED = [(8, 8, 8192, 4096), (7, 8, 14336, 4096), (64, 5, 4104, 13184)]   # R, E, N, K: weights read as not used again
 
 
 @pytest.mark.parametrize("R,E,N,K", STREAMED)
@@ -111,11 +111,14 @@ def test_few_rows_of_large_weights(R, E, N, K):
     p, offsets, token = a_plan(R, E, 2)
     x = randn(R, K, seed=14)
     q = fp8.quantize_blocks(randn(E, N, K, seed=15))
-    y = fp8.expert_fwd(p, x, q)
-    for e in range(E):
-        a, b = offsets[e], offsets[e + 1]
-        near(y[a:b], x[token[a:b]], fp8.dequantize(Fp8Blocks(q.codes[e:e + 1], q.scales[e:e + 1].clone()))[0], False)
-    assert not y[offsets[-1]:].any()
+    for act in (x, fp8.quantize_rows(x)):
+        eight = isinstance(act, Fp8Rows)
+        value = fp8.dequantize(act) if eight else x
+        y = fp8.expert_fwd(p, act, q)
+        for e in range(E):
+            a, b = offsets[e], offsets[e + 1]
+            near(y[a:b], value[token[a:b]], fp8.dequantize(Fp8Blocks(q.codes[e:e + 1], q.scales[e:e + 1].clone()))[0], eight)
+        assert not y[offsets[-1]:].any()
 
 
 @pytest.mark.parametrize("R", [3, 200])
