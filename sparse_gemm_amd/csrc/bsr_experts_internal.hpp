@@ -190,6 +190,8 @@ int32_t launch_expert_fwd_fp8_fp8(const ExpertShape &s, const uint8_t *xcodes, c
 // whole lines of `values` of them, `waves` of the 16 hold all, and a unit is 8 q gate rows with their up rows for each such set; wide:
 // more columns than the 16 waves hold, in several spans. rs: sets of 8 output columns of a work-group of the down product; splits: work-groups that share such columns, where there are fewer sets than CUs and
 // each wave of the work-groups has a line. stream_up, stream_down: see streams().
+// Both sides of the rules, us: few | not: 4 tokens on 4-bit weights, 4096 / 7168 66 | 71, 4 tokens on 32 8-bit experts, 1024 / 2048 36 | 40. q = 2
+// and sets | 256 columns a wave: the same 36 | 44, 16 tokens on 32 4-bit experts, 2048 / 2048 68 | 90. rs 2 | 1: 4096 / 7168 66 | 74.
 struct FfnVariant {
     bool few;
     int span, q, waves;
