@@ -232,9 +232,10 @@ __device__ __forceinline__ f32x4 logit_sums(const FfnArgs &g, int e0, int first,
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             const int s = s0 + b * step;
-            w[b] = Piece8<BSR_WEIGHTS_BF16>(m, s < to ? s : kNoLine).load(m, router, e0);   // (of lines from `to` on: none)
+            // lines from `to` on: zeros on both sides (an infinite value of x times a zero would be NaN)
+            w[b] = Piece8<BSR_WEIGHTS_BF16>(m, s < to ? s : kNoLine).load(m, router, e0);
 #pragma unroll
-            for (int i = 0; i < Tokens<Few>::kN; ++i) v[b][i] = load_tokens<BSR_WEIGHTS_BF16, Few>(x, row, g.dim, s, 0, i);
+            for (int i = 0; i < Tokens<Few>::kN; ++i) v[b][i] = load_tokens<BSR_WEIGHTS_BF16, Few>(x, s < to ? row : kPast, g.dim, s, 0, i);
         }
 #pragma unroll
         for (int b = 0; b < B; ++b) acc.add(expand<BSR_WEIGHTS_BF16>(w[b], 0), v[b]);
