@@ -4,6 +4,7 @@ from __future__ import annotations
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 
 class _Gradient(torch.autograd.Function):
@@ -35,3 +36,13 @@ def first_order(backward):
         return tuple(_Gradient.apply(r, *sources) if isinstance(r, torch.Tensor) else r for r in results)
 
     return wrapped
+
+
+def no_tangents(what: str, *tensors) -> None:
+    """For a call of the library outside an autograd function: raises where one of the tensors carries a forward-mode derivative, as
+    such a function without a jvp does. requires_grad does not show it, and the library would drop it without a word."""
+    if getattr(forward_ad, "_current_level", 0) < 0:   # no dual level is open (private to torch: asked for each tensor where it is missing)
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{what} has no forward-mode derivative")

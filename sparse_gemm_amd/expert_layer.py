@@ -11,7 +11,7 @@ from torch import nn
 from torch.nn import functional as F
 
 from . import experts, few_tokens, fp8, mx4
-from .autograd import first_order
+from .autograd import first_order, no_tangents
 from .experts import ExpertPlan
 
 
@@ -115,10 +115,11 @@ def expert_linear_fp8(plan: ExpertPlan, x: torch.Tensor, W: torch.Tensor, bias: 
 def expert_ffn(x: torch.Tensor, router: torch.Tensor, up, down, k: int, renormalize: bool = True,
                up_bias: Optional[torch.Tensor] = None, down_bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """A whole layer of experts for up to 16 tokens x [T, dim] in one call, few_tokens.expert_ffn: weights in bf16, Mx4 or
-    Fp8Blocks, forward only (raises where a gradient is wanted). Against the single calls it keeps the router's logits and each
+    Fp8Blocks, forward only (raises where a gradient is wanted, in reverse or forward mode). Against the single calls it keeps the router's logits and each
     expert's result in 32 bits, and rounds silu(gate) * up to bf16 once."""
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, router, up, down, up_bias, down_bias)):
         raise RuntimeError("expert_ffn has no backward pass")
+    no_tangents("expert_ffn", x, router, up, down, up_bias, down_bias)
     return few_tokens.expert_ffn(_whole(x), router, up, down, k, renormalize, up_bias, down_bias)
 
 
@@ -231,6 +232,7 @@ class ExpertFFN(nn.Module):
             gate, up = linear(plan, x, self.up, self.up_bias).chunk(2, dim=1)
             y = linear(plan, F.silu(gate) * up, self.down, self.down_bias, gather=False)
             return combine(plan, y, weight).reshape(*lead, self.dim)
+        no_tangents("a quantised ExpertFFN", self.up_bias, self.down_bias)   # (those of x and the router are refused by route)
         held, (quantize, expert_fwd) = self._held(), {"mx4": (mx4.quantize, mx4.expert_fwd),
                                                       "fp8": (fp8.quantize_rows, fp8.expert_fwd)}[self.form]
         form = quantize if x.shape[0] > self.prompt_tokens else (lambda t: t)
