@@ -221,8 +221,8 @@ class ExpertFFN(nn.Module):
             raise RuntimeError("a quantised ExpertFFN has no backward pass")
         lead = x.shape[:-1]
         x = _whole(x.reshape(-1, self.dim).to(torch.bfloat16))
-        if 0 < x.shape[0] <= self.decode_tokens and not (torch.is_grad_enabled() and (
-                x.requires_grad or any(p.requires_grad for p in self.parameters()))):
+        if 0 < x.shape[0] <= self.decode_tokens and not (torch.is_grad_enabled() and any(   # (the tensors in use, parameters or not)
+                t is not None and t.requires_grad for t in (x, self.router, self.up, self.down, self.up_bias, self.down_bias))):
             held = (self.up, self.down) if not self.quantized else self._held()
             return expert_ffn(x, self.router, *held, self.k, self.renormalize, self.up_bias, self.down_bias).reshape(*lead, self.dim)
         index, weight = route(F.linear(x, self.router), self.k, self.renormalize)
