@@ -20,7 +20,8 @@ class _Gradient(torch.autograd.Function):
 
 
 def first_order(backward):
-    """For a Function's backward that calls the library: under create_graph=True its results refuse to be differentiated.
+    """For a Function's backward that calls the library: under create_graph=True its results refuse to be differentiated, by the
+    incoming gradients, by what the forward pass saved and by ctx.sources, where it has set them (inputs that it need not save).
     The calls carry no graph, so a second derivative would lose their terms without a word wherever another path has one.
     (torch's once_differentiable looks at the incoming gradients alone, and lets those pass that need no gradient.)"""
 
@@ -30,7 +31,7 @@ def first_order(backward):
             return backward(ctx, *grads)
         with torch.no_grad():
             results = backward(ctx, *grads)
-        sources = [t for t in (*grads, *ctx.saved_tensors) if isinstance(t, torch.Tensor) and t.requires_grad]
+        sources = [t for t in (*grads, *ctx.saved_tensors, *getattr(ctx, "sources", ())) if isinstance(t, torch.Tensor) and t.requires_grad]
         if not sources:
             return results
         return tuple(_Gradient.apply(r, *sources) if isinstance(r, torch.Tensor) else r for r in results)

@@ -77,18 +77,19 @@ class _ExpertLinearFp8Fn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, bias, plan, gather, want_dx):
         ctx.plan, ctx.gather, ctx.has_bias = plan, gather, bias is not None
+        ctx.sources = (W,)   # not saved: backward takes its codes, so it may change in place
         if want_dx:
             Wq, Wt = fp8.quantize_blocks(W, transposed=True)
-            ctx.save_for_backward(x, W, Wt.codes, Wt.scales)
+            ctx.save_for_backward(x, Wt.codes, Wt.scales)
         else:
             Wq = fp8.quantize_blocks(W)
-            ctx.save_for_backward(x, W)
+            ctx.save_for_backward(x)
         return fp8.expert_fwd(plan, fp8.quantize_rows(x), Wq, bias, gather)
 
     @staticmethod
     @first_order
     def backward(ctx, dY):
-        x, _, *Wt = ctx.saved_tensors
+        x, *Wt = ctx.saved_tensors
         plan = ctx.plan
         dY = _whole(dY.to(torch.bfloat16))
         dX = dW = db = None
