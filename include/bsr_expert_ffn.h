@@ -30,7 +30,8 @@ extern "C" {
 enum bsr_weight_form {
     BSR_WEIGHTS_BF16 = 0,   /* [E][rows][columns] bf16; scales NULL */
     BSR_WEIGHTS_MX4 = 1,    /* bsr_mx4.h: codes [E][rows][columns/2], scales [E][ceil(columns/256)][rows][8] */
-    BSR_WEIGHTS_FP8 = 2     /* bsr_fp8_blocks.h: codes [E][rows][columns], scales [E][ceil(rows/128)][ceil(columns/128)] */
+    BSR_WEIGHTS_FP8 = 2     /* bsr_fp8_blocks.h: codes [E][rows][columns], scales [E][ceil(rows/128)][ceil(columns/128)],
+                               which may start at any byte */
 };
 
 /* Bytes of device workspace that bsr_expert_ffn needs (0 for sizes that it refuses). */

@@ -18,7 +18,8 @@
  *           codes [rows][K]; scales [ceil(K/512)][rows][4], the bytes of a row's 512 columns side by side (those of groups
  *           at or past K are written 0 and never used).
  *   blocks  weights [E][N][K]: a group is 128 rows by 128 columns of one matrix, cut at its ends.
- *           codes [E][N][K]; scales [E][ceil(N/128)][ceil(K/128)].
+ *           codes [E][N][K]; scales [E][ceil(N/128)][ceil(K/128)]. Where they are read the scales may start at any byte, so that a slice
+ *           of the experts serves as it is.
  */
 #ifndef BSR_FP8_BLOCKS_H
 #define BSR_FP8_BLOCKS_H

@@ -310,7 +310,7 @@ int32_t bsr_fp8_dequantize_blocks(const uint8_t *codes, const uint8_t *scales, i
                                   bsr_bf16 *values, void *stream) {
     BSR_TRY_BEGIN
     BSR_CHECK(check_fp8_blocks(E, N, K, false));
-    BSR_CHECK(check_ptrs({{codes, "codes", false, 16}, {scales, "scales", false, 16}, {values, "values", false, 16}}));
+    BSR_CHECK(check_ptrs({{codes, "codes", false, 16}, {scales, "scales", false, 1}, {values, "values", false, 16}}));
     return launch_fp8_dequantize_blocks(codes, scales, E, N, K, values, stream);
     BSR_TRY_END
 }
@@ -322,7 +322,7 @@ int32_t bsr_expert_fwd_fp8(const bsr_bf16 *X, int64_t T, int64_t R, int32_t E, i
     BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 16, 8, false));
     const bool none = R == 0;
     BSR_CHECK(check_ptrs({{X, "X", none || (row_token && T == 0), 16}, {offsets, "offsets", none, 16},
-                          {row_token, "row_token", true, 16}, {codes, "codes", none, 16}, {scales, "scales", none, 16},
+                          {row_token, "row_token", true, 16}, {codes, "codes", none, 16}, {scales, "scales", none, 1},
                           {bias, "bias", true, 16}, {Y, "Y", none, 16}}));
     if (none) return BSR_OK;
     return launch_expert_fwd_fp8({(int)T, (int)R, E, N, K, offsets, row_token}, X, codes, scales, bias, Y, stream);
@@ -337,7 +337,7 @@ int32_t bsr_expert_fwd_fp8_fp8(const uint8_t *xcodes, const uint8_t *xscales, in
     BSR_CHECK(check_product(T, R, E, N, K, row_token != nullptr, 8, 8, false));
     const bool none = R == 0, nox = none || (row_token && T == 0);
     BSR_CHECK(check_ptrs({{xcodes, "xcodes", nox, 16}, {xscales, "xscales", nox, 16}, {offsets, "offsets", none, 16},
-                          {row_token, "row_token", true, 16}, {codes, "codes", none, 16}, {scales, "scales", none, 16},
+                          {row_token, "row_token", true, 16}, {codes, "codes", none, 16}, {scales, "scales", none, 1},
                           {bias, "bias", true, 16}, {Y, "Y", none, 16}}));
     if (none) return BSR_OK;
     return launch_expert_fwd_fp8_fp8({(int)T, (int)R, E, N, K, offsets, row_token}, xcodes, xscales, codes, scales, bias, Y,
@@ -377,10 +377,11 @@ int32_t bsr_expert_ffn(const bsr_bf16 *x, int32_t T, int32_t dim, int32_t hidden
     if ((uint64_t)2 * hidden * dim * bits / 8 > kMaxOperandBytes)
         return fail(BSR_ERR_INVALID_ARG, "one expert's weight has more than 0xF0000000 bytes");
     const bool none = T == 0, bare = form == BSR_WEIGHTS_BF16;
+    const unsigned at = form == BSR_WEIGHTS_FP8 ? 1 : 16;   // of scales
     const size_t need = expert_ffn_workspace_bytes(T, dim, hidden, E, k);
     BSR_CHECK(check_ptrs({{x, "x", none, 16}, {router, "router", none, 16}, {up, "up", none, 16},
-                          {up_scales, "up_scales", none || bare, 16}, {down, "down", none, 16},
-                          {down_scales, "down_scales", none || bare, 16}, {up_bias, "up_bias", true, 16},
+                          {up_scales, "up_scales", none || bare, at}, {down, "down", none, 16},
+                          {down_scales, "down_scales", none || bare, at}, {up_bias, "up_bias", true, 16},
                           {down_bias, "down_bias", true, 16}, {out, "out", none, 16}, {workspace, "workspace", need == 0, 16}}));
     if (ws_bytes < need)
         return fail(BSR_ERR_WORKSPACE_TOO_SMALL,
