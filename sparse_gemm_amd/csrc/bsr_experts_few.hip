@@ -282,7 +282,7 @@ int32_t launch_expert_fwd_few_fp8(const ExpertShape &s, int mt, const uint16_t *
     const FewArgs g{X, codes, scales, bias, Y, s.offsets, s.row_token, s.T, s.R, s.E, s.N, s.K};
     const char *what = "bsr_expert_fwd_fp8";
     const bool once = mt == 1 && stream_fp8(1, s.R, s.E, s.N, s.K);
-    if (few_cols_fp8(mt, s.R, s.E, s.N) == 32)
+    if (few_cols_fp8(mt, s.R, s.E, s.N, s.K) == 32)
         return once ? launch<kFp8W, 1, 32, 5, true>(g, stream, what) : launch<kFp8W, 1, 32, 5>(g, stream, what);
     if (mt == 1) return once ? launch<kFp8W, 1, 64, 3, true>(g, stream, what) : launch<kFp8W, 1, 64, 3>(g, stream, what);
     return mt == 2 ? launch<kFp8W, 2, 64, 4>(g, stream, what) : launch<kFp8W, 4, 64, 3>(g, stream, what);
