@@ -178,7 +178,7 @@ class ExpertPlan:
         self._offsets = o = empty_strided((max(E, 0) + 1,), (1,), _I32)
         self._token = t = empty_strided((R,), (1,), _I32)
         self._row = s = new2(T, k, _I32)
-        E, need, ws = min(E, MOST), 0, None
+        E, need, ws = max(min(E, MOST), -1), 0, None
         if R > PLAN_SLOTS:
             need = C.bsr_expert_plan_workspace(T, k, E)
             ws = empty_strided((need,), (1,), torch.uint8)

@@ -6,7 +6,7 @@ from typing import Optional, Union
 import torch
 
 from . import _lib
-from .experts import C, current_device, elsewhere, empty_strided, narrow, new2, pointer, raw_stream, sizes
+from .experts import C, MOST, current_device, elsewhere, empty_strided, narrow, new2, pointer, raw_stream, sizes
 from .fp8 import GROUP, Fp8Blocks
 from .mx4 import Mx4, chunks
 
@@ -56,7 +56,7 @@ def expert_ffn(x: torch.Tensor, router: torch.Tensor, up: Weight, down: Weight, 
         op = out.data_ptr()
     else:
         op = pointer(out, "out", (T, dim), _BF16, d)
-    k = min(k, (1 << 31) - 1)
+    k = max(min(k, MOST), -1)   # ctypes would pass the low 32 bits
     need = C.bsr_expert_ffn_workspace(T, dim, hidden, E, k)
     ws = empty_strided((need,), (1,), _U8)
     status = C.bsr_expert_ffn(xp, T, dim, hidden, E, k, renormalize, rp, form, wp, wsp, vp, vsp, bp, cp, op, ws.data_ptr(), need,
