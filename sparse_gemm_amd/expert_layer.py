@@ -77,24 +77,27 @@ class _ExpertLinearFp8Fn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, bias, plan, gather, want_dx):
         ctx.plan, ctx.gather, ctx.has_bias = plan, gather, bias is not None
-        ctx.sources = (W,)   # not saved: backward takes its codes, so it may change in place
+        # backward takes W's codes, W itself is only what they came from: a parameter is not saved, so that it may change in place; a
+        # weight computed for this call is, so that it is released with the rest
+        ctx.sources = (W,) if W.requires_grad and W.is_leaf else ()
+        saved = [x, W] if W.requires_grad and not W.is_leaf else [x]
         if want_dx:
             Wq, Wt = fp8.quantize_blocks(W, transposed=True)
-            ctx.save_for_backward(x, Wt.codes, Wt.scales)
+            saved += [Wt.codes, Wt.scales]
         else:
             Wq = fp8.quantize_blocks(W)
-            ctx.save_for_backward(x)
+        ctx.save_for_backward(*saved)
         return fp8.expert_fwd(plan, fp8.quantize_rows(x), Wq, bias, gather)
 
     @staticmethod
     @first_order
     def backward(ctx, dY):
-        x, *Wt = ctx.saved_tensors
+        x, *rest = ctx.saved_tensors
         plan = ctx.plan
         dY = _whole(dY.to(torch.bfloat16))
         dX = dW = db = None
         if ctx.needs_input_grad[0]:
-            dX = fp8.expert_fwd(plan, fp8.quantize_rows(dY), fp8.Fp8Blocks(*Wt), gather=False)
+            dX = fp8.expert_fwd(plan, fp8.quantize_rows(dY), fp8.Fp8Blocks(*rest[-2:]), gather=False)
             if ctx.gather:
                 dX = experts.combine_fwd(plan, dX)
         if ctx.needs_input_grad[1] or (ctx.has_bias and ctx.needs_input_grad[2]):
