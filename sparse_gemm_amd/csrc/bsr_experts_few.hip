@@ -8,8 +8,8 @@
 // columns of the output (16 x 16 x 32 products, fp32 sums) and add their sums through LDS at the end, in a fixed
 // order: with the contraction split inside the work-group, BN can be small, and a narrow layer still fills the card.
 // Weights not in the caches, bytes of the experts that have rows: 8 of 8, 4096 -> 14336, one row each: in bf16 146 us, 6.4 TB/s,
-// in 8 bits 83 us, 5.7 TB/s, in 4 bits 51 us, 4.9 TB/s; 4 tokens, k = 2 of 8, there (5.5 experts on average) in 4 bits 45 us, 4.4 TB/s, in 8 bits
-// 69 us, 4.7. 64 of 64, 4096 -> 1536, in bf16: 128 us, 6.3 TB/s. Nothing is read twice (219 MB counted for 7 experts' 218): the tiles
+// in 8 bits 83 us, 5.7 TB/s, in 4 bits 51 us, 4.9 TB/s; 4 tokens, k = 2 of 8, there: in 4 bits (5.5 experts on average) 45 us, 4.4 TB/s, in 8 bits
+// (7 experts) 74 us, 5.5. 64 of 64, 4096 -> 1536, in bf16: 128 us, 6.3 TB/s. Nothing is read twice (219 MB counted for 7 experts' 218): the tiles
 // of codes have 16 steps each in a few rounds of work-groups, whose starts and ends weigh. One token, k = 2 of 8, 2048 -> 1024 in bf16: 6 us, eight dependent steps.
 //   bf16: lane (r = l % 16, g = l / 16) takes the columns 64 w + 32 i + 8 g + 0 .. 7 of wave w's product i
 //   4-bit: the columns 64 w + 16 g + 8 i + 0 .. 7, so that its 16 codes are 8 neighbouring bytes of one group
@@ -40,7 +40,7 @@ struct FewArgs {
 };
 
 // Weights of a tile: bf16 with the contraction contiguous (forward), bf16 with the output columns contiguous
-// input gradient), 4-bit or 8-bit codes with the contraction contiguous.
+// (input gradient), 4-bit or 8-bit codes with the contraction contiguous.
 enum Weights { kRowsW, kColsW, kMx4W, kFp8W };
 
 template <Weights W, int MT, int BN, int NS>

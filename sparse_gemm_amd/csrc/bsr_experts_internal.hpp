@@ -112,13 +112,12 @@ inline int few_cols_mx4(int mt, int64_t R, int64_t E, int64_t cols) {
 }
 // 8-bit weights, the same, while tiles of 64 leave a quarter of the CUs without one: one row, one expert, 4096 -> 4096: 7.5 us
 // against 9.2; where they do not, 64 rows of it (256 tiles) 12.4 against 11.1, one row of 60 experts, 2064 -> 1008: 32 against 30.5. And
-// 32 for more than one round of tiles of 64, two a CU, of rows whose pitch C is a whole number of 4096 bytes: the rows of a tile then
-// start in the same memory channels, and twice as many of them wait for each other. One row of each expert, us, 32 | 64:
+// 32 for more than one round of tiles of 64, two a CU, of rows whose pitch C is a whole number of 4096 bytes, so that all rows of a
+// tile start at the same place of such a piece (pitches beside it, 3840 and 4608, show no such difference). One row of each expert, us, 32 | 64:
 //   8 experts, 4096 ->   4096 (512 tiles): 32.2 | 33.8   5120: 39.1 | 42.3   8192: 54 | 72   9728: 58 | 63   14336: 81 | 88   18432: 101 | 109
 //   8 experts, 8192 ->   4096: 53 | 65   5120: 56 | 61   8192: 101 | 137   14336: 139 | 139        64 experts, 4096 -> 512: 37 | 31   1024: 51 | 57
 //   8 experts, 2048 ->   4096: 18.8 | 15.0   5120: 22.8 | 20.6   8192: 33 | 30   14336: 53 | 48    64 experts, 2048 -> 1024: 35 | 29
 //   8 experts, 12288 -> 5120: 81 | 88   9728: 154 | 156                                           1 expert, 4096 -> 32768: 34 | 31   65536: 59 | 60
-//   8 experts, 2048 ->  4096: 18.8 | 15.0   5120: 22.8 | 20.6   8192: 33 | 30   14336: 53 | 48     64 experts, 2048 -> 1024: 35 | 29
 // And 32 where a long contraction's tiles of 64 leave half of a last round empty that tiles of 32 fill: 8 experts, 14336 -> 5120 (640
 // tiles) 87 | 95, 8192 (1024, no such round) 137 | 138; 6144 -> 5120 47 | 50; but 4608 -> 9728 (1216) 62 | 59, 3584 -> 5120 32.8 | 32.3.
 // (C that is not given: a long contraction of no such pitch.)

@@ -27,8 +27,9 @@ struct GemmArgs {
 // bf16 activations: one 128 x 128 tile a work-group of 4 waves, steps of 64 columns. The codes are staged as they are (64 bytes a row
 // and step) and turned into bf16 fragments in registers: half-wave h of a row takes the columns 32 h .. 32 h + 31, two 16-byte reads a
 // step, 8 codes a product. The scale of a step is one byte for the whole tile, whose columns are those of one block. Three stages a
-// side, loads two steps ahead; two work-groups a CU. 2048 rows, 8 experts, 4096 -> 14336: 248 us, 970 TFLOP/s; 512 rows there 133 us,
-// 3.5 TB/s of weights: each code is expanded by the two waves that share its column.
+// side, loads two steps ahead; two work-groups a CU. 8 experts, 4096 -> 14336, equal groups: 512 rows 153 us (3.1 TB/s of weights), 2048 rows
+// 264 us (910 TFLOP/s; ragged groups 303), 16384 rows 1872 us (1030 TFLOP/s), where the same product on bf16 weights with its 256 x 256 tiles takes 230 and
+// 1405: each code is expanded by the two waves that share its column, and both sides are read twice as often.
 // ------------------------------------------------------------------------------------------
 constexpr int kA = 128 * 128, kB = 128 * 64, kStage = kA + kB;
 

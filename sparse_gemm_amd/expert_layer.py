@@ -111,7 +111,9 @@ def expert_linear_fp8(plan: ExpertPlan, x: torch.Tensor, W: torch.Tensor, bias: 
     """expert_linear with its products in 8 bits, for training on bf16 weights: x is quantised by row and W by block (fp8.quantize_rows,
     fp8.quantize_blocks; N and K multiples of 16) in every call, and so is the incoming gradient for the input gradient
     q(dY) . q(W). The weight and bias gradients are expert_linear's, on x and dY in bf16: they contract over the rows, along which
-    neither has scales. The rounding to codes counts as the identity in the gradients."""
+    neither has scales. The rounding to codes counts as the identity in the gradients. A gathered x's gradient is rounded to bf16 for
+    each of a token's k rows before they are added, as expert_linear's is. The matrix cores drop what lies below 2^-13 of the largest of
+    eight neighbouring products (include/bsr_fp8_blocks.h)."""
     x = _whole(x)
     return _ExpertLinearFp8Fn.apply(x, W, bias, plan, gather, torch.is_grad_enabled() and x.requires_grad)
 
@@ -119,8 +121,8 @@ def expert_linear_fp8(plan: ExpertPlan, x: torch.Tensor, W: torch.Tensor, bias: 
 def expert_ffn(x: torch.Tensor, router: torch.Tensor, up, down, k: int, renormalize: bool = True,
                up_bias: Optional[torch.Tensor] = None, down_bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """A whole layer of experts for up to 16 tokens x [T, dim] in one call, few_tokens.expert_ffn: weights in bf16, Mx4 or
-    Fp8Blocks, forward only (raises where a gradient is wanted, in reverse or forward mode). Against the single calls it keeps the router's logits and each
-    expert's result in 32 bits, and rounds silu(gate) * up to bf16 once."""
+    Fp8Blocks, forward only (raises where a gradient is wanted, in reverse or forward mode). Against the single calls it keeps the
+    router's logits and each expert's result in 32 bits, and rounds silu(gate) * up to bf16 once."""
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, router, up, down, up_bias, down_bias)):
         raise RuntimeError("expert_ffn has no backward pass")
     no_tangents("expert_ffn", x, router, up, down, up_bias, down_bias)
@@ -158,7 +160,8 @@ class ExpertFFN(nn.Module):
     46, 256 tokens 114 against 50). quantize_("fp8") does the same in 8 bits (there 16 tokens 90 against 110 us, 64 tokens 124
     against 110, 256 tokens 135 against 116).
     fp8: the products of the experts in 8 bits while the layer trains on its bf16 weights (expert_linear_fp8; dim and hidden
-    multiples of 16).
+    multiples of 16). Every call quantises the weights of all experts, also one without gradients and of one token (100 us for 8 x 4096
+    x 4096); between training steps few tokens can take decode_tokens instead, and longer evaluations a copy under quantize_("fp8").
     decode_tokens: batches of up to so many tokens (16 at most) whose gradient nobody wants take expert_ffn, in any form of the weights."""
 
     fp8, decode_tokens = False, 0   # of layers stored before these existed
