@@ -162,7 +162,9 @@ class ExpertFFN(nn.Module):
     fp8: the products of the experts in 8 bits while the layer trains on its bf16 weights (expert_linear_fp8; dim and hidden
     multiples of 16). Every call quantises the weights of all experts, also one without gradients and of one token (100 us for 8 x 4096
     x 4096); between training steps few tokens can take decode_tokens instead, and longer evaluations a copy under quantize_("fp8").
-    decode_tokens: batches of up to so many tokens (16 at most) whose gradient nobody wants take expert_ffn, in any form of the weights."""
+    decode_tokens: batches of up to so many tokens (16 at most) whose gradient nobody wants take expert_ffn, in any form of the weights.
+    A reentrant checkpoint hides in its first pass that it wants one: such a batch then takes expert_ffn there and the single calls
+    when it is recomputed, whose roundings differ."""
 
     fp8, decode_tokens = False, 0   # of layers stored before these existed
 
