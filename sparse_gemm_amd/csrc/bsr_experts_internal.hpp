@@ -121,7 +121,7 @@ inline int few_cols_mx4(int mt, int64_t R, int64_t E, int64_t cols) {
 // And 32 where a long contraction's tiles of 64 leave half of a last round empty that tiles of 32 fill: 8 experts, 14336 -> 5120 (640
 // tiles) 87 | 95, 8192 (1024, no such round) 137 | 138; 6144 -> 5120 47 | 50; but 4608 -> 9728 (1216) 62 | 59, 3584 -> 5120 32.8 | 32.3.
 // Where it is off: one whole round (512 tiles) of such pitches, where 64 stay, may be slower by up to a fifth or faster by as much, and one
-// expert of 65536 columns, 8192 long, takes 15% more. (C that is not given: a long contraction of no such pitch.)
+// expert of 65536 columns, 8192 long, takes 18% more. (C that is not given: a long contraction of no such pitch.)
 inline int few_cols_fp8(int mt, int64_t R, int64_t E, int64_t cols, int64_t C = (1 << 20) - 1) {
     if (mt != 1) return 64;
     const int64_t groups = std::min(E, R), tiles = groups * ((R / groups + 15) / 16) * ((cols + 63) / 64);   // of equal groups
